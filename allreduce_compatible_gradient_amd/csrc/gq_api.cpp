@@ -20,6 +20,7 @@
 
 #include "gq.h"
 #include "gq_internal.h"
+#include "gq_lm.h"
 #include "gq_lq.h"
 
 #define GQ_EXPORT extern "C" __attribute__((visibility("default")))
@@ -915,4 +916,272 @@ GQ_EXPORT gq_status gq_lq_step_workers(gq_ctx *c, const float *const *G, float *
   hipError_t e = gq::lq_step_workers(c->lq, a, s);
   if (e == hipErrorOutOfMemory) return fail(c, GQ_ENOMEM, "LQ scratch allocation failed");
   return e == hipSuccess ? GQ_OK : hip_fail(c, e, "lq_step_workers launch");
+}
+
+// ================================================================ language-model operators
+namespace {
+
+// A matrix of rows x cols with row stride ld.
+gq_status check_matrix(gq_ctx *c, int64_t rows, int64_t cols, int64_t ld, int64_t max_rows,
+                       int64_t max_cols, const char *what) {
+  if (rows < 0 || rows > max_rows)
+    return fail(c, GQ_EINVAL, "%s: rows = %lld outside [0, %lld]", what, (long long)rows, (long long)max_rows);
+  if (cols < 1 || cols > max_cols)
+    return fail(c, GQ_EINVAL, "%s: row length %lld outside [1, %lld]", what, (long long)cols, (long long)max_cols);
+  if (ld < cols || ld > (int64_t)1 << 40)
+    return fail(c, GQ_EINVAL, "%s: row stride %lld is below the row length %lld or above 2^40", what,
+                (long long)ld, (long long)cols);
+  return GQ_OK;
+}
+
+gq_status check_flag(gq_ctx *c, int32_t v, const char *what) {
+  return v == 0 || v == 1 ? GQ_OK : fail(c, GQ_EINVAL, "%s = %d, must be 0 or 1", what, v);
+}
+
+gq_status check_temperature(gq_ctx *c, float t) {
+  if (!(t >= 1e-4f && t <= 1e4f)) return fail(c, GQ_EINVAL, "temperature = %g outside [1e-4, 1e4]", (double)t);
+  return GQ_OK;
+}
+
+gq_status check_distill(gq_ctx *c, const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                        int64_t ld, const int32_t *ids, const float *lps, int32_t top, float t,
+                        int32_t tail, const float *weight) {
+  TRY(check_dtype(c, dtype, "dtype"));
+  TRY(check_matrix(c, rows, vocab, ld, gq::kVocabRows, gq::kVocabMax, "logits"));
+  if (top < 1 || top > gq::kVocabTop) return fail(c, GQ_EINVAL, "top = %d outside [1, %d]", top, gq::kVocabTop);
+  TRY(check_temperature(c, t));
+  TRY(check_flag(c, tail, "tail"));
+  TRY(check_ptr(c, logits, "logits", rows == 0));
+  TRY(check_ptr(c, ids, "top_ids", rows == 0));
+  TRY(check_ptr(c, lps, "top_logprobs", rows == 0));
+  TRY(check_ptr(c, weight, "row_weight", true));
+  return GQ_OK;
+}
+
+gq::DistillArgs distill_args(const void *logits, int64_t rows, int64_t vocab, int64_t ld,
+                             const int32_t *ids, const float *lps, int32_t top, float t,
+                             int32_t tail, const float *weight) {
+  gq::DistillArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.logits = logits;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.ld = ld;
+  a.top_ids = ids;
+  a.top_logprobs = lps;
+  a.top = top;
+  a.temperature = t;
+  a.inv_t = 1.0f / t;
+  a.tail = tail;
+  a.weight = weight;
+  return a;
+}
+
+// Buffers a call writes must not be the ones it reads at other places.
+gq_status check_dlogits(gq_ctx *c, const void *logits, int64_t ld, const void *dlogits, int64_t ldd,
+                        int64_t vocab, int64_t rows) {
+  TRY(check_ptr(c, dlogits, "dlogits", rows == 0));
+  if (ldd < vocab || ldd > (int64_t)1 << 40)
+    return fail(c, GQ_EINVAL, "dlogits: row stride %lld is below the row length %lld or above 2^40",
+                (long long)ldd, (long long)vocab);
+  if (dlogits && dlogits == logits && ldd != ld)
+    return fail(c, GQ_EINVAL, "dlogits is logits with another row stride");
+  return GQ_OK;
+}
+
+}  // namespace
+
+GQ_EXPORT int64_t gq_mx_pitch(int64_t cols) { return cols < 1 ? 0 : gq::mx_pitch(cols); }
+
+GQ_EXPORT gq_status gq_mx_quantize(gq_ctx *c, const void *x, int32_t dtype, int64_t rows,
+                                   int64_t cols, int64_t ld, int32_t rounding, uint64_t seed,
+                                   uint32_t worker, uint32_t index_base, uint8_t *codes,
+                                   uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
+                                   void *stream) {
+  if (!c) return GQ_EINVAL;
+  TRY(check_dtype(c, dtype, "dtype"));
+  TRY(check_matrix(c, rows, cols, ld, gq::kMxMaxDim, gq::kMxMaxDim, "x"));
+  if (rounding != GQ_MX_NEAREST && rounding != GQ_MX_STOCHASTIC)
+    return fail(c, GQ_EINVAL, "rounding = %d", rounding);
+  if (rounding == GQ_MX_STOCHASTIC) TRY(check_counter(c, rows * cols, index_base));
+  if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
+    return fail(c, GQ_EINVAL, "codes without scales, or scales without codes");
+  if (rows > 0 && !codes && !codes_t) return fail(c, GQ_EINVAL, "neither codes nor codes_t is given");
+  TRY(check_ptr(c, x, "x", rows == 0));
+  TRY(check_ptr(c, codes, "codes", true));
+  TRY(check_ptr(c, scales, "scales", true));
+  TRY(check_ptr(c, codes_t, "codes_t", true));
+  TRY(check_ptr(c, scales_t, "scales_t", true));
+  if (rows == 0) return GQ_OK;
+  gq::MxQuantArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.codes = codes;
+  a.scales = scales;
+  a.codes_t = codes_t;
+  a.scales_t = scales_t;
+  a.stochastic = rounding == GQ_MX_STOCHASTIC;
+  if (a.stochastic) a.key_mix = key_mix(worker_key(seed, worker));
+  a.index_base = index_base;
+  const hipError_t e = gq::launch_mx_quantize(a, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "mx_quantize launch");
+}
+
+GQ_EXPORT gq_status gq_mx_dequantize(gq_ctx *c, const uint8_t *codes, const uint8_t *scales,
+                                     int64_t rows, int64_t cols, int32_t out_dtype, void *out,
+                                     int64_t ld, void *stream) {
+  if (!c) return GQ_EINVAL;
+  TRY(check_dtype(c, out_dtype, "out_dtype"));
+  TRY(check_matrix(c, rows, cols, ld, gq::kMxMaxDim, gq::kMxMaxDim, "out"));
+  TRY(check_ptr(c, codes, "codes", rows == 0));
+  TRY(check_ptr(c, scales, "scales", rows == 0));
+  TRY(check_ptr(c, out, "out", rows == 0));
+  if (rows == 0) return GQ_OK;
+  const gq::MxDequantArgs a = {codes, scales, rows, cols, ld, out};
+  const hipError_t e = gq::launch_mx_dequantize(a, out_dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "mx_dequantize launch");
+}
+
+GQ_EXPORT gq_status gq_mx_matmul(gq_ctx *c, const void *a, int32_t a_dtype,
+                                 const uint8_t *a_scales, int64_t lda, const uint8_t *b,
+                                 const uint8_t *b_scales, int64_t M, int64_t N, int64_t K,
+                                 const float *bias_or_null, int32_t accumulate, int32_t out_dtype,
+                                 void *out, int64_t ldo, void *stream) {
+  if (!c) return GQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool packed = a_dtype == GQ_MX;
+  if (!packed) TRY(check_dtype(c, a_dtype, "a_dtype"));
+  TRY(check_dtype(c, out_dtype, "out_dtype"));
+  TRY(check_flag(c, accumulate, "accumulate"));
+  TRY(check_matrix(c, M, K, packed ? K : lda, gq::kMxMaxDim, gq::kMxMaxDim, "a"));
+  TRY(check_matrix(c, M, N, ldo, gq::kMxMaxDim, gq::kMxMaxDim, "out"));
+  if (M > 0 && packed != (a_scales != nullptr))
+    return fail(c, GQ_EINVAL, packed ? "a_scales is NULL" : "a_scales is given for rows that are not packed");
+  TRY(check_ptr(c, a, "a", M == 0));
+  TRY(check_ptr(c, a_scales, "a_scales", true));
+  TRY(check_ptr(c, b, "b"));
+  TRY(check_ptr(c, b_scales, "b_scales"));
+  TRY(check_ptr(c, bias_or_null, "bias", true));
+  TRY(check_ptr(c, out, "out", M == 0));
+  if (M == 0) return GQ_OK;
+  gq::MxMatmulArgs m;
+  std::memset(&m, 0, sizeof m);
+  m.a = a;
+  m.a_scales = a_scales;
+  m.b = b;
+  m.b_scales = b_scales;
+  m.bias = bias_or_null;
+  m.out = out;
+  m.M = M;
+  m.N = N;
+  m.K = K;
+  m.lda = lda;
+  m.ldo = ldo;
+  m.a_dtype = a_dtype;
+  m.out_dtype = out_dtype;
+  m.accumulate = accumulate;
+  // scratch: A's packed rows (unless the product packs them itself), then partial products
+  const bool pack = !packed && !gq::mx_matmul_packs_rows(M);
+  const size_t blocks = pack ? (size_t)M * (size_t)gq::mx_pitch(K) : 0;
+  const size_t rows_bytes = align256(blocks * 16) + align256(blocks);
+  const size_t partial = gq::mx_matmul_scratch(M, N, K);
+  if (rows_bytes + partial > 0) TRY(ensure_scratch(c, rows_bytes + partial, s));
+  char *scratch = static_cast<char *>(c->scratch);
+  if (partial) m.partial = reinterpret_cast<float *>(scratch + rows_bytes);
+  hipError_t e = hipSuccess;
+  if (pack) {
+    gq::MxQuantArgs q;
+    std::memset(&q, 0, sizeof q);
+    q.x = a;
+    q.rows = M;
+    q.cols = K;
+    q.ld = lda;
+    q.codes = reinterpret_cast<uint8_t *>(scratch);
+    q.scales = reinterpret_cast<uint8_t *>(scratch + align256(blocks * 16));
+    e = gq::launch_mx_quantize(q, a_dtype, s);
+    if (e != hipSuccess) return hip_fail(c, e, "mx_matmul launch");
+    m.a = q.codes;
+    m.a_scales = q.scales;
+    m.a_dtype = GQ_MX;
+  }
+  e = gq::launch_mx_matmul(m, s);
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "mx_matmul launch");
+}
+
+GQ_EXPORT gq_status gq_token_logprobs(gq_ctx *c, const void *logits, int32_t dtype, int64_t rows,
+                                      int64_t vocab, int64_t ld, const int64_t *tokens,
+                                      float temperature, int32_t top, float *logprob,
+                                      float *entropy, int32_t *top_ids, float *top_logprobs,
+                                      void *stream) {
+  if (!c) return GQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  TRY(check_dtype(c, dtype, "dtype"));
+  TRY(check_matrix(c, rows, vocab, ld, gq::kVocabRows, gq::kVocabMax, "logits"));
+  TRY(check_temperature(c, temperature));
+  if (top < 0 || top > gq::kVocabTop || top > vocab)
+    return fail(c, GQ_EINVAL, "top = %d outside [0, min(%d, vocab)]", top, gq::kVocabTop);
+  TRY(check_ptr(c, logits, "logits", rows == 0));
+  TRY(check_ptr(c, tokens, "tokens", rows == 0));
+  TRY(check_ptr(c, logprob, "logprob", rows == 0));
+  TRY(check_ptr(c, entropy, "entropy", rows == 0));
+  TRY(check_ptr(c, top_ids, "top_ids", rows == 0 || top == 0));
+  TRY(check_ptr(c, top_logprobs, "top_logprobs", rows == 0 || top == 0));
+  if (rows == 0) return GQ_OK;
+  const size_t bytes = gq::logprobs_scratch(rows, vocab, top);
+  if (bytes) TRY(ensure_scratch(c, bytes, s));
+  const gq::LogprobArgs a = {logits, rows,    vocab,   ld,      tokens,       1.0f / temperature,
+                             top,    logprob, entropy, top_ids, top_logprobs, c->scratch};
+  const hipError_t e = gq::launch_token_logprobs(a, dtype, s);
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "token_logprobs launch");
+}
+
+GQ_EXPORT gq_status gq_distill_loss(gq_ctx *c, const void *logits, int32_t dtype, int64_t rows,
+                                    int64_t vocab, int64_t ld, const int32_t *top_ids,
+                                    const float *top_logprobs, int32_t top, float temperature,
+                                    int32_t tail, const float *row_weight_or_null, float *loss,
+                                    float *stats_or_null, void *dlogits_or_null, int64_t ldd,
+                                    void *stream) {
+  if (!c) return GQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  TRY(check_distill(c, logits, dtype, rows, vocab, ld, top_ids, top_logprobs, top, temperature,
+                    tail, row_weight_or_null));
+  TRY(check_ptr(c, loss, "loss", rows == 0));
+  TRY(check_ptr(c, stats_or_null, "stats", true));
+  if (dlogits_or_null) TRY(check_dlogits(c, logits, ld, dlogits_or_null, ldd, vocab, rows));
+  if (rows == 0) return GQ_OK;
+  gq::DistillArgs a = distill_args(logits, rows, vocab, ld, top_ids, top_logprobs, top, temperature,
+                                   tail, row_weight_or_null);
+  a.loss = loss;
+  a.stats = stats_or_null;
+  a.grad = dlogits_or_null;
+  a.ldg = ldd;
+  const size_t bytes = gq::distill_scratch(rows, vocab);
+  if (bytes) TRY(ensure_scratch(c, bytes, s));
+  a.scratch = c->scratch;
+  const hipError_t e = gq::launch_distill_loss(a, dtype, s);
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "distill_loss launch");
+}
+
+GQ_EXPORT gq_status gq_distill_grad(gq_ctx *c, const void *logits, int32_t dtype, int64_t rows,
+                                    int64_t vocab, int64_t ld, const int32_t *top_ids,
+                                    const float *top_logprobs, int32_t top, float temperature,
+                                    int32_t tail, const float *stats,
+                                    const float *row_weight_or_null, void *dlogits, int64_t ldd,
+                                    void *stream) {
+  if (!c) return GQ_EINVAL;
+  TRY(check_distill(c, logits, dtype, rows, vocab, ld, top_ids, top_logprobs, top, temperature,
+                    tail, row_weight_or_null));
+  TRY(check_ptr(c, stats, "stats", rows == 0));
+  TRY(check_dlogits(c, logits, ld, dlogits, ldd, vocab, rows));
+  if (rows == 0) return GQ_OK;
+  gq::DistillArgs a = distill_args(logits, rows, vocab, ld, top_ids, top_logprobs, top, temperature,
+                                   tail, row_weight_or_null);
+  a.stats = const_cast<float *>(stats);
+  a.grad = dlogits;
+  a.ldg = ldd;
+  const hipError_t e = gq::launch_distill_grad(a, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "distill_grad launch");
 }

@@ -1,0 +1,534 @@
+// gq_mx.hip -- gfx950 kernels of microscaled 4-bit floating point: quantisation of a matrix by
+// rows and by columns, decoding, and the product of two packed matrices.
+//
+// Format.  A row is cut into blocks of 32; a block holds one scale 2^(s - 127), s a byte, and 32
+// codes of 4 bits: a sign and a magnitude of {0, 0.5, 1, 1.5, 2, 3, 4, 6}.  Element 2t of a row
+// sits in the low nibble of its byte t.  s = 255 makes the whole block NaN.  Rows are padded to
+// a multiple of 256 elements (8 blocks) with zero codes and zero scales, which stand for zeros,
+// so the product's K loop has no tail.
+#include <math.h>
+
+#include "gq_lm.h"
+
+namespace gq {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// rows of an odd length start at any element: vectors that need no more than its alignment
+typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_e2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_e4 __attribute__((aligned(4)));
+
+#define LDS_PTR __attribute__((address_space(3)))
+
+// ---------------------------------------------------------------- one block's encoding
+// Scale byte of a block whose largest magnitude has the bits `top` (sign cleared).  To nearest:
+// floor(log2 a) - 2, so that a lies in [4, 8) scales and what exceeds 6 saturates.  Stochastic:
+// the least scale with a <= 6 scales, so that nothing saturates and the rounding is unbiased:
+// one more where the mantissa is above 1.5.  Both are clamped at 2^-127 (byte 0).
+template <bool STOCH>
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+  int s = (int)(top >> 23) - 2;
+  if (STOCH) s += (top & 0x7FFFFFu) > 0x400000u;
+  return s < 0 ? 0 : s;
+}
+
+__device__ __forceinline__ float inverse_scale(int s) {
+  return __uint_as_float((uint32_t)(254 - s) << 23);
+}
+
+// 2^(s - 127); 2^-127 is subnormal, 255 is NaN.
+__device__ __forceinline__ float scale_value(uint32_t s) {
+  return s == 0 ? __uint_as_float(0x00400000u) : s == 255 ? __uint_as_float(0x7FC00000u)
+                                                           : __uint_as_float(s << 23);
+}
+
+// MurmurHash3's 32-bit finaliser of (counter XOR key), its first step already applied to the key.
+__device__ __forceinline__ uint32_t draw(uint32_t counter, uint32_t key_mix) {
+  uint32_t h = (counter ^ (counter >> 16)) ^ key_mix;
+  h *= 0x85EBCA6Bu;
+  h ^= h >> 13;
+  h *= 0xC2B2AE35u;
+  return h ^ (h >> 16);
+}
+
+// Stochastic code of x (|x| * inv <= 6): the grid's spacing is 1/2 below 2, 1 below 4, 2 above;
+// in units of it v has an exact floor and fraction p, and the code goes up if fp32(h) < p * 2^32.
+__device__ __forceinline__ uint32_t stochastic_code(float x, float inv, uint32_t h) {
+  const float v = fabsf(x) * inv;
+  const float unit = v < 2.0f ? 2.0f : v < 4.0f ? 1.0f : 0.5f;
+  const uint32_t first = v < 2.0f ? 0u : v < 4.0f ? 2u : 4u;
+  const float w = v * unit, low = floorf(w);
+  const uint32_t up = (float)h < (w - low) * 4294967296.0f;
+  return ((uint32_t)low + first + up) | ((__float_as_uint(x) >> 28) & 8u);
+}
+
+// Eight codes of x * inv to nearest, ties to even, saturating at 6.
+__device__ __forceinline__ uint32_t nearest_codes(const float *x, float inv) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0] * inv, x[1] * inv, 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2] * inv, x[3] * inv, 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4] * inv, x[5] * inv, 1.0f, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6] * inv, x[7] * inv, 1.0f, 3);
+  return w;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_one(const void *p, int64_t i) {
+  if constexpr (DT == 0)
+    return static_cast<const float *>(p)[i];
+  else
+    return __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16);
+}
+
+// Eight consecutive elements at any element's alignment.
+template <int DT>
+__device__ __forceinline__ void load_eight(const void *p, int64_t i, float (&x)[8]) {
+  if constexpr (DT == 0) {
+    const f32x4_e4 *q = reinterpret_cast<const f32x4_e4 *>(static_cast<const float *>(p) + i);
+    const f32x4 a = q[0], b = q[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = a[j];
+      x[4 + j] = b[j];
+    }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4_e2 *>(static_cast<const uint16_t *>(p) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(a[j] << 16);
+      x[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+  return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+template <bool STOCH>
+__device__ __forceinline__ uint32_t encode_block(const float (&x)[32], const uint32_t *counters,
+                                                 uint32_t key_mix, u32x4 &codes) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  if (top >= 0x7F800000u) {
+    codes = u32x4{0, 0, 0, 0};
+    return 255;
+  }
+  const int s = scale_byte<STOCH>(top);
+  const float inv = inverse_scale(s);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (STOCH) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w |= stochastic_code(x[8 * q + j], inv, draw(counters[8 * q + j], key_mix)) << (4 * j);
+      codes[q] = w;
+    } else {
+      codes[q] = nearest_codes(x + 8 * q, inv);
+    }
+  }
+  return (uint32_t)s;
+}
+
+// ---------------------------------------------------------------- quantisation
+// A thread a block of 32: along a row, or along a column (lanes on neighbouring columns).
+template <int DT, bool STOCH, bool BY_COLS>
+__global__ __launch_bounds__(256) void k_mx_quantize(const MxQuantArgs a, int64_t pitch) {
+  const int64_t lines = BY_COLS ? a.cols : a.rows, length = BY_COLS ? a.rows : a.cols;
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= lines * pitch) return;
+  const int64_t line = BY_COLS ? t % lines : t / pitch, blk = BY_COLS ? t / lines : t % pitch;
+  const int64_t first = blk * kMxBlock;
+  const int64_t step = BY_COLS ? a.ld : 1;
+  const int64_t base = BY_COLS ? first * a.ld + line : line * a.ld + first;
+  const int64_t cnt = length - first;
+  float x[32];
+  uint32_t counter[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    x[i] = i < cnt ? load_one<DT>(a.x, base + i * step) : 0.0f;
+    counter[i] = a.index_base + (uint32_t)(BY_COLS ? (first + i) * a.cols + line
+                                                   : line * a.cols + first + i);
+  }
+  u32x4 codes;
+  const uint32_t s = encode_block<STOCH>(x, counter, a.key_mix, codes);
+  uint8_t *out = BY_COLS ? a.codes_t : a.codes, *scales = BY_COLS ? a.scales_t : a.scales;
+  *reinterpret_cast<u32x4 *>(out + (line * pitch + blk) * 16) = codes;
+  scales[line * pitch + blk] = (uint8_t)s;
+}
+
+// ---------------------------------------------------------------- decoding
+// A thread eight elements: one word of codes, one scale.  The decoded values are exact in bf16.
+template <int DT>
+__global__ __launch_bounds__(256) void k_mx_dequantize(const MxDequantArgs a, int64_t pitch) {
+  const int64_t words = (a.cols + 7) / 8;
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.rows * words) return;
+  const int64_t row = t / words, word = t % words;
+  const uint32_t c = reinterpret_cast<const uint32_t *>(a.codes + row * pitch * 16)[word];
+  const float f = scale_value(a.scales[row * pitch + word / 4]);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t n = c >> (4 * i), mag = n & 7u;
+    const float m = mag < 2 ? 0.5f * mag
+                            : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
+    v[i] = (n & 8u ? -m : m) * f;
+  }
+  const int64_t at = row * a.ld + word * 8;
+  const int64_t cnt = a.cols - word * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < cnt) {
+      if constexpr (DT == 0)
+        static_cast<float *>(a.out)[at + i] = v[i];
+      else
+        static_cast<uint16_t *>(a.out)[at + i] = to_bf16(v[i]);
+    }
+}
+
+// ---------------------------------------------------------------- products
+// One output element: what there is of bias and of the old value is added in fp32, and the sum
+// is rounded once.
+__device__ __forceinline__ void finish_one(const MxMatmulArgs &a, int64_t m, int64_t n, float v) {
+  if (a.bias) v += a.bias[n];
+  const int64_t at = m * a.ldo + n;
+  if (a.out_dtype == 0) {
+    float *o = static_cast<float *>(a.out) + at;
+    *o = a.accumulate ? *o + v : v;
+  } else {
+    uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+    if (a.accumulate) v += __uint_as_float((uint32_t)*o << 16);
+    *o = to_bf16(v);
+  }
+}
+
+// Tiled product: a block of WM x WN waves, a wave FM x FN tiles of 32 x 32, K in steps of 256
+// (128 bytes of a row).  v_mfma_scale_f32_32x32x64: lane l holds 32 elements of row l mod 32,
+// those of block l / 32, and that block's scale; the result has column l mod 32 and rows
+// 8 i + 4 (l / 32) + 0..3.  The weights (B) are the first operand, so a lane ends with four
+// neighbouring n of one m.
+//
+// The operands go from memory to LDS without registers (buffer loads with an LDS destination),
+// one K step ahead, in two static buffers: the loop body handles two steps, so that every LDS
+// access names its buffer and waits only for its own loads.  Row r's 16-byte chunk c is kept at
+// chunk c XOR (r mod 8): a wave's reads of one chunk column fall on all banks.  A lane's eight
+// scale bytes of a row and step are loaded to registers, and one permutation puts its four
+// (every second byte) into a word whose bytes the four products of the step select.
+template <int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a, int pitch,
+                                                           int tiles_m, int tiles_n,
+                                                           int steps_each) {
+#if defined(__HIP_DEVICE_COMPILE__)  // buffer resources are a type of the device only
+  constexpr int BM = WM * FM * 32, BN = WN * FN * 32, T = WM * WN * 64;
+  constexpr int CA = BM * 8 / T, CB = BN * 8 / T;  // 16-byte chunks a thread and step
+  __shared__ __align__(1024) uint8_t lds0[(BM + BN) * 128];
+  __shared__ __align__(1024) uint8_t lds1[(BM + BN) * 128];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int bm = blockIdx.x % tiles_m, bn = blockIdx.x / tiles_m;
+  const int64_t m0 = (int64_t)bm * BM, n0 = (int64_t)bn * BN;
+  const int steps = pitch / 8;
+  const int step0 = blockIdx.y * steps_each;
+  const int count = min(steps_each, steps - step0);
+  const int row_bytes = pitch * 16;
+  const int rows_a = (int)min((int64_t)BM, a.M - m0), rows_b = (int)min((int64_t)BN, a.N - n0);
+  // resources that end with the tile's last row: nothing outside the matrices is ever read
+  const auto ra = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(static_cast<const uint8_t *>(a.a) + m0 * row_bytes), 0, rows_a * row_bytes, 0x00027000);
+  const auto rb = __builtin_amdgcn_make_buffer_rsrc((void *)(a.b + n0 * row_bytes), 0,
+                                                    rows_b * row_bytes, 0x00027000);
+  const auto rsa = __builtin_amdgcn_make_buffer_rsrc((void *)(a.a_scales + m0 * pitch), 0,
+                                                     rows_a * pitch, 0x00027000);
+  const auto rsb = __builtin_amdgcn_make_buffer_rsrc((void *)(a.b_scales + n0 * pitch), 0,
+                                                     rows_b * pitch, 0x00027000);
+  int off_a[CA], off_b[CB];
+  {
+    const int row = tid >> 3, chunk = ((tid & 7) ^ (row & 7)) << 4;
+#pragma unroll
+    for (int i = 0; i < CA; ++i) off_a[i] = min(row + i * (T / 8), rows_a - 1) * row_bytes + chunk;
+#pragma unroll
+    for (int i = 0; i < CB; ++i) off_b[i] = min(row + i * (T / 8), rows_b - 1) * row_bytes + chunk;
+  }
+  const int r32 = lane & 31, half = lane >> 5;
+  int soff_a[FM], soff_b[FN], frag[4];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) soff_a[i] = min((wm * FM + i) * 32 + r32, rows_a - 1) * pitch;
+#pragma unroll
+  for (int i = 0; i < FN; ++i) soff_b[i] = min((wn * FN + i) * 32 + r32, rows_b - 1) * pitch;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) frag[j] = r32 * 128 + (((2 * j + half) ^ (r32 & 7)) << 4);
+  const uint32_t mine = half ? 0x07050301u : 0x06040200u;
+
+  f32x16 acc[FM][FN] = {};
+  u32x2 sa[FM], sb[FN];
+  int pa[FM], pb[FN];
+  auto issue = [&](uint8_t *lds, int k) {  // loads of step k
+#pragma unroll
+    for (int i = 0; i < CA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_PTR void *)(lds + (i * T + wave * 64) * 16),
+                                               16, off_a[i], k * 128, 0, 0);
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rb, (LDS_PTR void *)(lds + BM * 128 + (i * T + wave * 64) * 16), 16, off_b[i], k * 128, 0,
+          0);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, soff_a[i], k * 8, 0);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) sb[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, soff_b[i], k * 8, 0);
+  };
+  auto arrive = [&]() {  // every wave's loads of the step are in LDS, its reads of the other done
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FM; ++i) pa[i] = __builtin_amdgcn_perm(sa[i].y, sa[i].x, mine);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) pb[i] = __builtin_amdgcn_perm(sb[i].y, sb[i].x, mine);
+  };
+  auto multiply = [&](const uint8_t *lds) {
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t *la = lds + wm * FM * 32 * 128, *lb = lds + (BM + wn * FN * 32) * 128;
+#define GQ_MX_STEP(J)                                                                        \
+  {                                                                                          \
+    i32x4 fa[FM], fb[FN];                                                                    \
+    _Pragma("unroll") for (int i = 0; i < FM; ++i) fa[i] =                                   \
+        *reinterpret_cast<const i32x4 *>(la + frag[J] + i * 4096);                           \
+    _Pragma("unroll") for (int j = 0; j < FN; ++j) fb[j] =                                   \
+        *reinterpret_cast<const i32x4 *>(lb + frag[J] + j * 4096);                           \
+    _Pragma("unroll") for (int i = 0; i < FM; ++i)                                           \
+        _Pragma("unroll") for (int j = 0; j < FN; ++j) {                                     \
+      const i32x8 x = __builtin_shufflevector(fa[i], fa[i], 0, 1, 2, 3, -1, -1, -1, -1);     \
+      const i32x8 y = __builtin_shufflevector(fb[j], fb[j], 0, 1, 2, 3, -1, -1, -1, -1);     \
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], 4, 4, J,  \
+                                                                  pb[j], J, pa[i]);          \
+    }                                                                                        \
+  }
+    GQ_MX_STEP(0)
+    GQ_MX_STEP(1)
+    GQ_MX_STEP(2)
+    GQ_MX_STEP(3)
+#undef GQ_MX_STEP
+  };
+  const int last = step0 + count - 1;
+  int k = step0;
+  if (count & 1) {  // an odd count's first step, so that the loop takes two at a time
+    issue(lds1, k);
+    arrive();
+    issue(lds0, min(k + 1, last));
+    multiply(lds1);
+    ++k;
+  } else {
+    issue(lds0, k);
+  }
+  for (; k <= last; k += 2) {
+    arrive();
+    issue(lds1, k + 1);
+    multiply(lds0);
+    arrive();
+    issue(lds0, min(k + 2, last));  // past the end: the last step again, not multiplied
+    multiply(lds1);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  __syncthreads();  // no load into LDS is in flight when the block ends
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + (wm * FM + i) * 32 + r32;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = n0 + (wn * FN + j) * 32 + 8 * q + 4 * half;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.N) {
+            if (gridDim.y > 1)
+              a.partial[((int64_t)blockIdx.y * a.M + m) * a.N + n + e] = acc[i][j][4 * q + e];
+            else
+              finish_one(a, m, n + e, acc[i][j][4 * q + e]);
+          }
+      }
+  }
+#endif
+}
+
+// The partial products of the K splits, added in their order.
+__global__ __launch_bounds__(256) void k_mx_join(const MxMatmulArgs a, int splits) {
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.M * a.N) return;
+  float v = 0.0f;
+  for (int i = 0; i < splits; ++i) v += a.partial[(int64_t)i * a.M * a.N + t];
+  finish_one(a, t / a.N, t % a.N, v);
+}
+
+// Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it, so
+// each block streams 16 rows of B straight to registers, its waves on interleaved K steps of
+// 256, and nothing of B is shared.  v_mfma_scale_f32_16x16x128: lane l holds 32 elements of row
+// l mod 16, block l / 16 of the step.  That is one whole block of A, so a lane quantises its own
+// block of fp32 / bf16 rows to nearest in registers.  The waves' sums meet in LDS, in order.
+constexpr int kFewWaves = 8;
+template <int AT>
+__global__ __launch_bounds__(kFewWaves * 64) void k_mx_matmul_few(const MxMatmulArgs a, int pitch) {
+  __shared__ f32x4 sums[kFewWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, quarter = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n = min(n0 + r16, a.N - 1);
+  const uint8_t *b = a.b + n * pitch * 16, *bs = a.b_scales + n * pitch;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int blk = wave * 8; blk < pitch; blk += kFewWaves * 8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = blk + 4 * h + quarter;
+      const i32x4 fb = *reinterpret_cast<const i32x4 *>(b + (int64_t)at * 16);
+      const int sb = bs[at];
+      i32x4 fa = {0, 0, 0, 0};
+      int sa = 0;
+      if (r16 < a.M) {
+        if constexpr (AT == 2) {
+          fa = *reinterpret_cast<const i32x4 *>(static_cast<const uint8_t *>(a.a) +
+                                                ((int64_t)r16 * pitch + at) * 16);
+          sa = a.a_scales[(int64_t)r16 * pitch + at];
+        } else {
+          const int64_t k0 = (int64_t)at * kMxBlock;
+          float x[32];
+          if (k0 + kMxBlock <= a.K) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              load_eight<AT>(a.a, r16 * a.lda + k0 + 8 * q, *reinterpret_cast<float(*)[8]>(x + 8 * q));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[i] = k0 + i < a.K ? load_one<AT>(a.a, r16 * a.lda + k0 + i) : 0.0f;
+          }
+          u32x4 c;
+          sa = (int)encode_block<false>(x, nullptr, 0, c);
+          fa = i32x4{(int)c.x, (int)c.y, (int)c.z, (int)c.w};
+        }
+      }
+      const i32x8 x = __builtin_shufflevector(fa, fa, 0, 1, 2, 3, -1, -1, -1, -1);
+      const i32x8 y = __builtin_shufflevector(fb, fb, 0, 1, 2, 3, -1, -1, -1, -1);
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(y, x, acc, 4, 4, 0, sb, 0, sa);
+    }
+  }
+  sums[wave][lane] = acc;
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    const int from = threadIdx.x >> 2, e = threadIdx.x & 3;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) v += sums[w][from][e];
+    const int64_t m = from & 15, col = n0 + 4 * (from >> 4) + e;
+    if (m < a.M && col < a.N) finish_one(a, m, col, v);
+  }
+}
+
+struct MatmulPlan {
+  int bm, bn;          // tile
+  int splits, each;    // K splits and steps of each
+};
+
+// Tile and K splits of a product of more than kFewRows rows.
+MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K) {
+  MatmulPlan p;
+  const int64_t steps = mx_pitch(K) / 8;
+  auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  p.bm = 256, p.bn = 256;
+  if (tiles(256, 256) < 256) p.bm = 128, p.bn = 128;
+  if (M <= 64) p.bm = 64, p.bn = 128;
+  int64_t splits = 512 / tiles(p.bm, p.bn);
+  if (splits > steps / 2) splits = steps / 2;
+  if (splits > 16) splits = 16;
+  if (splits < 1) splits = 1;
+  p.each = (int)((steps + splits - 1) / splits);
+  p.splits = (int)((steps + p.each - 1) / p.each);
+  return p;
+}
+
+constexpr int64_t kFewRows = 16;
+
+template <int WM, int WN, int FM, int FN>
+void matmul_tiles(const MxMatmulArgs &a, const MatmulPlan &p, hipStream_t s) {
+  const int tm = (int)((a.M + p.bm - 1) / p.bm), tn = (int)((a.N + p.bn - 1) / p.bn);
+  k_mx_matmul<WM, WN, FM, FN><<<dim3((unsigned)((int64_t)tm * tn), p.splits), WM * WN * 64, 0, s>>>(
+      a, (int)mx_pitch(a.K), tm, tn, p.each);
+}
+
+unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
+
+template <int DT, bool STOCH>
+void quantize_both(const MxQuantArgs &a, hipStream_t s) {
+  if (a.codes) {
+    const int64_t pitch = mx_pitch(a.cols);
+    k_mx_quantize<DT, STOCH, false><<<blocks_of(a.rows * pitch), 256, 0, s>>>(a, pitch);
+  }
+  if (a.codes_t) {
+    const int64_t pitch = mx_pitch(a.rows);
+    k_mx_quantize<DT, STOCH, true><<<blocks_of(a.cols * pitch), 256, 0, s>>>(a, pitch);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const MxQuantArgs &a, int dtype, hipStream_t s) {
+  if (dtype == 0)
+    a.stochastic ? quantize_both<0, true>(a, s) : quantize_both<0, false>(a, s);
+  else
+    a.stochastic ? quantize_both<1, true>(a, s) : quantize_both<1, false>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const MxDequantArgs &a, int out_dtype, hipStream_t s) {
+  const unsigned blocks = blocks_of(a.rows * ((a.cols + 7) / 8));
+  const int64_t pitch = mx_pitch(a.cols);
+  if (out_dtype == 0)
+    k_mx_dequantize<0><<<blocks, 256, 0, s>>>(a, pitch);
+  else
+    k_mx_dequantize<1><<<blocks, 256, 0, s>>>(a, pitch);
+  return hipGetLastError();
+}
+
+bool mx_matmul_packs_rows(int64_t M) { return M <= kFewRows; }
+
+size_t mx_matmul_scratch(int64_t M, int64_t N, int64_t K) {
+  if (M <= kFewRows) return 0;
+  const MatmulPlan p = plan_matmul(M, N, K);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
+}
+
+hipError_t launch_mx_matmul(const MxMatmulArgs &a, hipStream_t s) {
+  const int pitch = (int)mx_pitch(a.K);
+  if (a.M <= kFewRows) {
+    const unsigned blocks = (unsigned)((a.N + 15) / 16);
+    if (a.a_dtype == 0)
+      k_mx_matmul_few<0><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+    else if (a.a_dtype == 1)
+      k_mx_matmul_few<1><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+    else
+      k_mx_matmul_few<2><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+    return hipGetLastError();
+  }
+  const MatmulPlan p = plan_matmul(a.M, a.N, a.K);
+  if (p.bm == 256)
+    matmul_tiles<2, 4, 4, 2>(a, p, s);
+  else if (p.bm == 128)
+    matmul_tiles<2, 2, 2, 2>(a, p, s);
+  else
+    matmul_tiles<1, 4, 2, 1>(a, p, s);
+  if (p.splits > 1) k_mx_join<<<blocks_of(a.M * a.N), 256, 0, s>>>(a, p.splits);
+  return hipGetLastError();
+}
+
+}  // namespace gq

@@ -1,0 +1,754 @@
+// gq_vocab.hip -- gfx950 passes over rows of logits: the log probability of a given token with
+// the row's entropy and its most likely alternatives, and the distillation loss from a teacher's
+// top log probabilities with its gradient.
+//
+// Every pass reads a row once with the running maximum and sum of its softmax.  A block of 256
+// threads streams a row, or a slice of it where there are few rows; slices are joined in their
+// order by a second kernel, so results do not depend on timing.  A thread's step is a group of
+// 32 elements, four 8-element chunks 2048 apart, each chunk aligned to its own size in memory: a
+// row of an odd length starts inside a chunk, and the first and last chunk of a row are read
+// element by element, nothing outside the row at all.
+//
+// With m the largest logit, c = 1 / T and d = z - m:  s = sum e^(c d), lse = c m + log s.  d is
+// formed before it is scaled, so its rounding is relative to d, not to z.
+#include <float.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "gq_lm.h"
+
+namespace gq {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_e4 __attribute__((aligned(4)));
+
+constexpr int kThreads = 256;
+constexpr int kPart = kThreads * 8;         // elements of one chunk of every thread
+constexpr int kSweep = 4 * kPart;           // elements of one group of every thread
+constexpr int kSweeps = 16;                 // groups of a thread in a slice, at most
+constexpr int64_t kSlice = (int64_t)kSweep * kSweeps;
+constexpr int kMaxSlices = 64;
+constexpr int kCandidates = 1024;           // entries at or above the threshold, at most
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// A slice of a row: virtual index v counts from the aligned place at or before the slice's first
+// element; entry v - lead of the slice exists for lead <= v < lead + count.
+struct Slice {
+  const void *row;   // the row's first element
+  int64_t first;     // slice's first entry in the row
+  int32_t count;     // entries
+  int32_t lead;      // 0..7
+};
+
+__device__ __forceinline__ Slice slice_of(const void *logits, int elem, int64_t row, int64_t ld,
+                                          int64_t vocab, int64_t part, int64_t each) {
+  Slice s;
+  s.row = static_cast<const char *>(logits) + row * ld * elem;
+  s.first = part * each;
+  s.count = (int32_t)min(each, vocab - s.first);
+  s.lead = (int32_t)((row * ld + s.first) & 7);
+  return s;
+}
+
+__device__ __forceinline__ int sweeps_of(const Slice &s) {
+  return (s.lead + s.count + kSweep - 1) / kSweep;
+}
+
+template <int DT>
+__device__ __forceinline__ float entry(const Slice &s, int64_t i) {  // entry i of the slice
+  if constexpr (DT == 0)
+    return static_cast<const float *>(s.row)[s.first + i];
+  else
+    return __uint_as_float((uint32_t) static_cast<const uint16_t *>(s.row)[s.first + i] << 16);
+}
+
+// The eight entries at virtual index v (a multiple of 8); what is not there is -inf.
+template <int DT>
+__device__ __forceinline__ void load_chunk(const Slice &s, int v, float *x) {
+  const int at = v - s.lead;
+  if (at >= 0 && at + 8 <= s.count) {
+    if constexpr (DT == 0) {
+      const f32x4_e4 *p =
+          reinterpret_cast<const f32x4_e4 *>(static_cast<const float *>(s.row) + s.first + at);
+      const f32x4 a = p[0], b = p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = a[i];
+        x[4 + i] = b[i];
+      }
+    } else {
+      const u32x4 a =
+          *reinterpret_cast<const u32x4_e2 *>(static_cast<const uint16_t *>(s.row) + s.first + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(a[i] << 16);
+        x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = at + i >= 0 && at + i < s.count ? entry<DT>(s, at + i) : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------- softmax statistics
+// m: the largest entry (-inf: none above it); s = sum e^(c (x - ref)), w = sum (x - ref) e^(...),
+// ref = max(m, lowest): a row masked everywhere gives s = 0.
+struct Stat {
+  float m, s, w;
+};
+
+__device__ __forceinline__ float ref_of(float m) { return fmaxf(m, -FLT_MAX); }
+
+// e^(c d) with cl = c log2 e; d = -inf gives 0.
+__device__ __forceinline__ float exp_of(float d, float cl) { return __builtin_amdgcn_exp2f(d * cl); }
+
+__device__ __forceinline__ Stat moved(const Stat &a, float m, float cl) {  // to the reference of m
+  if (a.s == 0.0f) return Stat{m, 0.0f, 0.0f};
+  const float d = ref_of(a.m) - ref_of(m);
+  const float f = exp_of(d, cl);
+  return Stat{m, f * a.s, f == 0.0f ? 0.0f : f * (a.w + d * a.s)};
+}
+
+__device__ __forceinline__ Stat joined(const Stat &a, const Stat &b, float cl) {
+  const float m = fmaxf(a.m, b.m);
+  const Stat x = moved(a, m, cl), y = moved(b, m, cl);
+  return Stat{m, x.s + y.s, x.w + y.w};
+}
+
+template <bool W>
+__device__ __forceinline__ void add_group(Stat &a, const float (&x)[32], float gm, float cl) {
+  if (gm > a.m) a = moved(a, gm, cl);
+  const float ref = ref_of(a.m);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float d = x[i] - ref, e = exp_of(d, cl);
+    a.s += e;
+    if constexpr (W) a.w = fmaf(fmaxf(d, -FLT_MAX), e, a.w);
+  }
+}
+
+__device__ __forceinline__ float group_max(const float (&x)[32]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < 32; ++i) m = fmaxf(m, x[i]);
+  return m;
+}
+
+// The block's statistic, the same in every thread.  `room` holds one entry a wave.
+__device__ __forceinline__ Stat block_join(Stat a, float cl, Stat *room) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const Stat b = {__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.w, d)};
+    a = joined(a, b, cl);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = a;
+  __syncthreads();
+  a = room[0];
+  for (int i = 1; i < kThreads / 64; ++i) a = joined(a, room[i], cl);
+  return a;
+}
+
+__device__ __forceinline__ double block_sum(double v, double *room) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = room[0];
+  for (int i = 1; i < kThreads / 64; ++i) v += room[i];
+  return v;
+}
+
+// ---------------------------------------------------------------- the largest entries
+// Keys that order entries as their values, the lowest index first among equals; NaN is largest.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 as +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ uint64_t full_key(uint32_t key, uint32_t index) {
+  return (uint64_t)key << 32 | (uint32_t)~index;
+}
+
+struct TopRoom {
+  float group[kSweeps * kThreads];   // largest entry of each group
+  uint32_t thread_max[kThreads];
+  uint64_t cand[kCandidates];
+  uint32_t hist[256];
+  uint32_t count, prefix, need;
+};
+
+// Threshold t with at least k threads' maxima at or above it (0: fewer threads have an entry):
+// the slice's k-th largest entry is not below it.  Bit by bit over the 256 maxima, four a lane,
+// in every wave alike; stops as soon as exactly k are above.
+__device__ __forceinline__ uint32_t top_threshold(const TopRoom &room, int k) {
+  const int lane = threadIdx.x & 63;
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = room.thread_max[lane + 64 * i];
+  uint32_t t = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = t | 1u << bit;
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) above += __popcll(__ballot(v[i] >= c));
+    if (above >= k) t = c;
+    if (above == k) break;
+  }
+  return t;
+}
+
+// The k-th largest entry of the slice by its digits, then what is above it and the lowest
+// indices of what equals it.  For slices with more entries at the threshold than there is room
+// for (masked or constant rows), and for NaN.
+template <int DT>
+__device__ void top_by_digits(const Slice &s, int k, TopRoom &room) {
+  const int tid = threadIdx.x;
+  uint32_t prefix = 0, mask = 0;
+  if (tid == 0) room.need = (uint32_t)k;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    room.hist[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < s.count; i += kThreads) {
+      const uint32_t key = order_key(entry<DT>(s, i));
+      if ((key & mask) == prefix) atomicAdd(&room.hist[key >> shift & 255u], 1u);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t need = room.need;
+      int digit = 255;
+      while (digit > 0 && room.hist[digit] < need) need -= room.hist[digit--];
+      room.need = need;
+      room.prefix = prefix | (uint32_t)digit << shift;
+    }
+    __syncthreads();
+    prefix = room.prefix;
+    mask |= 255u << shift;
+  }
+  const uint32_t need = room.need;
+  if (tid == 0) room.count = 0;
+  __syncthreads();
+  for (int i = tid; i < s.count; i += kThreads) {
+    const uint32_t key = order_key(entry<DT>(s, i));
+    if (key > prefix) room.cand[atomicAdd(&room.count, 1u)] = full_key(key, (uint32_t)(s.first + i));
+  }
+  uint32_t taken = 0;
+  for (int base = 0; base < s.count && taken < need; base += kThreads) {
+    const int i = base + tid;
+    const bool equal = i < s.count && order_key(entry<DT>(s, i)) == prefix;
+    const uint64_t in_wave = __ballot(equal);
+    __syncthreads();
+    if ((tid & 63) == 0) room.hist[tid >> 6] = (uint32_t)__popcll(in_wave);
+    __syncthreads();
+    uint32_t before = taken, all = taken;
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < tid >> 6) before += room.hist[w];
+      all += room.hist[w];
+    }
+    before += (uint32_t)__popcll(in_wave & ((1ull << (tid & 63)) - 1));
+    if (equal && before < need)
+      room.cand[atomicAdd(&room.count, 1u)] = full_key(prefix, (uint32_t)(s.first + i));
+    taken = all;
+  }
+  __syncthreads();
+}
+
+// Leaves the slice's min(k, count) largest entries' keys in room.cand (at least those), with
+// room.count of them; room.group holds the groups' maxima, my_max this thread's.
+template <int DT>
+__device__ void top_candidates(const Slice &s, int k, float my_max, bool odd, TopRoom &room) {
+  const int tid = threadIdx.x;
+  room.thread_max[tid] = order_key(my_max);
+  if (tid == 0) room.count = 0;
+  __syncthreads();
+  if (!odd) {  // no NaN
+    const uint32_t t = top_threshold(room, k);
+    for (int g = 0; g < sweeps_of(s); ++g) {
+      if (order_key(room.group[g * kThreads + tid]) < t) continue;
+      for (int j = 0; j < 4; ++j) {
+        float x[8];
+        const int v = g * kSweep + j * kPart + tid * 8;
+        load_chunk<DT>(s, v, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = v - s.lead + i;
+          const uint32_t key = order_key(x[i]);
+          if (key >= t && at >= 0 && at < s.count) {
+            const uint32_t n = atomicAdd(&room.count, 1u);
+            if (n < kCandidates) room.cand[n] = full_key(key, (uint32_t)(s.first + at));
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (odd || room.count > kCandidates) {
+    __syncthreads();
+    top_by_digits<DT>(s, min(k, s.count), room);
+  }
+}
+
+// ---------------------------------------------------------------- log probabilities
+__device__ __forceinline__ void put_top(const LogprobArgs &a, int64_t row, int place, uint64_t key,
+                                        float ref, float log_s) {
+  const float x = key_value((uint32_t)(key >> 32));
+  const float d = (x - ref) * a.inv_t - log_s;
+  a.top_ids[row * a.top + place] = (int32_t)~(uint32_t)key;
+  a.top_logprobs[row * a.top + place] = x == -INFINITY ? -INFINITY : d;
+}
+
+template <int DT>
+__device__ __forceinline__ void put_token(const LogprobArgs &a, int64_t row, const Stat &all) {
+  const int64_t token = a.tokens[row];
+  const float log_s = logf(all.s);
+  float lp = 0.0f;
+  if (token >= 0 && token < a.vocab) {
+    const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, 0, a.vocab);
+    const float x = entry<DT>(s, token);
+    lp = x == -INFINITY && all.s == all.s ? -INFINITY : (x - ref_of(all.m)) * a.inv_t - log_s;
+  }
+  a.logprob[row] = lp;
+  a.entropy[row] = all.s == 0.0f ? 0.0f : log_s - a.inv_t * all.w / all.s;
+}
+
+// A block a slice.  One slice a row: the row's results; else the slice's statistic and its
+// largest entries in order, for k_logprobs_join.
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int slices,
+                                                       int64_t each) {
+  __shared__ Stat stats[kThreads / 64];
+  __shared__ typename std::conditional<TOP, TopRoom, int>::type room;
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
+  const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
+  const float cl = a.inv_t * kLog2e;
+  Stat mine = {-INFINITY, 0.0f, 0.0f};
+  float my_max = -INFINITY;
+  const int sweeps = sweeps_of(s);
+  for (int g = 0; g < sweeps; ++g) {
+    float x[32];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_chunk<DT>(s, g * kSweep + j * kPart + tid * 8, x + 8 * j);
+    const float gm = group_max(x);
+    if constexpr (TOP) room.group[g * kThreads + tid] = gm;
+    my_max = fmaxf(my_max, gm);
+    add_group<true>(mine, x, gm, cl);
+  }
+  const Stat all = block_join(mine, cl, stats);
+  uint64_t *keys = nullptr;
+  if (slices > 1) {
+    Stat *out = static_cast<Stat *>(a.scratch);
+    keys = reinterpret_cast<uint64_t *>(out + (((int64_t)gridDim.x + 1) & ~1ll)) +
+           (int64_t)blockIdx.x * a.top;
+    if (tid == 0) out[blockIdx.x] = all;
+  } else if (tid == 0) {
+    put_token<DT>(a, row, all);
+  }
+  if constexpr (TOP) {
+    top_candidates<DT>(s, a.top, my_max, all.s != all.s, room);
+    const int n = (int)room.count;
+    const float ref = ref_of(all.m), log_s = logf(all.s);
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t key = room.cand[i];
+      int place = 0;
+      for (int j = 0; j < n; ++j) place += room.cand[j] > key;
+      if (place < a.top) {
+        if (slices > 1)
+          keys[place] = key;
+        else
+          put_top(a, row, place, key, ref, log_s);
+      }
+    }
+    if (slices > 1)
+      for (int i = n + tid; i < a.top; i += kThreads) keys[i] = 0;
+  }
+}
+
+// A block a row: the slices' statistics in their order; an entry's place is the number of larger
+// ones, found in every slice's ordered list by bisection.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_logprobs_join(const LogprobArgs a, int slices) {
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const float cl = a.inv_t * kLog2e;
+  const Stat *in = static_cast<const Stat *>(a.scratch);
+  const uint64_t *keys =
+      reinterpret_cast<const uint64_t *>(in + ((a.rows * slices + 1) & ~1ll)) + row * slices * a.top;
+  in += row * slices;
+  Stat all = in[0];
+  for (int i = 1; i < slices; ++i) all = joined(all, in[i], cl);
+  if (tid == 0) put_token<DT>(a, row, all);
+  const float ref = ref_of(all.m), log_s = logf(all.s);
+  for (int i = tid; i < slices * a.top; i += kThreads) {
+    const uint64_t key = keys[i];
+    if (key == 0) continue;
+    int place = 0;
+    for (int p = 0; p < slices && place < a.top; ++p) {
+      const uint64_t *list = keys + p * a.top;
+      int lo = 0, hi = a.top;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid] > key)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      place += lo;
+    }
+    if (place < a.top) put_top(a, row, place, key, ref, log_s);
+  }
+}
+
+// ---------------------------------------------------------------- distillation
+// With S the taught entries (a row's ids: inside the vocabulary, each at its first place) and R
+// the rest: p_j = e^(lp_j), divided by their sum unless the rest has a bucket of its own, whose
+// mass p_R = 1 - sum p_j is matched with q_R = sum of q over R.
+//   loss = T^2 (sum p_j (log p_j - log q_j) + p_R (log p_R - log q_R))
+//   dz_v = w T (q_v - p_v) in S,  w T q_v (1 - p_R / q_R) in R
+// q_R is summed over R itself: the groups that hold a taught entry are left out of the stream
+// and added entry by entry, so nothing is subtracted.
+struct Taught {
+  int32_t id[kVocabTop];     // -1: not taught
+  float p[kVocabTop];
+  uint32_t in_group[kSweeps * kThreads];  // taught entries of each group of the slice
+  double sums[kThreads / 64];
+  Stat stats[kThreads / 64];
+};
+
+struct RowStat {  // what the gradient needs of a row
+  float ref;      // largest logit
+  float inv_s;    // 1 / sum e^(c (z - ref)); 0: the row is not taught
+  float rest;     // 1 - p_R / q_R
+  float scale;    // p_j = scale e^(lp_j)
+};
+
+// Loads the row's ids and e^(lp); returns the sum of the latter, in 64 bits: p_R is 1 less it.
+__device__ __forceinline__ double load_taught(const DistillArgs &a, int64_t row, Taught &t) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (tid < a.top) t.id[tid] = a.top_ids[row * a.top + tid];
+  __syncthreads();
+  bool ok = false;
+  double p = 0.0;
+  if (tid < a.top) {
+    const int32_t id = t.id[tid];
+    ok = id >= 0 && id < a.vocab;
+    for (int i = 0; i < tid && ok; ++i) ok = t.id[i] != id;
+    if (ok) p = exp((double)a.top_logprobs[row * a.top + tid]);
+  }
+  __syncthreads();
+  if (tid < a.top) {
+    if (!ok) t.id[tid] = -1;
+    t.p[tid] = (float)p;
+  }
+  return block_sum(p, t.sums);
+}
+
+__device__ __forceinline__ int place_in(const Slice &s, int64_t id, int *bit) {
+  const int v = (int)(id - s.first) + s.lead;
+  const int in = v % kSweep;
+  *bit = (in / kPart) * 8 + (in & 7);
+  return v / kSweep * kThreads + (in % kPart) / 8;
+}
+
+// Statistic of the slice's entries in R (tail) or of all of them.
+template <int DT, bool TAIL>
+__device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, Taught &t) {
+  const int tid = threadIdx.x;
+  const float cl = a.inv_t * kLog2e;
+  const int sweeps = sweeps_of(s);
+  if constexpr (TAIL) {
+    for (int g = 0; g < sweeps; ++g) t.in_group[g * kThreads + tid] = 0;
+    __syncthreads();
+    if (tid < a.top && t.id[tid] >= s.first && t.id[tid] < s.first + s.count) {
+      int bit;
+      const int g = place_in(s, t.id[tid], &bit);
+      atomicOr(&t.in_group[g], 1u << bit);
+    }
+    __syncthreads();
+  }
+  Stat mine = {-INFINITY, 0.0f, 0.0f};
+  for (int g = 0; g < sweeps; ++g) {
+    float x[32];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_chunk<DT>(s, g * kSweep + j * kPart + tid * 8, x + 8 * j);
+    if (TAIL && t.in_group[g * kThreads + tid] != 0) continue;
+    add_group<false>(mine, x, group_max(x), cl);
+  }
+  if constexpr (TAIL) {
+    // the group of taught entry j, if no earlier one is in it
+    if (tid < a.top && t.id[tid] >= s.first && t.id[tid] < s.first + s.count) {
+      int bit;
+      const int g = place_in(s, t.id[tid], &bit);
+      bool first = true;
+      for (int i = 0; i < tid && first; ++i)
+        if (t.id[i] >= s.first && t.id[i] < s.first + s.count) {
+          int b;
+          first = place_in(s, t.id[i], &b) != g;
+        }
+      if (first) {
+        const uint32_t mask = t.in_group[g];
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          load_chunk<DT>(s, (g / kThreads) * kSweep + j * kPart + (g % kThreads) * 8, x + 8 * j);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (mask >> i & 1u) x[i] = -INFINITY;
+        add_group<false>(mine, x, group_max(x), cl);
+      }
+    }
+  }
+  return block_join(mine, cl, t.stats);
+}
+
+// Loss and gradient constants of a row from the statistic of R (tail) or of all entries.  The
+// loss is a small difference of logarithms of the same sums, so what follows the stream (128
+// terms at most) is held in 64 bits: an error of R's sum then counts q_R - p_R times only.
+template <int DT, bool TAIL>
+__device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row, Stat rest,
+                                              double sum_p, Taught &t) {
+  const int tid = threadIdx.x;
+  const float cl = a.inv_t * kLog2e;
+  const bool mine = tid < a.top && t.id[tid] >= 0;
+  float x = 0.0f, lp = 0.0f;
+  if (mine) {
+    const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, 0, a.vocab);
+    x = entry<DT>(s, t.id[tid]);
+    lp = a.top_logprobs[row * a.top + tid];
+  }
+  float m = rest.m;
+  if constexpr (TAIL) m = block_join(Stat{mine ? fmaxf(x, rest.m) : rest.m, 0.0f, 0.0f}, cl, t.stats).m;
+  const float ref = ref_of(m);
+  const double inv_t = 1.0 / (double)a.temperature;
+  const double rest_s =
+      rest.s == 0.0f ? 0.0 : (double)rest.s * exp(((double)ref_of(rest.m) - ref) * inv_t);
+  double all_s = rest_s;
+  if constexpr (TAIL) all_s += block_sum(mine ? (double)exp_of(x - ref, cl) : 0.0, t.sums);
+  const double log_s = log(all_s);
+  double p_rest = TAIL ? fmax(1.0 - sum_p, 0.0) : 0.0;
+  const double scale = TAIL ? 1.0 : 1.0 / sum_p;
+  double term = 0.0;
+  if (mine && !(lp == -INFINITY)) {
+    const double log_p = TAIL ? (double)lp : (double)lp - log(sum_p);
+    const double log_q =
+        x == -INFINITY && all_s == all_s ? -INFINITY : ((double)x - ref) * inv_t - log_s;
+    term = exp(log_p) * (log_p - log_q);
+  }
+  double loss = block_sum(term, t.sums);
+  const double taught = block_sum(mine ? 1.0 : 0.0, t.sums);
+  // a row masked everywhere has q = 0, not 0 / 0
+  RowStat r = {ref, all_s == 0.0 ? 1.0f : (float)(1.0 / all_s), 1.0f, (float)scale};
+  // no entry is left for the rest, or the student has none there and p_R is the sum's rounding
+  if (TAIL && (taught == (double)a.vocab || (rest_s == 0.0 && p_rest < 0x1p-16))) p_rest = 0.0;
+  if (TAIL && p_rest > 0.0) {
+    const double q_rest = rest_s == 0.0 ? 0.0 : rest_s / all_s;
+    loss += p_rest * log(p_rest / q_rest);
+    r.rest = (float)(1.0 - p_rest / q_rest);
+  }
+  const bool none = taught == 0.0 || (!TAIL && sum_p == 0.0);
+  if (none) r = RowStat{ref, 0.0f, 0.0f, 0.0f};
+  if (tid == 0) {
+    a.loss[row] = none ? 0.0f : (float)(loss * a.temperature * a.temperature);
+    if (a.stats) reinterpret_cast<f32x4 *>(a.stats)[row] = f32x4{r.ref, r.inv_s, r.rest, r.scale};
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+  return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+template <int DT>
+__device__ __forceinline__ void put_grad(const DistillArgs &a, int64_t at, float v) {
+  if constexpr (DT == 0)
+    static_cast<float *>(a.grad)[at] = v;
+  else
+    static_cast<uint16_t *>(a.grad)[at] = to_bf16(v);
+}
+
+// The gradient of the slice's entries: all of them as entries of R, then the taught ones.
+template <int DT>
+__device__ __forceinline__ void grad_slice(const DistillArgs &a, int64_t row, const Slice &s,
+                                           const RowStat &r, const Taught &t) {
+  const int tid = threadIdx.x;
+  const float cl = a.inv_t * kLog2e;
+  const float w = (a.weight ? a.weight[row] : 1.0f) * a.temperature;
+  const bool taught = r.inv_s != 0.0f;
+  const float f = w * r.rest * r.inv_s;
+  const int64_t out = row * a.ldg + s.first;
+  // this thread's taught entry, read before the stream: the gradient may replace the logits
+  const bool mine = tid < a.top && t.id[tid] >= s.first && t.id[tid] < s.first + s.count;
+  const float mine_x = mine ? entry<DT>(s, t.id[tid] - s.first) : 0.0f;
+  __syncthreads();
+  const int parts = (s.lead + s.count + kPart - 1) / kPart;
+  for (int g = 0; g < parts; ++g) {
+    const int v = g * kPart + tid * 8, at = v - s.lead;
+    float x[8];
+    load_chunk<DT>(s, v, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float e = exp_of(x[i] - r.ref, cl);
+      x[i] = !taught || e == 0.0f ? 0.0f : f * e;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at + i >= 0 && at + i < s.count) put_grad<DT>(a, out + at + i, x[i]);
+  }
+  __syncthreads();  // the taught entries are written over what the stream put there
+  if (mine) {
+    const float q = exp_of(mine_x - r.ref, cl) * r.inv_s;
+    put_grad<DT>(a, row * a.ldg + t.id[tid], taught ? w * (q - t.p[tid] * r.scale) : 0.0f);
+  }
+}
+
+// A block a row: the loss, and the gradient where it is asked for.
+template <int DT, bool TAIL>
+__global__ __launch_bounds__(kThreads) void k_distill_rows(const DistillArgs a) {
+  __shared__ Taught t;
+  const int64_t row = blockIdx.x;
+  const double sum_p = load_taught(a, row, t);
+  const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, 0, a.vocab);
+  const Stat rest = rest_stat<DT, TAIL>(a, s, t);
+  const RowStat r = finish_row<DT, TAIL>(a, row, rest, sum_p, t);
+  if (a.grad) grad_slice<DT>(a, row, s, r, t);
+}
+
+// A block a slice: the slice's statistic.
+template <int DT, bool TAIL>
+__global__ __launch_bounds__(kThreads) void k_distill_slices(const DistillArgs a, int slices,
+                                                             int64_t each) {
+  __shared__ Taught t;
+  const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
+  if constexpr (TAIL) load_taught(a, row, t);
+  const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
+  const Stat rest = rest_stat<DT, TAIL>(a, s, t);
+  if (threadIdx.x == 0) static_cast<Stat *>(a.scratch)[blockIdx.x] = rest;
+}
+
+// A block a row: the slices' statistics in their order, the loss and the gradient's constants.
+template <int DT, bool TAIL>
+__global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, int slices) {
+  __shared__ Taught t;
+  const int64_t row = blockIdx.x;
+  const double sum_p = load_taught(a, row, t);
+  const Stat *in = static_cast<const Stat *>(a.scratch) + row * slices;
+  Stat rest = in[0];
+  for (int i = 1; i < slices; ++i) rest = joined(rest, in[i], a.inv_t * kLog2e);
+  finish_row<DT, TAIL>(a, row, rest, sum_p, t);
+}
+
+// A block a slice: the gradient from the rows' constants.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, int slices,
+                                                           int64_t each) {
+  __shared__ Taught t;
+  const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
+  load_taught(a, row, t);
+  const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
+  const f32x4 r = reinterpret_cast<const f32x4 *>(a.stats)[row];
+  grad_slice<DT>(a, row, s, RowStat{r.x, r.y, r.z, r.w}, t);
+}
+
+// Slices of a row: as many as fill the GPU, at least 2048 entries each, at most kSlice.
+int slices_of(int64_t rows, int64_t vocab, int64_t *each) {
+  int64_t n = 1024 / rows;
+  if (n > vocab / kPart) n = vocab / kPart;
+  if (n > kMaxSlices) n = kMaxSlices;
+  const int64_t least = (vocab + kSlice - 9) / (kSlice - 8);
+  if (n < least) n = least;
+  if (n < 1) n = 1;
+  *each = ((vocab + n - 1) / n + 7) & ~7ll;
+  return (int)((vocab + *each - 1) / *each);
+}
+
+template <int DT>
+void logprobs_of(const LogprobArgs &a, int slices, int64_t each, hipStream_t s) {
+  const unsigned blocks = (unsigned)(a.rows * slices);
+  if (a.top > 0)
+    k_logprobs<DT, true><<<blocks, kThreads, 0, s>>>(a, slices, each);
+  else
+    k_logprobs<DT, false><<<blocks, kThreads, 0, s>>>(a, slices, each);
+  if (slices > 1) k_logprobs_join<DT><<<(unsigned)a.rows, kThreads, 0, s>>>(a, slices);
+}
+
+template <int DT>
+void distill_grad_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
+  k_distill_grad<DT><<<(unsigned)(a.rows * slices), kThreads, 0, s>>>(a, slices, each);
+}
+
+template <int DT, bool TAIL>
+void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
+  if (slices == 1) {
+    k_distill_rows<DT, TAIL><<<(unsigned)a.rows, kThreads, 0, s>>>(a);
+    return;
+  }
+  DistillArgs b = a;
+  if (!b.stats)
+    b.stats = reinterpret_cast<float *>(static_cast<char *>(a.scratch) +
+                                        (((size_t)a.rows * slices * sizeof(Stat) + 15) & ~(size_t)15));
+  k_distill_slices<DT, TAIL><<<(unsigned)(a.rows * slices), kThreads, 0, s>>>(b, slices, each);
+  k_distill_join<DT, TAIL><<<(unsigned)a.rows, kThreads, 0, s>>>(b, slices);
+  if (a.grad) distill_grad_of<DT>(b, slices, each, s);
+}
+
+}  // namespace
+
+size_t logprobs_scratch(int64_t rows, int64_t vocab, int top) {
+  int64_t each;
+  const int n = slices_of(rows, vocab, &each);
+  if (n == 1) return 0;
+  return (size_t)((rows * n + 1) & ~1ll) * sizeof(Stat) + (size_t)rows * n * top * 8;
+}
+
+hipError_t launch_token_logprobs(const LogprobArgs &a, int dtype, hipStream_t s) {
+  int64_t each;
+  const int n = slices_of(a.rows, a.vocab, &each);
+  if (dtype == 0)
+    logprobs_of<0>(a, n, each, s);
+  else
+    logprobs_of<1>(a, n, each, s);
+  return hipGetLastError();
+}
+
+size_t distill_scratch(int64_t rows, int64_t vocab) {
+  int64_t each;
+  const int n = slices_of(rows, vocab, &each);
+  return n == 1 ? 0 : (((size_t)rows * n * sizeof(Stat) + 15) & ~(size_t)15) + (size_t)rows * 16;
+}
+
+hipError_t launch_distill_loss(const DistillArgs &a, int dtype, hipStream_t s) {
+  int64_t each;
+  const int n = slices_of(a.rows, a.vocab, &each);
+  if (dtype == 0)
+    a.tail ? distill_of<0, true>(a, n, each, s) : distill_of<0, false>(a, n, each, s);
+  else
+    a.tail ? distill_of<1, true>(a, n, each, s) : distill_of<1, false>(a, n, each, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_distill_grad(const DistillArgs &a, int dtype, hipStream_t s) {
+  int64_t each;
+  const int n = slices_of(a.rows, a.vocab, &each);
+  if (dtype == 0)
+    distill_grad_of<0>(a, n, each, s);
+  else
+    distill_grad_of<1>(a, n, each, s);
+  return hipGetLastError();
+}
+
+}  // namespace gq

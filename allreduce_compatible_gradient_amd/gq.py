@@ -21,14 +21,16 @@ OK, EINVAL, EOVERFLOW, EALIGN, ELAUNCH, ENONFINITE, ENOMEM = range(7)
 F32, BF16 = 0, 1
 UNIFORM, EXP = 0, 1
 NORM_L2, NORM_MAX = 0, 1
+MX = 2                                   # element type of packed microscaled matrices
+MX_NEAREST, MX_STOCHASTIC = 0, 1
 
 if not os.path.exists(LIB_PATH):
     raise ImportError("libgq.so is not built (%s); run `python -m "
                       "allreduce_compatible_gradient_amd.build`" % LIB_PATH)
 
 _lib = C.CDLL(LIB_PATH)
-_p, _i32, _i64, _u32, _u64, _d = (C.c_void_p, C.c_int32, C.c_int64, C.c_uint32, C.c_uint64,
-                                   C.c_double)
+_p, _i32, _i64, _u32, _u64, _d, _f = (C.c_void_p, C.c_int32, C.c_int64, C.c_uint32, C.c_uint64,
+                                       C.c_double, C.c_float)
 _SIGS = {
     "gq_create": (_i32, [C.POINTER(C.c_void_p)]),
     "gq_destroy": (None, [_p]),
@@ -57,6 +59,18 @@ _SIGS = {
     "gq_lq_step_workers": (_i32, [_p, _p, _p, _p, _i32, _i64, _i64, _i32, _d, _i32, _i32, _p,
                                   _p, _p, _p, _p, _p, _p, _p]),
     "gq_trim": (_i32, [_p]),
+    "gq_mx_pitch": (_i64, [_i64]),
+    "gq_mx_quantize": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i32, _u64, _u32, _u32, _p, _p, _p,
+                              _p, _p]),
+    "gq_mx_dequantize": (_i32, [_p, _p, _p, _i64, _i64, _i32, _p, _i64, _p]),
+    "gq_mx_matmul": (_i32, [_p, _p, _i32, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _i32, _i32, _p,
+                            _i64, _p]),
+    "gq_token_logprobs": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _p, _f, _i32, _p, _p, _p, _p,
+                                 _p]),
+    "gq_distill_loss": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _p, _p, _i32, _f, _i32, _p, _p, _p,
+                               _p, _i64, _p]),
+    "gq_distill_grad": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _p, _p, _i32, _f, _i32, _p, _p, _p,
+                               _i64, _p]),
     "gq_global_norm_noalloc": (_i32, [_p, _p, _i32, _i32, _i64, _p, _i32, _p, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -445,6 +459,199 @@ def lq_step_workers(Gs, Es, Qs, alpha, bits, bits_q=None, out=None, want_pre=Fal
         _dev(o["q_codes"], "q_codes", torch.int8), _dev(o["q_colmax"], "q_colmax", torch.float32),
         _dev(o["G_hat"], "G_hat", torch.float32), opt("p_pre"), opt("q_pre"), _stream()))
     return o
+
+
+# ----------------------------------------------------------------------------- 4-bit matrices
+class MXTensor:
+    """A packed microscaled 4-bit matrix of rows x cols: ``codes`` rows x 16 * mx_pitch(cols)
+    and ``scales`` rows x mx_pitch(cols) bytes, padded with zeros as gq.h describes."""
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        pitch = mx_pitch(cols)
+        if (codes.dim() != 2 or tuple(scales.shape) != (codes.shape[0], pitch)
+                or codes.shape[1] != 16 * pitch):
+            raise ValueError("a packed matrix of %d columns has rows of %d code and %d scale bytes"
+                             % (cols, 16 * pitch, pitch))
+        self.codes, self.scales, self.rows, self.cols = codes, scales, codes.shape[0], cols
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "MXTensor":
+        pitch = mx_pitch(cols)
+        return MXTensor(torch.empty(rows, 16 * pitch, dtype=torch.uint8, device=device),
+                        torch.empty(rows, pitch, dtype=torch.uint8, device=device), cols)
+
+
+def mx_pitch(cols: int) -> int:
+    """Blocks of 32 in a packed row of ``cols`` elements, padding included."""
+    return (cols + 255) // 256 * 8
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None):
+    """(address, row stride) of a matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a matrix with contiguous rows" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
+
+
+def mx_quantize(x, rounding=MX_NEAREST, seed=0, worker=0, index_base=0, by_rows=True,
+                by_cols=False, out: Optional[MXTensor] = None, out_t: Optional[MXTensor] = None,
+                ctx: Optional[Context] = None):
+    """Quantise a matrix to microscaled 4-bit floating point.  Returns (packed rows, packed
+    columns), an MXTensor of x and one of its transpose; None for one that is not asked for."""
+    ctx = ctx or context()
+    p, ld = _rows(x, "x")
+    rows, cols = x.shape
+    q = (out or MXTensor.empty(rows, cols, x.device)) if by_rows else None
+    qt = (out_t or MXTensor.empty(cols, rows, x.device)) if by_cols else None
+    for t, shape, name in ((q, (rows, cols), "out"), (qt, (cols, rows), "out_t")):
+        if t is not None and (t.rows, t.cols) != shape:
+            raise ValueError("%s must be a packed %d x %d matrix" % (name, *shape))
+    ctx.check(_lib.gq_mx_quantize(
+        ctx.handle, p, _elt(x), rows, cols, ld, rounding, seed, worker, index_base,
+        None if q is None else _dev(q.codes, "out.codes", torch.uint8),
+        None if q is None else _dev(q.scales, "out.scales", torch.uint8),
+        None if qt is None else _dev(qt.codes, "out_t.codes", torch.uint8),
+        None if qt is None else _dev(qt.scales, "out_t.scales", torch.uint8), _stream()))
+    return q, qt
+
+
+def mx_dequantize(q: MXTensor, out_dtype=BF16, out=None, ctx: Optional[Context] = None):
+    """The values of a packed matrix (rows x cols, bf16 or fp32)."""
+    ctx = ctx or context()
+    if out is None:
+        out = torch.empty(q.rows, q.cols, dtype=_torch_dtype(out_dtype), device=q.codes.device)
+    p, ld = _rows(out, "out", _torch_dtype(out_dtype))
+    if tuple(out.shape) != (q.rows, q.cols):
+        raise ValueError("out must be %d x %d" % (q.rows, q.cols))
+    ctx.check(_lib.gq_mx_dequantize(ctx.handle, _dev(q.codes, "codes", torch.uint8),
+                                    _dev(q.scales, "scales", torch.uint8), q.rows, q.cols,
+                                    out_dtype, p, ld, _stream()))
+    return out
+
+
+def mx_matmul(a, b: MXTensor, bias=None, out_dtype=BF16, out=None, accumulate=False,
+              ctx: Optional[Context] = None):
+    """a @ b.T (+ bias) (+ out): ``b`` packed N x K; ``a`` packed M x K, or an fp32 / bf16 matrix
+    that the call quantises to nearest.  Returns M x N of out_dtype."""
+    ctx = ctx or context()
+    if isinstance(a, MXTensor):
+        m, k = a.rows, a.cols
+        pa, ta, sa, lda = (_dev(a.codes, "a.codes", torch.uint8), MX,
+                           _dev(a.scales, "a.scales", torch.uint8), 0)
+    else:
+        pa, lda = _rows(a, "a")
+        (m, k), ta, sa = a.shape, _elt(a), None
+    if k != b.cols:
+        raise ValueError("a has %d columns, b has %d" % (k, b.cols))
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(m, b.rows, dtype=_torch_dtype(out_dtype), device=b.codes.device)
+    po, ldo = _rows(out, "out", _torch_dtype(out_dtype))
+    if tuple(out.shape) != (m, b.rows):
+        raise ValueError("out must be %d x %d" % (m, b.rows))
+    if bias is not None and bias.numel() != b.rows:
+        raise ValueError("bias must hold %d values" % b.rows)
+    ctx.check(_lib.gq_mx_matmul(ctx.handle, pa, ta, sa, lda, _dev(b.codes, "b.codes", torch.uint8),
+                                _dev(b.scales, "b.scales", torch.uint8), m, b.rows, k,
+                                None if bias is None else _dev(bias, "bias", torch.float32),
+                                1 if accumulate else 0, out_dtype, po, ldo, _stream()))
+    return out
+
+
+# ----------------------------------------------------------------------------- rows of logits
+def token_logprobs(logits, tokens, top=0, temperature=1.0, out=None,
+                   ctx: Optional[Context] = None):
+    """(logprob, entropy, top_ids, top_logprobs) of each row: the given token's log probability,
+    the row's entropy and its ``top`` largest entries (None where top = 0).  ``out``: those
+    tensors, to be written in place of new ones."""
+    ctx = ctx or context()
+    p, ld = _rows(logits, "logits")
+    rows, vocab = logits.shape
+    if tokens.numel() != rows:
+        raise ValueError("tokens must hold one entry a row")
+    if out is None:
+        dev = logits.device
+        out = (torch.empty(rows, dtype=torch.float32, device=dev),
+               torch.empty(rows, dtype=torch.float32, device=dev),
+               torch.empty(rows, top, dtype=torch.int32, device=dev) if top > 0 else None,
+               torch.empty(rows, top, dtype=torch.float32, device=dev) if top > 0 else None)
+    elif out[0].numel() != rows or out[1].numel() != rows or (
+            top > 0 and (tuple(out[2].shape) != (rows, top) or tuple(out[3].shape) != (rows, top))):
+        raise ValueError("out must be (rows, rows, rows x top, rows x top)")
+    ctx.check(_lib.gq_token_logprobs(
+        ctx.handle, p, _elt(logits), rows, vocab, ld, _dev(tokens, "tokens", torch.int64),
+        temperature, top, _dev(out[0], "out[0]", torch.float32),
+        _dev(out[1], "out[1]", torch.float32),
+        _dev(out[2], "out[2]", torch.int32) if top > 0 else None,
+        _dev(out[3], "out[3]", torch.float32) if top > 0 else None, _stream()))
+    return out
+
+
+def _teacher(logits, top_ids, top_logprobs):
+    if top_ids.dim() != 2 or top_ids.shape[0] != logits.shape[0] \
+            or top_logprobs.shape != top_ids.shape:
+        raise ValueError("top_ids and top_logprobs must be rows x top")
+    return (_dev(top_ids, "top_ids", torch.int32),
+            _dev(top_logprobs, "top_logprobs", torch.float32), top_ids.shape[1])
+
+
+def _row_weight(w, rows):
+    if w is None:
+        return None
+    if w.numel() != rows:
+        raise ValueError("row_weight must hold one entry a row")
+    return _dev(w, "row_weight", torch.float32)
+
+
+def distill_loss(logits, top_ids, top_logprobs, temperature=1.0, tail=False, row_weight=None,
+                 dlogits=None, ctx: Optional[Context] = None):
+    """Each row's distillation loss from a teacher's top log probabilities.  Without row_weight
+    and dlogits: (loss, stats), the stats for distill_grad.  With either: (loss, dlogits), the
+    gradient of sum(row_weight * loss) from the same call; ``dlogits`` may be ``logits``."""
+    ctx = ctx or context()
+    p, ld = _rows(logits, "logits")
+    rows, vocab = logits.shape
+    ids, lps, top = _teacher(logits, top_ids, top_logprobs)
+    loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    stats, pd, ldd = None, None, 0
+    if row_weight is None and dlogits is None:
+        stats = torch.empty(rows, 4, dtype=torch.float32, device=logits.device)
+    else:
+        if dlogits is None:
+            dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        pd, ldd = _rows(dlogits, "dlogits", logits.dtype)
+        if dlogits.shape != logits.shape:
+            raise ValueError("dlogits must be %d x %d" % (rows, vocab))
+    ctx.check(_lib.gq_distill_loss(
+        ctx.handle, p, _elt(logits), rows, vocab, ld, ids, lps, top, temperature,
+        1 if tail else 0, _row_weight(row_weight, rows), _dev(loss, "loss"),
+        None if stats is None else _dev(stats, "stats"), pd, ldd, _stream()))
+    return loss, (dlogits if stats is None else stats)
+
+
+def distill_grad(logits, top_ids, top_logprobs, temperature, tail, stats, row_weight=None,
+                 dlogits=None, ctx: Optional[Context] = None):
+    """The gradient of sum(row_weight * loss) from distill_loss' stats."""
+    ctx = ctx or context()
+    p, ld = _rows(logits, "logits")
+    rows, vocab = logits.shape
+    ids, lps, top = _teacher(logits, top_ids, top_logprobs)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    pd, ldd = _rows(dlogits, "dlogits", logits.dtype)
+    if dlogits.shape != logits.shape or stats.numel() != 4 * rows:
+        raise ValueError("dlogits must be %d x %d and stats %d x 4" % (rows, vocab, rows))
+    ctx.check(_lib.gq_distill_grad(
+        ctx.handle, p, _elt(logits), rows, vocab, ld, ids, lps, top, temperature,
+        1 if tail else 0, _dev(stats, "stats", torch.float32), _row_weight(row_weight, rows), pd,
+        ldd, _stream()))
+    return dlogits
 
 
 def trim(ctx: Optional[Context] = None) -> None:

@@ -298,6 +298,105 @@ gq_status gq_lq_step_workers(gq_ctx *ctx, const float *const *G, float *const *E
                              float *p_colmax, int8_t *q_codes, float *q_colmax, float *G_hat,
                              float *p_pre_or_null, float *q_pre_or_null, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators of language models, for training in 4 bits from a teacher's answers with the
+ * gradients' exchange above: microscaled 4-bit floating point and its product, the log
+ * probabilities of given tokens, and distillation from a teacher's top log probabilities.
+ * Row strides are in elements and at least the row's length; rows may start at any element of
+ * a 16-byte aligned buffer (a vocabulary of an odd size). */
+
+/* Packed microscaled matrices (GQ_MX).  A row of `cols` elements is cut into blocks of 32.  A
+ * block holds a scale 2^(s - 127), s one byte, and 32 codes of 4 bits: bit 3 the sign, bits 0-2
+ * an index into {0, 0.5, 1, 1.5, 2, 3, 4, 6}; s = 255 makes the block NaN.  Element 2t of a row
+ * sits in the low nibble of its byte t.  Rows are padded to a multiple of 256 elements with
+ * zero codes and zero scale bytes; gq_mx_pitch(cols) is a row's number of blocks, so
+ *   codes  rows x 16 * gq_mx_pitch(cols) bytes,  scales  rows x gq_mx_pitch(cols) bytes.
+ * A matrix has at most 2^23 rows and 2^23 columns. */
+#define GQ_MX 2
+/* rounding of gq_mx_quantize, with a the block's largest magnitude */
+#define GQ_MX_NEAREST 0     /* scale 2^(floor(log2 a) - 2); to nearest, ties to the even code,
+                               magnitudes above 6 scales become 6 */
+#define GQ_MX_STOCHASTIC 1  /* the least power of two with a <= 6 scales; up with probability
+                               (v - l) / (u - l) between the codes' values l <= v < u */
+/* Blocks of a packed row of `cols` elements: ceil(cols / 256) * 8 (0 for cols < 1). */
+int64_t gq_mx_pitch(int64_t cols);
+
+/* Quantise a matrix by rows (codes, scales: rows x cols), by columns (codes_t, scales_t: the
+ * packed transpose, cols x rows, its blocks down the columns), or both; a pair that is not
+ * wanted is NULL.  Scales are clamped at 2^-127; a block that holds a NaN or an infinity gets
+ * s = 255 and zero codes.  Stochastic: element (i, j) draws from (seed, worker, index_base +
+ * i * cols + j) as gq_quantize_pack does, by rows and by columns alike, and goes up when the
+ * draw r < p; rows * cols + index_base must not exceed 2^32 (seed, worker and index_base are
+ * not used to nearest).
+ *   x  rows x cols of `dtype` (GQ_F32 / GQ_BF16), row stride ld */
+gq_status gq_mx_quantize(gq_ctx *ctx, const void *x, int32_t dtype, int64_t rows, int64_t cols,
+                         int64_t ld, int32_t rounding, uint64_t seed, uint32_t worker,
+                         uint32_t index_base, uint8_t *codes, uint8_t *scales,
+                         uint8_t *codes_t, uint8_t *scales_t, void *stream);
+
+/* The values of a packed matrix, exact in both types except that magnitudes below bf16's or
+ * above fp32's range round as the type does.  out rows x cols of out_dtype, row stride ld. */
+gq_status gq_mx_dequantize(gq_ctx *ctx, const uint8_t *codes, const uint8_t *scales,
+                           int64_t rows, int64_t cols, int32_t out_dtype, void *out, int64_t ld,
+                           void *stream);
+
+/* out = A B^T (+ bias) (+ out), A M x K, B N x K: a linear layer's forward product with B its
+ * weights; its backward products with B the weights by columns (dX = dY W) and with A and B the
+ * gradient and the activations by columns (dW = dY^T X).  Sums in fp32, rounded once.
+ *   a       packed codes (a_dtype GQ_MX, with a_scales; lda unused), or fp32 / bf16 rows of
+ *           stride lda (a_scales NULL) that are quantised to nearest as gq_mx_quantize would
+ *   b       packed codes and scales
+ *   bias    N fp32, or NULL;  accumulate: 1 adds to what `out` holds
+ *   out     M x N of out_dtype, row stride ldo */
+gq_status gq_mx_matmul(gq_ctx *ctx, const void *a, int32_t a_dtype, const uint8_t *a_scales,
+                       int64_t lda, const uint8_t *b, const uint8_t *b_scales, int64_t M,
+                       int64_t N, int64_t K, const float *bias_or_null, int32_t accumulate,
+                       int32_t out_dtype, void *out, int64_t ldo, void *stream);
+
+/* Log probabilities at a temperature T > 0: with u = z / T and lse = log sum_v e^(u_v),
+ *   logprob = u_token - lse,  entropy = -sum_v e^(u_v - lse) (u_v - lse),
+ * and the `top` largest entries in descending order, equal ones in the order of their index
+ * (NaN before everything), with their log probabilities.  A token outside [0, vocab) has
+ * logprob 0.  Entries of -inf have probability 0; a row of nothing else has log probabilities
+ * -inf and entropy 0.  A NaN or +inf makes the row's numbers NaN.
+ *   logits  rows x vocab of `dtype`, row stride ld;  tokens  rows int64
+ *   logprob, entropy  rows fp32;  top in [0, min(128, vocab)]
+ *   top_ids rows x top int32, top_logprobs rows x top fp32 (NULL where top = 0) */
+gq_status gq_token_logprobs(gq_ctx *ctx, const void *logits, int32_t dtype, int64_t rows,
+                            int64_t vocab, int64_t ld, const int64_t *tokens, float temperature,
+                            int32_t top, float *logprob, float *entropy, int32_t *top_ids,
+                            float *top_logprobs, void *stream);
+
+/* Distillation from a teacher's top log probabilities (gq_token_logprobs' top_ids and
+ * top_logprobs at the same temperature T).  With q = softmax(z / T) and p_j = e^(top_logprobs_j)
+ * over the row's taught entries S (ids in [0, vocab); one that occurs again counts once, others
+ * are padding):
+ *   tail = 0: p is divided by its sum;            loss = T^2 sum_S p_j (log p_j - log q_j)
+ *   tail = 1: the rest is one entry with p_R = max(0, 1 - sum_S p_j), q_R = sum over the rest:
+ *             loss = T^2 (sum_S p_j (log p_j - log q_j) + p_R (log p_R - log q_R))
+ * (p_R counts as 0 where S is the whole vocabulary, and below 2^-16 where q_R = 0).  A row that
+ * is taught nothing has loss 0 and gradient 0.
+ * The gradient of sum_rows w_row loss_row is w T (q_v - p_v) in S and w T q_v (1 - p_R / q_R)
+ * elsewhere; with dlogits it is written in the same call.
+ *   logits  rows x vocab of `dtype`, row stride ld;  1 <= top <= 128
+ *   loss    rows fp32;  stats_or_null  rows x 4 fp32, what gq_distill_grad needs
+ *   row_weight_or_null  rows fp32 (NULL: 1);  dlogits_or_null  rows x vocab of `dtype`, row
+ *           stride ldd; it may be `logits` itself (with ldd = ld) */
+gq_status gq_distill_loss(gq_ctx *ctx, const void *logits, int32_t dtype, int64_t rows,
+                          int64_t vocab, int64_t ld, const int32_t *top_ids,
+                          const float *top_logprobs, int32_t top, float temperature,
+                          int32_t tail, const float *row_weight_or_null, float *loss,
+                          float *stats_or_null, void *dlogits_or_null, int64_t ldd,
+                          void *stream);
+
+/* The same gradient from gq_distill_loss' stats, once the rows' weights (the gradient that
+ * arrives for each loss) are known. */
+gq_status gq_distill_grad(gq_ctx *ctx, const void *logits, int32_t dtype, int64_t rows,
+                          int64_t vocab, int64_t ld, const int32_t *top_ids,
+                          const float *top_logprobs, int32_t top, float temperature,
+                          int32_t tail, const float *stats, const float *row_weight_or_null,
+                          void *dlogits, int64_t ldd, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
