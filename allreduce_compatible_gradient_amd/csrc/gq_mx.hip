@@ -113,6 +113,14 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
   return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Two fp32 rounded to bf16 (nearest even) in one word, the first in its low half.
+__device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 template <bool STOCH>
 __device__ __forceinline__ uint32_t encode_block(const float (&x)[32], const uint32_t *counters,
                                                  uint32_t key_mix, u32x4 &codes) {
@@ -198,18 +206,68 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const MxDequantArgs a, in
 }
 
 // ---------------------------------------------------------------- products
-// One output element: what there is of bias and of the old value is added in fp32, and the sum
+// Where a product goes: what there is of bias and of the old values is added in fp32, and the sum
 // is rounded once.
-__device__ __forceinline__ void finish_one(const MxMatmulArgs &a, int64_t m, int64_t n, float v) {
-  if (a.bias) v += a.bias[n];
-  const int64_t at = m * a.ldo + n;
-  if (a.out_dtype == 0) {
-    float *o = static_cast<float *>(a.out) + at;
-    *o = a.accumulate ? *o + v : v;
+struct Sink {
+  void *out;
+  const float *bias;
+  int64_t ld, rows, cols;
+  int32_t dtype, accumulate;
+};
+
+__device__ __forceinline__ Sink sink_of(const MxMatmulArgs &a) {
+  return Sink{a.out, a.bias, a.ldo, a.M, a.N, a.out_dtype, a.accumulate};
+}
+
+__device__ __forceinline__ void put_one(const Sink &s, int64_t m, int64_t n, float v) {
+  if (s.bias) v += s.bias[n];
+  const int64_t at = m * s.ld + n;
+  if (s.dtype == 0) {
+    float *o = static_cast<float *>(s.out) + at;
+    *o = s.accumulate ? *o + v : v;
   } else {
-    uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-    if (a.accumulate) v += __uint_as_float((uint32_t)*o << 16);
+    uint16_t *o = static_cast<uint16_t *>(s.out) + at;
+    if (s.accumulate) v += __uint_as_float((uint32_t)*o << 16);
     *o = to_bf16(v);
+  }
+}
+
+// Eight neighbouring elements of a row (16 bytes of bf16, 32 of fp32).
+[[maybe_unused]] __device__ __forceinline__ void put_eight(const Sink &s, int64_t m, int64_t n, f32x4 lo, f32x4 hi) {
+  if (m >= s.rows || n >= s.cols) return;
+  if (n + 8 > s.cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (n + i < s.cols) put_one(s, m, n + i, i < 4 ? lo[i & 3] : hi[i & 3]);
+    return;
+  }
+  if (s.bias) {
+    const f32x4_e4 *b = reinterpret_cast<const f32x4_e4 *>(s.bias + n);
+    lo += b[0];
+    hi += b[1];
+  }
+  const int64_t at = m * s.ld + n;
+  if (s.dtype == 0) {
+    f32x4_e4 *o = reinterpret_cast<f32x4_e4 *>(static_cast<float *>(s.out) + at);
+    if (s.accumulate) {
+      lo += o[0];
+      hi += o[1];
+    }
+    o[0] = lo;
+    o[1] = hi;
+  } else {
+    uint16_t *o = static_cast<uint16_t *>(s.out) + at;
+    if (s.accumulate) {
+      float x[8];
+      load_eight<1>(o, 0, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] += x[i];
+        hi[i] += x[4 + i];
+      }
+    }
+    *reinterpret_cast<u32x4_e2 *>(o) = u32x4{to_bf16_pair(lo[0], lo[1]), to_bf16_pair(lo[2], lo[3]),
+                                             to_bf16_pair(hi[0], hi[1]), to_bf16_pair(hi[2], hi[3])};
   }
 }
 
@@ -342,24 +400,34 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
   }
   __builtin_amdgcn_sched_barrier(0);
   __syncthreads();  // no load into LDS is in flight when the block ends
+  // A wave's 32 rows of an i cross its own part of LDS, so that they leave along n: lane l has
+  // four n of row l mod 32 before, eight neighbouring n afterwards, whole 128-byte lines of bf16
+  // a row where FN = 2.  16-byte chunks are XORed with the row as above.
+  Sink sink = sink_of(a);
+  if (gridDim.y > 1)
+    sink = Sink{a.partial + (int64_t)blockIdx.y * a.M * a.N, nullptr, a.N, a.M, a.N, 0, 0};
+  constexpr int kRow = FN * 32 * 4, kChunks = FN * 8;  // bytes and chunks of a row of fp32
+  static_assert(WM * WN * 32 * kRow <= (BM + BN) * 128, "the waves' rows fit one buffer");
+  uint8_t *own = lds0 + wave * 32 * kRow;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + (wm * FM + i) * 32 + r32;
-    if (m >= a.M) continue;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + (wn * FN + j) * 32 + 8 * q + 4 * half;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) {
-            if (gridDim.y > 1)
-              a.partial[((int64_t)blockIdx.y * a.M + m) * a.N + n + e] = acc[i][j][4 * q + e];
-            else
-              finish_one(a, m, n + e, acc[i][j][4 * q + e]);
-          }
+        const int chunk = (j * 8 + 2 * q + half) ^ (r32 & (kChunks - 1));
+        *reinterpret_cast<f32x4 *>(own + r32 * kRow + chunk * 16) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
       }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < kChunks / 4; ++p) {
+      const int row = p * (128 / kChunks) + lane / (kChunks / 2), c = lane % (kChunks / 2) * 2;
+      const f32x4 lo = *reinterpret_cast<const f32x4 *>(own + row * kRow + ((c ^ (row & (kChunks - 1))) * 16));
+      const f32x4 hi = *reinterpret_cast<const f32x4 *>(own + row * kRow + (((c + 1) ^ (row & (kChunks - 1))) * 16));
+      put_eight(sink, m0 + (wm * FM + i) * 32 + row, n0 + wn * FN * 32 + c * 4, lo, hi);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 #endif
 }
@@ -370,7 +438,7 @@ __global__ __launch_bounds__(256) void k_mx_join(const MxMatmulArgs a, int split
   if (t >= a.M * a.N) return;
   float v = 0.0f;
   for (int i = 0; i < splits; ++i) v += a.partial[(int64_t)i * a.M * a.N + t];
-  finish_one(a, t / a.N, t % a.N, v);
+  put_one(sink_of(a), t / a.N, t % a.N, v);
 }
 
 // Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it, so
@@ -431,7 +499,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx_matmul_few(const MxMatmul
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) v += sums[w][from][e];
     const int64_t m = from & 15, col = n0 + 4 * (from >> 4) + e;
-    if (m < a.M && col < a.N) finish_one(a, m, col, v);
+    if (m < a.M && col < a.N) put_one(sink_of(a), m, col, v);
   }
 }
 
