@@ -280,9 +280,14 @@ __device__ __forceinline__ void put_one(const Sink &s, int64_t m, int64_t n, flo
 // The operands go from memory to LDS without registers (buffer loads with an LDS destination),
 // one K step ahead, in two static buffers: the loop body handles two steps, so that every LDS
 // access names its buffer and waits only for its own loads.  Row r's 16-byte chunk c is kept at
-// chunk c XOR (r mod 8): a wave's reads of one chunk column fall on all banks.  A lane's eight
-// scale bytes of a row and step are loaded to registers, and one permutation puts its four
-// (every second byte) into a word whose bytes the four products of the step select.
+// chunk c XOR key(r), key(r) = (r XOR r / 8 mod 4) mod 8: 16 rows' reads of one chunk column
+// fall on 16 different places of 256 bytes.  A row's scales of two steps are 16 bytes: a thread
+// a row brings them to LDS every second step (read by each wave for itself, 8 bytes of 32
+// different lines an instruction, they cost as much L2 traffic as the codes).  One permutation
+// puts a lane's four scales of a step (every second byte) into a word whose bytes the four
+// products of the step select.
+[[maybe_unused]] __device__ __forceinline__ int swizzle_key(int r) { return (r ^ (r >> 3 & 3)) & 7; }
+
 template <int WM, int WN, int FM, int FN>
 __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a, int pitch,
                                                            int tiles_m, int tiles_n,
@@ -292,6 +297,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
   constexpr int CA = BM * 8 / T, CB = BN * 8 / T;  // 16-byte chunks a thread and step
   __shared__ __align__(1024) uint8_t lds0[(BM + BN) * 128];
   __shared__ __align__(1024) uint8_t lds1[(BM + BN) * 128];
+  __shared__ __align__(1024) uint8_t lds_scales[(BM + BN + T - 1) / T * T * 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -313,25 +319,20 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
                                                      rows_b * pitch, 0x00027000);
   int off_a[CA], off_b[CB];
   {
-    const int row = tid >> 3, chunk = ((tid & 7) ^ (row & 7)) << 4;
+    const int row = tid >> 3, chunk = ((tid & 7) ^ swizzle_key(row)) << 4;  // T / 8 is a multiple of 32
 #pragma unroll
     for (int i = 0; i < CA; ++i) off_a[i] = min(row + i * (T / 8), rows_a - 1) * row_bytes + chunk;
 #pragma unroll
     for (int i = 0; i < CB; ++i) off_b[i] = min(row + i * (T / 8), rows_b - 1) * row_bytes + chunk;
   }
   const int r32 = lane & 31, half = lane >> 5;
-  int soff_a[FM], soff_b[FN], frag[4];
+  int frag[4];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) soff_a[i] = min((wm * FM + i) * 32 + r32, rows_a - 1) * pitch;
-#pragma unroll
-  for (int i = 0; i < FN; ++i) soff_b[i] = min((wn * FN + i) * 32 + r32, rows_b - 1) * pitch;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) frag[j] = r32 * 128 + (((2 * j + half) ^ (r32 & 7)) << 4);
+  for (int j = 0; j < 4; ++j) frag[j] = r32 * 128 + (((2 * j + half) ^ swizzle_key(r32)) << 4);
   const uint32_t mine = half ? 0x07050301u : 0x06040200u;
 
   f32x16 acc[FM][FN] = {};
-  u32x2 sa[FM], sb[FN];
-  int pa[FM], pb[FN];
+  int pa[2][FM], pb[2][FN];             // scales of two steps, ready for the products
   auto issue = [&](uint8_t *lds, int k) {  // loads of step k
 #pragma unroll
     for (int i = 0; i < CA; ++i)
@@ -342,20 +343,41 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rb, (LDS_PTR void *)(lds + BM * 128 + (i * T + wave * 64) * 16), 16, off_b[i], k * 128, 0,
           0);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, soff_a[i], k * 8, 0);
-#pragma unroll
-    for (int i = 0; i < FN; ++i) sb[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, soff_b[i], k * 8, 0);
   };
-  auto arrive = [&]() {  // every wave's loads of the step are in LDS, its reads of the other done
+  // Scales of steps k and k + 1, a thread a row (rows of A, then of B; a wave has only one kind).
+  auto issue_scales = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < (BM + BN + T - 1) / T; ++i) {
+      const int first = i * T + wave * 64, r = first + lane;
+      LDS_PTR void *to = (LDS_PTR void *)(lds_scales + first * 16);
+      if (first < BM)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, to, 16, min(r, rows_a - 1) * pitch, k * 8, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, to, 16, min(r - BM, rows_b - 1) * pitch, k * 8,
+                                                 0, 0);
+    }
+  };
+  auto pick = [&](uint32_t lo, uint32_t hi) { return (int)__builtin_amdgcn_perm(hi, lo, mine); };
+  auto read_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const u32x4 s = *reinterpret_cast<const u32x4 *>(lds_scales + ((wm * FM + i) * 32 + r32) * 16);
+      pa[0][i] = pick(s.x, s.y);
+      pa[1][i] = pick(s.z, s.w);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const u32x4 s =
+          *reinterpret_cast<const u32x4 *>(lds_scales + (BM + (wn * FN + j) * 32 + r32) * 16);
+      pb[0][j] = pick(s.x, s.y);
+      pb[1][j] = pick(s.z, s.w);
+    }
+  };
+  auto arrive = [&]() {  // every wave's loads so far are in LDS, its reads of the other buffer done
     __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < FM; ++i) pa[i] = __builtin_amdgcn_perm(sa[i].y, sa[i].x, mine);
-#pragma unroll
-    for (int i = 0; i < FN; ++i) pb[i] = __builtin_amdgcn_perm(sb[i].y, sb[i].x, mine);
   };
-  auto multiply = [&](const uint8_t *lds) {
+  auto multiply = [&](const uint8_t *lds, const int (&sa)[FM], const int (&sb)[FN]) {
     __builtin_amdgcn_sched_barrier(0);
     const uint8_t *la = lds + wm * FM * 32 * 128, *lb = lds + (BM + wn * FN * 32) * 128;
 #define GQ_MX_STEP(J)                                                                        \
@@ -370,7 +392,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
       const i32x8 x = __builtin_shufflevector(fa[i], fa[i], 0, 1, 2, 3, -1, -1, -1, -1);     \
       const i32x8 y = __builtin_shufflevector(fb[j], fb[j], 0, 1, 2, 3, -1, -1, -1, -1);     \
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], 4, 4, J,  \
-                                                                  pb[j], J, pa[i]);          \
+                                                                  sb[j], J, sa[i]);          \
     }                                                                                        \
   }
     GQ_MX_STEP(0)
@@ -383,20 +405,36 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
   int k = step0;
   if (count & 1) {  // an odd count's first step, so that the loop takes two at a time
     issue(lds1, k);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const u32x2 s = __builtin_amdgcn_raw_buffer_load_b64(
+          rsa, min((wm * FM + i) * 32 + r32, rows_a - 1) * pitch, k * 8, 0);
+      pa[0][i] = pick(s.x, s.y);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const u32x2 s = __builtin_amdgcn_raw_buffer_load_b64(
+          rsb, min((wn * FN + j) * 32 + r32, rows_b - 1) * pitch, k * 8, 0);
+      pb[0][j] = pick(s.x, s.y);
+    }
     arrive();
     issue(lds0, min(k + 1, last));
-    multiply(lds1);
+    if (k < last) issue_scales(k + 1);
+    multiply(lds1, pa[0], pb[0]);
     ++k;
   } else {
     issue(lds0, k);
+    issue_scales(k);
   }
   for (; k <= last; k += 2) {
     arrive();
     issue(lds1, k + 1);
-    multiply(lds0);
+    read_scales();
+    multiply(lds0, pa[0], pb[0]);
     arrive();
-    issue(lds0, min(k + 2, last));  // past the end: the last step again, not multiplied
-    multiply(lds1);
+    issue(lds0, min(k + 2, last));  // past the end: the last steps again, not multiplied
+    issue_scales(min(k + 2, last - 1));
+    multiply(lds1, pa[1], pb[1]);
   }
   __builtin_amdgcn_sched_barrier(0);
   __syncthreads();  // no load into LDS is in flight when the block ends
