@@ -380,20 +380,29 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
   auto multiply = [&](const uint8_t *lds, const int (&sa)[FM], const int (&sb)[FN]) {
     __builtin_amdgcn_sched_barrier(0);
     const uint8_t *la = lds + wm * FM * 32 * 128, *lb = lds + (BM + wn * FN * 32) * 128;
-#define GQ_MX_STEP(J)                                                                        \
-  {                                                                                          \
-    i32x4 fa[FM], fb[FN];                                                                    \
-    _Pragma("unroll") for (int i = 0; i < FM; ++i) fa[i] =                                   \
-        *reinterpret_cast<const i32x4 *>(la + frag[J] + i * 4096);                           \
-    _Pragma("unroll") for (int j = 0; j < FN; ++j) fb[j] =                                   \
-        *reinterpret_cast<const i32x4 *>(lb + frag[J] + j * 4096);                           \
-    _Pragma("unroll") for (int i = 0; i < FM; ++i)                                           \
-        _Pragma("unroll") for (int j = 0; j < FN; ++j) {                                     \
-      const i32x8 x = __builtin_shufflevector(fa[i], fa[i], 0, 1, 2, 3, -1, -1, -1, -1);     \
-      const i32x8 y = __builtin_shufflevector(fb[j], fb[j], 0, 1, 2, 3, -1, -1, -1, -1);     \
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], 4, 4, J,  \
-                                                                  sb[j], J, sa[i]);          \
-    }                                                                                        \
+    i32x4 fa[2][FM], fb[2][FN];
+    auto fetch = [&](int j) {  // operands of products j, one group ahead of them
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        fa[j & 1][i] = *reinterpret_cast<const i32x4 *>(la + frag[j] + i * 4096);
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+        fb[j & 1][i] = *reinterpret_cast<const i32x4 *>(lb + frag[j] + i * 4096);
+    };
+    fetch(0);
+#define GQ_MX_STEP(J)                                                                           \
+  {                                                                                             \
+    if (J < 3) fetch(J + 1);                                                                    \
+    __builtin_amdgcn_sched_barrier(0);                                                          \
+    _Pragma("unroll") for (int i = 0; i < FM; ++i)                                              \
+        _Pragma("unroll") for (int j = 0; j < FN; ++j) {                                        \
+      const i32x4 u = fa[J & 1][i], v = fb[J & 1][j];                                           \
+      const i32x8 x = __builtin_shufflevector(u, u, 0, 1, 2, 3, -1, -1, -1, -1);                \
+      const i32x8 y = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);                \
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], 4, 4, J,     \
+                                                                  sb[j], J, sa[i]);             \
+    }                                                                                           \
+    __builtin_amdgcn_sched_barrier(0);                                                          \
   }
     GQ_MX_STEP(0)
     GQ_MX_STEP(1)
