@@ -57,16 +57,20 @@ __device__ __forceinline__ uint32_t draw(uint32_t counter, uint32_t key_mix) {
   return h ^ (h >> 16);
 }
 
-// Stochastic code of x (|x| * inv <= 6): the grid's spacing is 1/2 below 2, 1 below 4, 2 above;
-// in units of it v has an exact floor and fraction p, and the code goes up if fp32(h) < p * 2^32.
+// Stochastic code of x (|x| * inv <= 6), 254 too large: the grid's spacing is 1/2 below 2, 1 below
+// 4, 2 above, i.e. 2^(e - 1) with e the exponent of max(v, 1).  In units of it v has an exact
+// whole part and fraction p, and the code goes up if fp32(h) < p * 2^32.  Codes are packed by
+// adding shifted words, so the 254s are taken off once a word (kCodeBias).
+constexpr uint32_t kCodeBias = 254u * 0x11111111u;
 __device__ __forceinline__ uint32_t stochastic_code(float x, float inv, uint32_t h) {
   const float v = fabsf(x) * inv;
-  const float unit = v < 2.0f ? 2.0f : v < 4.0f ? 1.0f : 0.5f;
-  const uint32_t first = v < 2.0f ? 0u : v < 4.0f ? 2u : 4u;
-  const float w = v * unit, low = floorf(w);
-  const uint32_t up = (float)h < (w - low) * 4294967296.0f;
-  return ((uint32_t)low + first + up) | ((__float_as_uint(x) >> 28) & 8u);
+  const uint32_t e = __float_as_uint(fmaxf(v, 1.0f)) & 0x7F800000u;
+  const float w = v * __uint_as_float(0x7F800000u - e);
+  const uint32_t up = (float)h < __builtin_amdgcn_fractf(w) * 4294967296.0f;
+  return (uint32_t)w + (e >> 22) + up;
 }
+
+__device__ __forceinline__ uint32_t sign_bit(float x) { return __float_as_uint(x) >> 31; }
 
 // Eight codes of x * inv to nearest, ties to even, saturating at 6.
 __device__ __forceinline__ uint32_t nearest_codes(const float *x, float inv) {
@@ -121,88 +125,298 @@ __device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-template <bool STOCH>
-__device__ __forceinline__ uint32_t encode_block(const float (&x)[32], const uint32_t *counters,
-                                                 uint32_t key_mix, u32x4 &codes) {
+// A whole block to nearest in one lane: its scale byte, its codes.
+__device__ __forceinline__ uint32_t encode_block(const float (&x)[32], i32x4 &codes) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
   if (top >= 0x7F800000u) {
-    codes = u32x4{0, 0, 0, 0};
+    codes = i32x4{0, 0, 0, 0};
     return 255;
   }
-  const int s = scale_byte<STOCH>(top);
+  const int s = scale_byte<false>(top);
   const float inv = inverse_scale(s);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if constexpr (STOCH) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w |= stochastic_code(x[8 * q + j], inv, draw(counters[8 * q + j], key_mix)) << (4 * j);
-      codes[q] = w;
-    } else {
-      codes[q] = nearest_codes(x + 8 * q, inv);
-    }
-  }
+  for (int q = 0; q < 4; ++q) codes[q] = (int)nearest_codes(x + 8 * q, inv);
   return (uint32_t)s;
 }
 
 // ---------------------------------------------------------------- quantisation
-// A thread a block of 32: along a row, or along a column (lanes on neighbouring columns).
-template <int DT, bool STOCH, bool BY_COLS>
-__global__ __launch_bounds__(256) void k_mx_quantize(const MxQuantArgs a, int64_t pitch) {
-  const int64_t lines = BY_COLS ? a.cols : a.rows, length = BY_COLS ? a.rows : a.cols;
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= lines * pitch) return;
-  const int64_t line = BY_COLS ? t % lines : t / pitch, blk = BY_COLS ? t / lines : t % pitch;
-  const int64_t first = blk * kMxBlock;
-  const int64_t step = BY_COLS ? a.ld : 1;
-  const int64_t base = BY_COLS ? first * a.ld + line : line * a.ld + first;
-  const int64_t cnt = length - first;
-  float x[32];
-  uint32_t counter[32];
+// Largest over the lane's neighbours: quads, then 16 lanes (a block's lanes in the two kernels).
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));  // [1,0,3,2]
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));  // [2,3,0,1]
+}
+
+// Four values at a time: a step of one needs two cycles' distance from its last.
+__device__ __forceinline__ void row_max(uint32_t (&v)[4]) {
+#define GQ_DPP_MAX(CTRL)                                                                        \
+  _Pragma("unroll") for (int i = 0; i < 4; ++i) v[i] =                                          \
+      max(v[i], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[i], CTRL, 0xF, 0xF, true));
+  GQ_DPP_MAX(0xB1)   // quad [1,0,3,2]
+  GQ_DPP_MAX(0x4E)   // quad [2,3,0,1]
+  GQ_DPP_MAX(0x141)  // half mirror
+  GQ_DPP_MAX(0x140)  // mirror
+#undef GQ_DPP_MAX
+}
+
+// By rows: a lane holds eight elements (one 16-byte load of bf16), four lanes a block.  Threads
+// run over the words of a packed row, padding included.
+template <int DT, bool STOCH>
+__global__ __launch_bounds__(256) void k_mx_rows(const MxQuantArgs a, int pitch) {
+  const int64_t row = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
+  const int word = blockIdx.x * blockDim.x + threadIdx.x;
+  if (row >= a.rows || word >= pitch * 4) return;  // whole quads
+  const int64_t first = (int64_t)word * 8;
+  float x[8] = {};
+  if (first + 8 <= a.cols) {
+    load_eight<DT>(a.x, row * a.ld + first, x);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    x[i] = i < cnt ? load_one<DT>(a.x, base + i * step) : 0.0f;
-    counter[i] = a.index_base + (uint32_t)(BY_COLS ? (first + i) * a.cols + line
-                                                   : line * a.cols + first + i);
+    for (int i = 0; i < 8; ++i)
+      if (first + i < a.cols) x[i] = load_one<DT>(a.x, row * a.ld + first + i);
   }
-  u32x4 codes;
-  const uint32_t s = encode_block<STOCH>(x, counter, a.key_mix, codes);
-  uint8_t *out = BY_COLS ? a.codes_t : a.codes, *scales = BY_COLS ? a.scales_t : a.scales;
-  *reinterpret_cast<u32x4 *>(out + (line * pitch + blk) * 16) = codes;
-  scales[line * pitch + blk] = (uint8_t)s;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  top = quad_max(top);
+  const int s = scale_byte<STOCH>(top);
+  const float inv = inverse_scale(s);
+  uint32_t codes = 0;
+  if constexpr (STOCH) {
+    const uint32_t counter = a.index_base + (uint32_t)(row * a.cols + first);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      codes += (stochastic_code(x[i], inv, draw(counter + i, a.key_mix)) << (4 * i)) +
+               (sign_bit(x[i]) << (4 * i + 3));
+    codes -= kCodeBias;
+  } else {
+    codes = nearest_codes(x, inv);
+  }
+  const bool bad = top >= 0x7F800000u;
+  reinterpret_cast<uint32_t *>(a.codes + row * pitch * 16)[word] = bad ? 0u : codes;
+  if ((threadIdx.x & 3) == 0) a.scales[row * pitch + word / 4] = bad ? 255 : (uint8_t)s;
+}
+
+// By columns, or both ways (ROWS) in one read.  A block takes 256 rows x 128 columns, a wave 64
+// rows of it, 32 at a time; a lane holds two neighbouring columns of the 32 rows, so a column's
+// block is a lane's own and a row's block lies in 16 lanes.  The draw of an element is shared by
+// its two codes.  Row codes (a byte a lane and row) and the scales of both ways are gathered in
+// LDS and leave as 16-byte, 4-byte and 8-byte pieces; a column's eight blocks of the 256 rows are
+// one 128-byte line of codes_t, written by one block.
+template <int DT>
+struct Pair;  // two neighbouring elements as loaded
+template <>
+struct Pair<0> {
+  float v[2];
+  __device__ __forceinline__ float get(int i) const { return v[i]; }
+};
+template <>
+struct Pair<1> {
+  uint32_t w;
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i ? w & 0xFFFF0000u : w << 16);
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ Pair<DT> load_pair(const void *p, int i) {
+  if constexpr (DT == 0) {
+    typedef float f32x2_e4 __attribute__((ext_vector_type(2), aligned(4)));
+    const f32x2_e4 v = *reinterpret_cast<const f32x2_e4 *>(static_cast<const float *>(p) + i);
+    return Pair<0>{{v.x, v.y}};
+  } else {
+    typedef uint32_t u32_e2 __attribute__((aligned(2)));
+    return Pair<1>{*reinterpret_cast<const u32_e2 *>(static_cast<const uint16_t *>(p) + i)};
+  }
+}
+
+constexpr int kBothRows = 256, kBothCols = 128;
+template <int DT, bool STOCH, bool ROWS>
+__global__ __launch_bounds__(256, DT == 0 && STOCH && ROWS ? 2 : 3) void k_mx_both(const MxQuantArgs a, int pitch, int pitch_t) {
+  __shared__ __align__(16) uint8_t row_codes[ROWS ? 4 : 1][ROWS ? 32 : 1][80];
+  __shared__ __align__(16) uint8_t row_scales[ROWS ? 4 : 1][ROWS ? 32 : 1][4];
+  __shared__ __align__(16) uint8_t col_scales[kBothCols][8];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t col0 = (int64_t)blockIdx.x * kBothCols, col = col0 + 2 * lane;
+  const bool cols_whole = (int64_t)(blockIdx.x + 1) * kBothCols <= a.cols;
+#pragma unroll 1
+  for (int it = 0; it < 2; ++it) {
+    const int64_t row0 = (int64_t)blockIdx.y * kBothRows + wave * 64 + it * 32;
+    const char *tile = static_cast<const char *>(a.x) + (row0 * a.ld + col0) * (DT == 0 ? 4 : 2);
+    const int64_t step = a.ld * (DT == 0 ? 4 : 2);  // rows are uniform: scalar addresses
+    Pair<DT> x[32];
+    if (cols_whole && row0 + 32 <= a.rows) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r) x[r] = load_pair<DT>(tile + r * step, 2 * lane);
+    } else {
+#if defined(__HIP_DEVICE_COMPILE__)  // buffer resources are a type of the device only
+      // a resource a row, as long as what is there of it: what is outside loads as 0
+      constexpr int kBytes = DT == 0 ? 4 : 2;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const bool there = row0 + r < a.rows && col0 < a.cols;
+        const auto row = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(there ? tile + r * step : tile), 0, there ? (int)(a.cols - col0) * kBytes : 0, 0x00027000);
+        if constexpr (DT == 0)
+          x[r] = Pair<0>{{__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row, lane * 8, 0, 0)),
+                          __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row, lane * 8 + 4, 0, 0))}};
+        else
+          x[r] = Pair<1>{(uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, lane * 4, 0, 0) |
+                         (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, lane * 4 + 2, 0, 0) << 16};
+      }
+#endif
+    }
+    uint32_t top[2] = {0, 0};
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 4) {
+      uint32_t row_top[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b0 = __float_as_uint(x[r0 + i].get(0)) & 0x7FFFFFFFu;
+        const uint32_t b1 = __float_as_uint(x[r0 + i].get(1)) & 0x7FFFFFFFu;
+        top[0] = max(top[0], b0);
+        top[1] = max(top[1], b1);
+        row_top[i] = max(b0, b1);
+      }
+      if constexpr (ROWS) {
+        row_max(row_top);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + i;
+          const bool bad = row_top[i] >= 0x7F800000u;
+          const int s = scale_byte<STOCH>(row_top[i]);
+          if ((lane & 15) == 0) row_scales[wave][r][lane >> 4] = bad ? 255 : (uint8_t)s;
+          if constexpr (!STOCH) {
+            const float f = inverse_scale(s);
+            const uint32_t two = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[r].get(0) * f, x[r].get(1) * f, 1.0f, 0);
+            row_codes[wave][r][lane] = bad ? 0 : (uint8_t)two;
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // keeps the live rows' temporaries few
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int s0 = scale_byte<STOCH>(top[0]), s1 = scale_byte<STOCH>(top[1]);
+    const float inv[2] = {inverse_scale(s0), inverse_scale(s1)};
+    u32x4 codes[2];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = 8 * q + j;
+        uint32_t h[2] = {0, 0};
+        if constexpr (STOCH) {
+          const uint32_t counter = a.index_base + (uint32_t)((row0 + r) * a.cols + col0);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            h[i] = draw(counter + 2 * lane + i, a.key_mix);
+            w[i] += (stochastic_code(x[r].get(i), inv[i], h[i]) << (4 * j)) +
+                    (sign_bit(x[r].get(i)) << (4 * j + 3));
+          }
+        } else if (j % 2 == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float lo = x[r].get(i) * inv[i], hi = x[r + 1].get(i) * inv[i];
+            if (j == 0) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 0);
+            if (j == 2) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 1);
+            if (j == 4) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 2);
+            if (j == 6) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 3);
+          }
+        }
+        if constexpr (ROWS && STOCH) {
+          const uint32_t s = row_scales[wave][r][lane >> 4];
+          const float f = inverse_scale((int)s);
+          const uint32_t two =
+              stochastic_code(x[r].get(0), f, h[0]) + (stochastic_code(x[r].get(1), f, h[1]) << 4) +
+              (sign_bit(x[r].get(0)) << 3) + (sign_bit(x[r].get(1)) << 7) - 254u * 0x11u;
+          row_codes[wave][r][lane] = s == 255 ? 0 : (uint8_t)two;
+        }
+        if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) codes[i][q] = STOCH ? w[i] - kCodeBias : w[i];
+    }
+    const int64_t blk = row0 / kMxBlock;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool bad = top[i] >= 0x7F800000u;
+      if (bad) codes[i] = u32x4{0, 0, 0, 0};
+      if (col + i < a.cols)
+        *reinterpret_cast<u32x4 *>(a.codes_t + ((col + i) * pitch_t + blk) * 16) = codes[i];
+      col_scales[2 * lane + i][wave * 2 + it] = bad ? 255 : (uint8_t)(i ? s1 : s0);
+    }
+    if constexpr (ROWS) {
+      __builtin_amdgcn_wave_barrier();  // the wave's own part of LDS, in order
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = half * 16 + (lane >> 2);
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(&row_codes[wave][r][(lane & 3) * 16]);
+        if (row0 + r < a.rows)
+          *reinterpret_cast<u32x4 *>(a.codes + ((row0 + r) * pitch + blockIdx.x * 4 + (lane & 3)) * 16) = v;
+      }
+      if (lane < 32 && row0 + lane < a.rows)
+        *reinterpret_cast<uint32_t *>(a.scales + (row0 + lane) * pitch + blockIdx.x * 4) =
+            *reinterpret_cast<const uint32_t *>(row_scales[wave][lane]);
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kBothCols) {
+    const int64_t c = (int64_t)blockIdx.x * kBothCols + threadIdx.x;
+    if (c < a.cols)
+      *reinterpret_cast<u32x2 *>(a.scales_t + c * pitch_t + blockIdx.y * 8) =
+          *reinterpret_cast<const u32x2 *>(col_scales[threadIdx.x]);
+  }
 }
 
 // ---------------------------------------------------------------- decoding
-// A thread eight elements: one word of codes, one scale.  The decoded values are exact in bf16.
+// A thread eight elements: one word of codes, one scale, one 16-byte store of bf16.  The decoded
+// values are exact in bf16.
 template <int DT>
-__global__ __launch_bounds__(256) void k_mx_dequantize(const MxDequantArgs a, int64_t pitch) {
-  const int64_t words = (a.cols + 7) / 8;
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= a.rows * words) return;
-  const int64_t row = t / words, word = t % words;
-  const uint32_t c = reinterpret_cast<const uint32_t *>(a.codes + row * pitch * 16)[word];
-  const float f = scale_value(a.scales[row * pitch + word / 4]);
-  float v[8];
+__global__ __launch_bounds__(256) void k_mx_dequantize(const MxDequantArgs a, int pitch) {
+  const int word = blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t first = (int64_t)word * 8;
+  if (first >= a.cols) return;
+  for (int64_t row = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; row < a.rows;
+       row += (int64_t)gridDim.y * blockDim.y) {
+    const uint32_t c = reinterpret_cast<const uint32_t *>(a.codes + row * pitch * 16)[word];
+    const float f = scale_value(a.scales[row * pitch + word / 4]);
+    float v[8];
+    const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
+    const auto v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+    const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
+    const auto v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t n = c >> (4 * i), mag = n & 7u;
-    const float m = mag < 2 ? 0.5f * mag
-                            : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
-    v[i] = (n & 8u ? -m : m) * f;
-  }
-  const int64_t at = row * a.ld + word * 8;
-  const int64_t cnt = a.cols - word * 8;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < cnt) {
-      if constexpr (DT == 0)
-        static_cast<float *>(a.out)[at + i] = v[i];
-      else
-        static_cast<uint16_t *>(a.out)[at + i] = to_bf16(v[i]);
+    for (int i = 0; i < 2; ++i) {
+      v[i] = v0[i] * f;
+      v[2 + i] = v1[i] * f;
+      v[4 + i] = v2[i] * f;
+      v[6 + i] = v3[i] * f;
     }
+    const int64_t at = row * a.ld + first;
+    if (first + 8 <= a.cols) {
+      if constexpr (DT == 0) {
+        f32x4_e4 *o = reinterpret_cast<f32x4_e4 *>(static_cast<float *>(a.out) + at);
+        o[0] = f32x4{v[0], v[1], v[2], v[3]};
+        o[1] = f32x4{v[4], v[5], v[6], v[7]};
+      } else {
+        *reinterpret_cast<u32x4_e2 *>(static_cast<uint16_t *>(a.out) + at) =
+            u32x4{to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3]), to_bf16_pair(v[4], v[5]),
+                  to_bf16_pair(v[6], v[7])};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (first + i < a.cols) {
+          if constexpr (DT == 0)
+            static_cast<float *>(a.out)[at + i] = v[i];
+          else
+            static_cast<uint16_t *>(a.out)[at + i] = to_bf16(v[i]);
+        }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- products
@@ -528,9 +742,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx_matmul_few(const MxMatmul
             for (int i = 0; i < 32; ++i)
               x[i] = k0 + i < a.K ? load_one<AT>(a.a, r16 * a.lda + k0 + i) : 0.0f;
           }
-          u32x4 c;
-          sa = (int)encode_block<false>(x, nullptr, 0, c);
-          fa = i32x4{(int)c.x, (int)c.y, (int)c.z, (int)c.w};
+          sa = (int)encode_block(x, fa);
         }
       }
       const i32x8 x = __builtin_shufflevector(fa, fa, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -583,15 +795,37 @@ void matmul_tiles(const MxMatmulArgs &a, const MatmulPlan &p, hipStream_t s) {
 
 unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
 
+// Threads over the words of a row, the rest of a block of 256 over rows.
+struct RowGrid {
+  dim3 grid, block;
+};
+RowGrid row_grid(int64_t rows, int64_t words, int64_t most_rows) {
+  const unsigned bx = words > 64 ? 256 : words > 16 ? 64 : 16;
+  const int64_t by = 256 / bx, gy = (rows + by - 1) / by;
+  return RowGrid{dim3((unsigned)((words + bx - 1) / bx), (unsigned)(gy < most_rows ? gy : most_rows)),
+                 dim3(bx, (unsigned)by)};
+}
+
 template <int DT, bool STOCH>
-void quantize_both(const MxQuantArgs &a, hipStream_t s) {
-  if (a.codes) {
-    const int64_t pitch = mx_pitch(a.cols);
-    k_mx_quantize<DT, STOCH, false><<<blocks_of(a.rows * pitch), 256, 0, s>>>(a, pitch);
-  }
-  if (a.codes_t) {
-    const int64_t pitch = mx_pitch(a.rows);
-    k_mx_quantize<DT, STOCH, true><<<blocks_of(a.cols * pitch), 256, 0, s>>>(a, pitch);
+void quantize_of(const MxQuantArgs &a, hipStream_t s) {
+  const int pitch = (int)mx_pitch(a.cols), pitch_t = (int)mx_pitch(a.rows);
+  const dim3 grid((unsigned)(pitch / 4), (unsigned)(pitch_t / 8));
+  if (a.codes && a.codes_t) {
+    k_mx_both<DT, STOCH, true><<<grid, 256, 0, s>>>(a, pitch, pitch_t);
+  } else if (a.codes_t) {
+    k_mx_both<DT, STOCH, false><<<grid, 256, 0, s>>>(a, pitch, pitch_t);
+  } else {
+    MxQuantArgs part = a;  // a grid is at most 65535 blocks high
+    const int64_t most = 65535;
+    for (int64_t r = 0; r < a.rows; r += most) {
+      part.x = static_cast<const char *>(a.x) + r * a.ld * (DT == 0 ? 4 : 2);
+      part.codes = a.codes + r * pitch * 16;
+      part.scales = a.scales + r * pitch;
+      part.rows = a.rows - r < most ? a.rows - r : most;
+      part.index_base = a.index_base + (uint32_t)(r * a.cols);
+      const RowGrid g = row_grid(part.rows, pitch * 4ll, most);
+      k_mx_rows<DT, STOCH><<<g.grid, g.block, 0, s>>>(part, pitch);
+    }
   }
 }
 
@@ -599,19 +833,19 @@ void quantize_both(const MxQuantArgs &a, hipStream_t s) {
 
 hipError_t launch_mx_quantize(const MxQuantArgs &a, int dtype, hipStream_t s) {
   if (dtype == 0)
-    a.stochastic ? quantize_both<0, true>(a, s) : quantize_both<0, false>(a, s);
+    a.stochastic ? quantize_of<0, true>(a, s) : quantize_of<0, false>(a, s);
   else
-    a.stochastic ? quantize_both<1, true>(a, s) : quantize_both<1, false>(a, s);
+    a.stochastic ? quantize_of<1, true>(a, s) : quantize_of<1, false>(a, s);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const MxDequantArgs &a, int out_dtype, hipStream_t s) {
-  const unsigned blocks = blocks_of(a.rows * ((a.cols + 7) / 8));
-  const int64_t pitch = mx_pitch(a.cols);
+  const int pitch = (int)mx_pitch(a.cols);
+  const RowGrid g = row_grid(a.rows, (a.cols + 7) / 8, 65535);
   if (out_dtype == 0)
-    k_mx_dequantize<0><<<blocks, 256, 0, s>>>(a, pitch);
+    k_mx_dequantize<0><<<g.grid, g.block, 0, s>>>(a, pitch);
   else
-    k_mx_dequantize<1><<<blocks, 256, 0, s>>>(a, pitch);
+    k_mx_dequantize<1><<<g.grid, g.block, 0, s>>>(a, pitch);
   return hipGetLastError();
 }
 
