@@ -66,33 +66,60 @@ __device__ __forceinline__ float entry(const Slice &s, int64_t i) {  // entry i 
     return __uint_as_float((uint32_t) static_cast<const uint16_t *>(s.row)[s.first + i] << 16);
 }
 
-// The eight entries at virtual index v (a multiple of 8); what is not there is -inf.
+// Eight entries as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load_chunk(const Slice &s, int v, float *x) {
+struct Chunk {
+  u32x4 w[DT == 0 ? 2 : 1];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (DT == 0)
+      return __uint_as_float(w[i / 4][i % 4]);
+    else
+      return __uint_as_float(i % 2 ? w[0][i / 2] & 0xFFFF0000u : w[0][i / 2] << 16);
+  }
+};
+
+// The chunk at virtual index v (a multiple of 8), all of whose entries exist.
+template <int DT>
+__device__ __forceinline__ Chunk<DT> load_whole(const Slice &s, int v) {
+  const u32x4 *p = reinterpret_cast<const u32x4 *>(
+      static_cast<const char *>(s.row) + (s.first - s.lead + v) * (DT == 0 ? 4 : 2));
+  Chunk<DT> c;
+  c.w[0] = p[0];
+  if constexpr (DT == 0) c.w[1] = p[1];
+  return c;
+}
+
+// Any chunk of the slice; what is not there is -inf.
+template <int DT>
+__device__ __forceinline__ Chunk<DT> load_chunk(const Slice &s, int v) {
   const int at = v - s.lead;
-  if (at >= 0 && at + 8 <= s.count) {
-    if constexpr (DT == 0) {
-      const f32x4_e4 *p =
-          reinterpret_cast<const f32x4_e4 *>(static_cast<const float *>(s.row) + s.first + at);
-      const f32x4 a = p[0], b = p[1];
+  if (at >= 0 && at + 8 <= s.count) return load_whole<DT>(s, v);
+  Chunk<DT> c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = a[i];
-        x[4 + i] = b[i];
-      }
-    } else {
-      const u32x4 a =
-          *reinterpret_cast<const u32x4_e2 *>(static_cast<const uint16_t *>(s.row) + s.first + at);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x =
+        __float_as_uint(at + i >= 0 && at + i < s.count ? entry<DT>(s, at + i) : -INFINITY);
+    if constexpr (DT == 0)
+      c.w[i / 4][i % 4] = x;
+    else if (i % 2 == 0)
+      c.w[0][i / 2] = x >> 16;
+    else
+      c.w[0][i / 2] |= x;
+  }
+  return c;
+}
+
+// A thread's four chunks of sweep g.  Whether they are whole is one question a wave.
+template <int DT>
+__device__ __forceinline__ void load_group(const Slice &s, int g, Chunk<DT> (&c)[4]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int v = g * kSweep + wave * 512;  // the wave's first chunk
+  if (v >= s.lead && v + 3 * kPart + 512 <= s.lead + s.count) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(a[i] << 16);
-        x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-      }
-    }
+    for (int j = 0; j < 4; ++j) c[j] = load_whole<DT>(s, v + j * kPart + lane * 8);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = at + i >= 0 && at + i < s.count ? entry<DT>(s, at + i) : -INFINITY;
+    for (int j = 0; j < 4; ++j) c[j] = load_chunk<DT>(s, v + j * kPart + lane * 8);
   }
 }
 
@@ -121,26 +148,32 @@ __device__ __forceinline__ Stat joined(const Stat &a, const Stat &b, float cl) {
   return Stat{m, x.s + y.s, x.w + y.w};
 }
 
-template <bool W>
-__device__ __forceinline__ void add_group(Stat &a, const float (&x)[32], float gm, float cl) {
-  if (gm > a.m) a = moved(a, gm, cl);
-  const float ref = ref_of(a.m);
+template <int DT, int N>
+__device__ __forceinline__ float max_of(const Chunk<DT> (&c)[N]) {
+  float m = c[0].get(0);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float d = x[i] - ref, e = exp_of(d, cl);
-    a.s += e;
-    if constexpr (W) a.w = fmaf(fmaxf(d, -FLT_MAX), e, a.w);
-  }
-}
-
-__device__ __forceinline__ float group_max(const float (&x)[32]) {
-  float m = x[0];
-#pragma unroll
-  for (int i = 1; i < 32; ++i) m = fmaxf(m, x[i]);
+  for (int i = 1; i < 8 * N; ++i) m = fmaxf(m, c[i / 8].get(i % 8));
   return m;
 }
 
+// Adds chunks whose largest entry is gm.  Two partial sums: half the chain of dependent adds.
+template <bool W, int DT, int N>
+__device__ __forceinline__ void add_group(Stat &a, const Chunk<DT> (&c)[N], float gm, float cl) {
+  if (gm > a.m) a = moved(a, gm, cl);
+  const float ref = ref_of(a.m);
+  float s[2] = {a.s, 0.0f}, w[2] = {a.w, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 8 * N; ++i) {
+    const float d = c[i / 8].get(i % 8) - ref, e = exp_of(d, cl);
+    s[i & 1] += e;
+    if constexpr (W) w[i & 1] = fmaf(fmaxf(d, -FLT_MAX), e, w[i & 1]);
+  }
+  a.s = s[0] + s[1];
+  if constexpr (W) a.w = w[0] + w[1];
+}
+
 // The block's statistic, the same in every thread.  `room` holds one entry a wave.
+template <int T = kThreads>
 __device__ __forceinline__ Stat block_join(Stat a, float cl, Stat *room) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
@@ -151,10 +184,11 @@ __device__ __forceinline__ Stat block_join(Stat a, float cl, Stat *room) {
   if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = a;
   __syncthreads();
   a = room[0];
-  for (int i = 1; i < kThreads / 64; ++i) a = joined(a, room[i], cl);
+  for (int i = 1; i < T / 64; ++i) a = joined(a, room[i], cl);
   return a;
 }
 
+template <int T = kThreads>
 __device__ __forceinline__ double block_sum(double v, double *room) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
@@ -162,7 +196,7 @@ __device__ __forceinline__ double block_sum(double v, double *room) {
   if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
   __syncthreads();
   v = room[0];
-  for (int i = 1; i < kThreads / 64; ++i) v += room[i];
+  for (int i = 1; i < T / 64; ++i) v += room[i];
   return v;
 }
 
@@ -278,13 +312,12 @@ __device__ void top_candidates(const Slice &s, int k, float my_max, bool odd, To
     for (int g = 0; g < sweeps_of(s); ++g) {
       if (order_key(room.group[g * kThreads + tid]) < t) continue;
       for (int j = 0; j < 4; ++j) {
-        float x[8];
         const int v = g * kSweep + j * kPart + tid * 8;
-        load_chunk<DT>(s, v, x);
+        const Chunk<DT> c = load_chunk<DT>(s, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int at = v - s.lead + i;
-          const uint32_t key = order_key(x[i]);
+          const uint32_t key = order_key(c.get(i));
           if (key >= t && at >= 0 && at < s.count) {
             const uint32_t n = atomicAdd(&room.count, 1u);
             if (n < kCandidates) room.cand[n] = full_key(key, (uint32_t)(s.first + at));
@@ -337,14 +370,16 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
   Stat mine = {-INFINITY, 0.0f, 0.0f};
   float my_max = -INFINITY;
   const int sweeps = sweeps_of(s);
+  Chunk<DT> now[4], next[4];
+  load_group<DT>(s, 0, now);
   for (int g = 0; g < sweeps; ++g) {
-    float x[32];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) load_chunk<DT>(s, g * kSweep + j * kPart + tid * 8, x + 8 * j);
-    const float gm = group_max(x);
+    if (g + 1 < sweeps) load_group<DT>(s, g + 1, next);
+    const float gm = max_of(now);
     if constexpr (TOP) room.group[g * kThreads + tid] = gm;
     my_max = fmaxf(my_max, gm);
-    add_group<true>(mine, x, gm, cl);
+    add_group<true>(mine, now, gm, cl);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) now[j] = next[j];
   }
   const Stat all = block_join(mine, cl, stats);
   uint64_t *keys = nullptr;
@@ -435,7 +470,8 @@ struct RowStat {  // what the gradient needs of a row
 };
 
 // Loads the row's ids and e^(lp); returns the sum of the latter, in 64 bits: p_R is 1 less it.
-__device__ __forceinline__ double load_taught(const DistillArgs &a, int64_t row, Taught &t) {
+template <int T = kThreads, typename Room>
+__device__ __forceinline__ double load_taught(const DistillArgs &a, int64_t row, Room &t) {
   const int tid = threadIdx.x;
   __syncthreads();
   if (tid < a.top) t.id[tid] = a.top_ids[row * a.top + tid];
@@ -453,7 +489,7 @@ __device__ __forceinline__ double load_taught(const DistillArgs &a, int64_t row,
     if (!ok) t.id[tid] = -1;
     t.p[tid] = (float)p;
   }
-  return block_sum(p, t.sums);
+  return block_sum<T>(p, t.sums);
 }
 
 __device__ __forceinline__ int place_in(const Slice &s, int64_t id, int *bit) {
@@ -480,12 +516,13 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, 
     __syncthreads();
   }
   Stat mine = {-INFINITY, 0.0f, 0.0f};
+  Chunk<DT> now[4], next[4];
+  load_group<DT>(s, 0, now);
   for (int g = 0; g < sweeps; ++g) {
-    float x[32];
+    if (g + 1 < sweeps) load_group<DT>(s, g + 1, next);
+    if (!TAIL || t.in_group[g * kThreads + tid] == 0) add_group<false>(mine, now, max_of(now), cl);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_chunk<DT>(s, g * kSweep + j * kPart + tid * 8, x + 8 * j);
-    if (TAIL && t.in_group[g * kThreads + tid] != 0) continue;
-    add_group<false>(mine, x, group_max(x), cl);
+    for (int j = 0; j < 4; ++j) now[j] = next[j];
   }
   if constexpr (TAIL) {
     // the group of taught entry j, if no earlier one is in it
@@ -500,14 +537,16 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, 
         }
       if (first) {
         const uint32_t mask = t.in_group[g];
-        float x[32];
+        for (int j = 0; j < 4; ++j) {
+          Chunk<0> c[1];
+          const Chunk<DT> raw =
+              load_chunk<DT>(s, (g / kThreads) * kSweep + j * kPart + (g % kThreads) * 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          load_chunk<DT>(s, (g / kThreads) * kSweep + j * kPart + (g % kThreads) * 8, x + 8 * j);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (mask >> i & 1u) x[i] = -INFINITY;
-        add_group<false>(mine, x, group_max(x), cl);
+          for (int i = 0; i < 8; ++i)
+            c[0].w[i / 4][i % 4] =
+                __float_as_uint(mask >> (8 * j + i) & 1u ? -INFINITY : raw.get(i));
+          add_group<false>(mine, c, max_of(c), cl);
+        }
       }
     }
   }
@@ -517,9 +556,9 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, 
 // Loss and gradient constants of a row from the statistic of R (tail) or of all entries.  The
 // loss is a small difference of logarithms of the same sums, so what follows the stream (128
 // terms at most) is held in 64 bits: an error of R's sum then counts q_R - p_R times only.
-template <int DT, bool TAIL>
+template <int DT, bool TAIL, int T, typename Room>
 __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row, Stat rest,
-                                              double sum_p, Taught &t) {
+                                              double sum_p, Room &t) {
   const int tid = threadIdx.x;
   const float cl = a.inv_t * kLog2e;
   const bool mine = tid < a.top && t.id[tid] >= 0;
@@ -530,13 +569,13 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
     lp = a.top_logprobs[row * a.top + tid];
   }
   float m = rest.m;
-  if constexpr (TAIL) m = block_join(Stat{mine ? fmaxf(x, rest.m) : rest.m, 0.0f, 0.0f}, cl, t.stats).m;
+  if constexpr (TAIL) m = block_join<T>(Stat{mine ? fmaxf(x, rest.m) : rest.m, 0.0f, 0.0f}, cl, t.stats).m;
   const float ref = ref_of(m);
   const double inv_t = 1.0 / (double)a.temperature;
   const double rest_s =
       rest.s == 0.0f ? 0.0 : (double)rest.s * exp(((double)ref_of(rest.m) - ref) * inv_t);
   double all_s = rest_s;
-  if constexpr (TAIL) all_s += block_sum(mine ? (double)exp_of(x - ref, cl) : 0.0, t.sums);
+  if constexpr (TAIL) all_s += block_sum<T>(mine ? (double)exp_of(x - ref, cl) : 0.0, t.sums);
   const double log_s = log(all_s);
   double p_rest = TAIL ? fmax(1.0 - sum_p, 0.0) : 0.0;
   const double scale = TAIL ? 1.0 : 1.0 / sum_p;
@@ -547,8 +586,8 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
         x == -INFINITY && all_s == all_s ? -INFINITY : ((double)x - ref) * inv_t - log_s;
     term = exp(log_p) * (log_p - log_q);
   }
-  double loss = block_sum(term, t.sums);
-  const double taught = block_sum(mine ? 1.0 : 0.0, t.sums);
+  double loss = block_sum<T>(term, t.sums);
+  const double taught = block_sum<T>(mine ? 1.0 : 0.0, t.sums);
   // a row masked everywhere has q = 0, not 0 / 0
   RowStat r = {ref, all_s == 0.0 ? 1.0f : (float)(1.0 / all_s), 1.0f, (float)scale};
   // no entry is left for the rest, or the student has none there and p_R is the sum's rounding
@@ -581,42 +620,111 @@ __device__ __forceinline__ void put_grad(const DistillArgs &a, int64_t at, float
     static_cast<uint16_t *>(a.grad)[at] = to_bf16(v);
 }
 
-// The gradient of the slice's entries: all of them as entries of R, then the taught ones.
-template <int DT>
-__device__ __forceinline__ void grad_slice(const DistillArgs &a, int64_t row, const Slice &s,
-                                           const RowStat &r, const Taught &t) {
-  const int tid = threadIdx.x;
-  const float cl = a.inv_t * kLog2e;
-  const float w = (a.weight ? a.weight[row] : 1.0f) * a.temperature;
-  const bool taught = r.inv_s != 0.0f;
-  const float f = w * r.rest * r.inv_s;
-  const int64_t out = row * a.ldg + s.first;
-  // this thread's taught entry, read before the stream: the gradient may replace the logits
-  const bool mine = tid < a.top && t.id[tid] >= s.first && t.id[tid] < s.first + s.count;
-  const float mine_x = mine ? entry<DT>(s, t.id[tid] - s.first) : 0.0f;
-  __syncthreads();
-  const int parts = (s.lead + s.count + kPart - 1) / kPart;
-  for (int g = 0; g < parts; ++g) {
-    const int v = g * kPart + tid * 8, at = v - s.lead;
-    float x[8];
-    load_chunk<DT>(s, v, x);
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// What a row's entries outside S get: f e^(c (z - ref)).
+struct RowGrad {
+  float f, ref, cl;
+  bool plain;  // f is finite; else an entry without probability must not become 0 times it
+};
+
+__device__ __forceinline__ float row_weight(const DistillArgs &a, int64_t row) {
+  return (a.weight ? a.weight[row] : 1.0f) * a.temperature;
+}
+
+__device__ __forceinline__ RowGrad row_grad(const DistillArgs &a, const RowStat &r, float w) {
+  const float f = r.inv_s == 0.0f ? 0.0f : w * r.rest * r.inv_s;
+  return RowGrad{f, r.inv_s == 0.0f ? 0.0f : r.ref, a.inv_t * kLog2e, r.inv_s != 0.0f && fabsf(f) < INFINITY};
+}
+
+// Gradient of the chunk whose first entry is entry `at` of the slice; out: the row's gradient.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void put_chunk(const DistillArgs &a, int64_t out, const Slice &s, int at,
+                                          const Chunk<DT> &c, const RowGrad &g) {
+  float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float e = exp_of(x[i] - r.ref, cl);
-      x[i] = !taught || e == 0.0f ? 0.0f : f * e;
+  for (int i = 0; i < 8; ++i) {
+    const float e = exp_of(c.get(i) - g.ref, g.cl);
+    y[i] = g.f * e;
+    if (!g.plain && (g.f == 0.0f || e == 0.0f)) y[i] = 0.0f;
+  }
+  if constexpr (WHOLE) {
+    if constexpr (DT == 0) {
+      f32x4_e4 *o = reinterpret_cast<f32x4_e4 *>(static_cast<float *>(a.grad) + out + at);
+      o[0] = f32x4{y[0], y[1], y[2], y[3]};
+      o[1] = f32x4{y[4], y[5], y[6], y[7]};
+    } else {
+      *reinterpret_cast<u32x4_e2 *>(static_cast<uint16_t *>(a.grad) + out + at) =
+          u32x4{to_bf16_pair(y[0], y[1]), to_bf16_pair(y[2], y[3]), to_bf16_pair(y[4], y[5]),
+                to_bf16_pair(y[6], y[7])};
     }
+  } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (at + i >= 0 && at + i < s.count) put_grad<DT>(a, out + at + i, x[i]);
-  }
-  __syncthreads();  // the taught entries are written over what the stream put there
-  if (mine) {
-    const float q = exp_of(mine_x - r.ref, cl) * r.inv_s;
-    put_grad<DT>(a, row * a.ldg + t.id[tid], taught ? w * (q - t.p[tid] * r.scale) : 0.0f);
+      if (at + i >= 0 && at + i < s.count) put_grad<DT>(a, out + at + i, y[i]);
   }
 }
 
-// A block a row: the loss, and the gradient where it is asked for.
+// The taught entry of this thread, if the slice has it: read before the row's gradient is
+// written (which may replace the logits), written after it.
+struct TaughtEntry {
+  bool mine;
+  int32_t id;
+  float x, p;
+};
+
+template <int DT, typename Room>
+__device__ __forceinline__ TaughtEntry taught_entry(const DistillArgs &a, const Slice &s, const Room &t) {
+  TaughtEntry e = {false, -1, 0.0f, 0.0f};
+  if ((int)threadIdx.x < a.top) {
+    e.id = t.id[threadIdx.x];
+    e.p = t.p[threadIdx.x];
+    e.mine = e.id >= s.first && e.id < s.first + s.count;
+    if (e.mine) e.x = entry<DT>(s, e.id - s.first);
+  }
+  return e;
+}
+
+template <int DT>
+__device__ __forceinline__ void put_taught(const DistillArgs &a, int64_t row, const TaughtEntry &e,
+                                           const RowStat &r, float w) {
+  if (!e.mine) return;
+  const float q = exp_of(e.x - r.ref, a.inv_t * kLog2e) * r.inv_s;
+  put_grad<DT>(a, row * a.ldg + e.id, r.inv_s == 0.0f ? 0.0f : w * (q - e.p * r.scale));
+}
+
+// A block a row: the loss, and the gradient where it is asked for, from a second read of the row
+// (which the Infinity Cache still holds: the rows in flight are some 100 MB).
+template <int DT>
+__device__ __forceinline__ void grad_stream(const DistillArgs &a, int64_t row, const Slice &s,
+                                            const RowStat &r, const Taught &t) {
+  const TaughtEntry mine = taught_entry<DT>(a, s, t);
+  __syncthreads();
+  const float w = row_weight(a, row);
+  const RowGrad g = row_grad(a, r, w);
+  const int sweeps = sweeps_of(s);
+  Chunk<DT> now[4], next[4];
+  load_group<DT>(s, 0, now);
+  for (int i = 0; i < sweeps; ++i) {
+    if (i + 1 < sweeps) load_group<DT>(s, i + 1, next);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = i * kSweep + j * kPart + (int)threadIdx.x * 8 - s.lead;
+      if (at >= 0 && at + 8 <= s.count)
+        put_chunk<DT, true>(a, row * a.ldg + s.first, s, at, now[j], g);
+      else
+        put_chunk<DT, false>(a, row * a.ldg + s.first, s, at, now[j], g);
+      now[j] = next[j];
+    }
+  }
+  __syncthreads();
+  put_taught<DT>(a, row, mine, r, w);
+}
+
 template <int DT, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_rows(const DistillArgs a) {
   __shared__ Taught t;
@@ -624,8 +732,8 @@ __global__ __launch_bounds__(kThreads) void k_distill_rows(const DistillArgs a) 
   const double sum_p = load_taught(a, row, t);
   const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, 0, a.vocab);
   const Stat rest = rest_stat<DT, TAIL>(a, s, t);
-  const RowStat r = finish_row<DT, TAIL>(a, row, rest, sum_p, t);
-  if (a.grad) grad_slice<DT>(a, row, s, r, t);
+  const RowStat r = finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t);
+  if (a.grad) grad_stream<DT>(a, row, s, r, t);
 }
 
 // A block a slice: the slice's statistic.
@@ -649,7 +757,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, 
   const Stat *in = static_cast<const Stat *>(a.scratch) + row * slices;
   Stat rest = in[0];
   for (int i = 1; i < slices; ++i) rest = joined(rest, in[i], a.inv_t * kLog2e);
-  finish_row<DT, TAIL>(a, row, rest, sum_p, t);
+  finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t);
 }
 
 // A block a slice: the gradient from the rows' constants.
@@ -660,8 +768,8 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
   const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
   load_taught(a, row, t);
   const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
-  const f32x4 r = reinterpret_cast<const f32x4 *>(a.stats)[row];
-  grad_slice<DT>(a, row, s, RowStat{r.x, r.y, r.z, r.w}, t);
+  const f32x4 q = reinterpret_cast<const f32x4 *>(a.stats)[row];
+  grad_stream<DT>(a, row, s, RowStat{q.x, q.y, q.z, q.w}, t);
 }
 
 // Slices of a row: as many as fill the GPU, at least 2048 entries each, at most kSlice.
