@@ -109,18 +109,22 @@ __device__ __forceinline__ Chunk<DT> load_chunk(const Slice &s, int v) {
   return c;
 }
 
-// A thread's four chunks of sweep g.  Whether they are whole is one question a wave.
+// A thread's four chunks of sweep g; returns how many of them its wave has anything of.  Whether
+// they are whole is one question a wave.
 template <int DT>
-__device__ __forceinline__ void load_group(const Slice &s, int g, Chunk<DT> (&c)[4]) {
+__device__ __forceinline__ int load_group(const Slice &s, int g, Chunk<DT> (&c)[4]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int v = g * kSweep + wave * 512;  // the wave's first chunk
-  if (v >= s.lead && v + 3 * kPart + 512 <= s.lead + s.count) {
+  const int v = g * kSweep + wave * 512, end = s.lead + s.count;  // the wave's first chunk
+  if (v >= s.lead && v + 3 * kPart + 512 <= end) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = load_whole<DT>(s, v + j * kPart + lane * 8);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = load_chunk<DT>(s, v + j * kPart + lane * 8);
+    return 4;
   }
+  const int there = v >= end ? 0 : min((end - v + kPart - 1) / kPart, 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < there) c[j] = load_chunk<DT>(s, v + j * kPart + lane * 8);
+  return there;
 }
 
 // ---------------------------------------------------------------- softmax statistics
@@ -158,7 +162,7 @@ __device__ __forceinline__ float max_of(const Chunk<DT> (&c)[N]) {
 
 // Adds chunks whose largest entry is gm.  Two partial sums: half the chain of dependent adds.
 template <bool W, int DT, int N>
-__device__ __forceinline__ void add_group(Stat &a, const Chunk<DT> (&c)[N], float gm, float cl) {
+__device__ __forceinline__ void add_chunks(Stat &a, const Chunk<DT> (&c)[N], float gm, float cl) {
   if (gm > a.m) a = moved(a, gm, cl);
   const float ref = ref_of(a.m);
   float s[2] = {a.s, 0.0f}, w[2] = {a.w, 0.0f};
@@ -172,19 +176,62 @@ __device__ __forceinline__ void add_group(Stat &a, const Chunk<DT> (&c)[N], floa
   if constexpr (W) a.w = w[0] + w[1];
 }
 
-// The block's statistic, the same in every thread.  `room` holds one entry a wave.
-template <int T = kThreads>
+// Adds the `there` chunks of a group; returns their largest entry.
+template <bool W, int DT>
+__device__ __forceinline__ float add_group(Stat &a, const Chunk<DT> (&c)[4], int there, float cl) {
+  if (there == 4) {
+    const float gm = max_of(c);
+    add_chunks<W>(a, c, gm, cl);
+    return gm;
+  }
+  float gm = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= there) break;
+    const Chunk<DT> one[1] = {c[j]};
+    const float m = max_of(one);
+    add_chunks<W>(a, one, m, cl);
+    gm = fmaxf(gm, m);
+  }
+  return gm;
+}
+
+// The block's statistic, the same in every thread: the maximum first, then every thread's sums at
+// it, added in one order.  `room` holds one entry a wave.
+template <int T>
+__device__ __forceinline__ float block_max(float m, Stat *room) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6].m = m;
+  __syncthreads();
+  m = room[threadIdx.x % (T / 64)].m;
+#pragma unroll
+  for (int d = T / 128; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  return m;
+}
+
+template <bool W, int T = kThreads>
 __device__ __forceinline__ Stat block_join(Stat a, float cl, Stat *room) {
+  a = moved(a, block_max<T>(a.m, room), cl);
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
-    const Stat b = {__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.w, d)};
-    a = joined(a, b, cl);
+    a.s += __shfl_xor(a.s, d);
+    if constexpr (W) a.w += __shfl_xor(a.w, d);
+  }
+  // only the sums: another wave may still be reading the maxima
+  if ((threadIdx.x & 63) == 0) {
+    room[threadIdx.x >> 6].s = a.s;
+    room[threadIdx.x >> 6].w = a.w;
   }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = a;
-  __syncthreads();
-  a = room[0];
-  for (int i = 1; i < T / 64; ++i) a = joined(a, room[i], cl);
+  a.s = room[threadIdx.x % (T / 64)].s;
+  a.w = room[threadIdx.x % (T / 64)].w;
+#pragma unroll
+  for (int d = T / 128; d >= 1; d >>= 1) {
+    a.s += __shfl_xor(a.s, d);
+    if constexpr (W) a.w += __shfl_xor(a.w, d);
+  }
   return a;
 }
 
@@ -195,8 +242,9 @@ __device__ __forceinline__ double block_sum(double v, double *room) {
   __syncthreads();
   if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = room[0];
-  for (int i = 1; i < T / 64; ++i) v += room[i];
+  v = room[threadIdx.x % (T / 64)];
+#pragma unroll
+  for (int d = T / 128; d >= 1; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
 
@@ -221,7 +269,8 @@ struct TopRoom {
   uint32_t thread_max[kThreads];
   uint64_t cand[kCandidates];
   uint32_t hist[256];
-  uint32_t count, prefix, need;
+  uint16_t hits[kCandidates];        // groups with an entry at or above the threshold
+  uint32_t count, groups, prefix, need;
 };
 
 // Threshold t with at least k threads' maxima at or above it (0: fewer threads have an entry):
@@ -305,29 +354,32 @@ template <int DT>
 __device__ void top_candidates(const Slice &s, int k, float my_max, bool odd, TopRoom &room) {
   const int tid = threadIdx.x;
   room.thread_max[tid] = order_key(my_max);
-  if (tid == 0) room.count = 0;
+  if (tid == 0) room.count = room.groups = 0;
   __syncthreads();
   if (!odd) {  // no NaN
-    const uint32_t t = top_threshold(room, k);
-    for (int g = 0; g < sweeps_of(s); ++g) {
-      if (order_key(room.group[g * kThreads + tid]) < t) continue;
-      for (int j = 0; j < 4; ++j) {
-        const int v = g * kSweep + j * kPart + tid * 8;
-        const Chunk<DT> c = load_chunk<DT>(s, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = v - s.lead + i;
-          const uint32_t key = order_key(c.get(i));
-          if (key >= t && at >= 0 && at < s.count) {
-            const uint32_t n = atomicAdd(&room.count, 1u);
-            if (n < kCandidates) room.cand[n] = full_key(key, (uint32_t)(s.first + at));
-          }
-        }
+    // as a value: what is not below it is taken
+    const float t = key_value(max(top_threshold(room, k), order_key(-INFINITY)));
+    for (int g = 0; g < sweeps_of(s); ++g)
+      if (room.group[g * kThreads + tid] >= t) {
+        const uint32_t n = atomicAdd(&room.groups, 1u);
+        if (n < kCandidates) room.hits[n] = (uint16_t)(g * kThreads + tid);
       }
+    __syncthreads();
+    // a lane an entry of those groups: they are few, and a thread's own 32 would be read in turn
+    const int entries = (int)min(room.groups, (uint32_t)kCandidates) * 32;
+    for (int i = tid; i < entries; i += kThreads) {
+      const int g = room.hits[i >> 5], e = i & 31;
+      const int at =
+          g / kThreads * kSweep + e / 8 * kPart + g % kThreads * 8 + (e & 7) - s.lead;
+      if (at < 0 || at >= s.count) continue;
+      const float x = entry<DT>(s, at);
+      if (!(x >= t)) continue;
+      const uint32_t n = atomicAdd(&room.count, 1u);
+      if (n < kCandidates) room.cand[n] = full_key(order_key(x), (uint32_t)(s.first + at));
     }
   }
   __syncthreads();
-  if (odd || room.count > kCandidates) {
+  if (odd || room.groups > kCandidates || room.count > kCandidates) {
     __syncthreads();
     top_by_digits<DT>(s, min(k, s.count), room);
   }
@@ -371,17 +423,17 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
   float my_max = -INFINITY;
   const int sweeps = sweeps_of(s);
   Chunk<DT> now[4], next[4];
-  load_group<DT>(s, 0, now);
+  int there = load_group<DT>(s, 0, now), there_next = 0;
   for (int g = 0; g < sweeps; ++g) {
-    if (g + 1 < sweeps) load_group<DT>(s, g + 1, next);
-    const float gm = max_of(now);
+    if (g + 1 < sweeps) there_next = load_group<DT>(s, g + 1, next);
+    const float gm = add_group<true>(mine, now, there, cl);
     if constexpr (TOP) room.group[g * kThreads + tid] = gm;
     my_max = fmaxf(my_max, gm);
-    add_group<true>(mine, now, gm, cl);
 #pragma unroll
     for (int j = 0; j < 4; ++j) now[j] = next[j];
+    there = there_next;
   }
-  const Stat all = block_join(mine, cl, stats);
+  const Stat all = block_join<true>(mine, cl, stats);
   uint64_t *keys = nullptr;
   if (slices > 1) {
     Stat *out = static_cast<Stat *>(a.scratch);
@@ -517,12 +569,13 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, 
   }
   Stat mine = {-INFINITY, 0.0f, 0.0f};
   Chunk<DT> now[4], next[4];
-  load_group<DT>(s, 0, now);
+  int there = load_group<DT>(s, 0, now), there_next = 0;
   for (int g = 0; g < sweeps; ++g) {
-    if (g + 1 < sweeps) load_group<DT>(s, g + 1, next);
-    if (!TAIL || t.in_group[g * kThreads + tid] == 0) add_group<false>(mine, now, max_of(now), cl);
+    if (g + 1 < sweeps) there_next = load_group<DT>(s, g + 1, next);
+    if (!TAIL || t.in_group[g * kThreads + tid] == 0) add_group<false>(mine, now, there, cl);
 #pragma unroll
     for (int j = 0; j < 4; ++j) now[j] = next[j];
+    there = there_next;
   }
   if constexpr (TAIL) {
     // the group of taught entry j, if no earlier one is in it
@@ -545,12 +598,12 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, 
           for (int i = 0; i < 8; ++i)
             c[0].w[i / 4][i % 4] =
                 __float_as_uint(mask >> (8 * j + i) & 1u ? -INFINITY : raw.get(i));
-          add_group<false>(mine, c, max_of(c), cl);
+          add_chunks<false>(mine, c, max_of(c), cl);
         }
       }
     }
   }
-  return block_join(mine, cl, t.stats);
+  return block_join<false>(mine, cl, t.stats);
 }
 
 // Loss and gradient constants of a row from the statistic of R (tail) or of all entries.  The
@@ -569,7 +622,7 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
     lp = a.top_logprobs[row * a.top + tid];
   }
   float m = rest.m;
-  if constexpr (TAIL) m = block_join<T>(Stat{mine ? fmaxf(x, rest.m) : rest.m, 0.0f, 0.0f}, cl, t.stats).m;
+  if constexpr (TAIL) m = block_max<T>(mine ? fmaxf(x, rest.m) : rest.m, t.stats);
   const float ref = ref_of(m);
   const double inv_t = 1.0 / (double)a.temperature;
   const double rest_s =
@@ -708,32 +761,132 @@ __device__ __forceinline__ void grad_stream(const DistillArgs &a, int64_t row, c
   const RowGrad g = row_grad(a, r, w);
   const int sweeps = sweeps_of(s);
   Chunk<DT> now[4], next[4];
-  load_group<DT>(s, 0, now);
+  int there = load_group<DT>(s, 0, now), there_next = 0;
   for (int i = 0; i < sweeps; ++i) {
-    if (i + 1 < sweeps) load_group<DT>(s, i + 1, next);
+    if (i + 1 < sweeps) there_next = load_group<DT>(s, i + 1, next);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = i * kSweep + j * kPart + (int)threadIdx.x * 8 - s.lead;
-      if (at >= 0 && at + 8 <= s.count)
-        put_chunk<DT, true>(a, row * a.ldg + s.first, s, at, now[j], g);
-      else
-        put_chunk<DT, false>(a, row * a.ldg + s.first, s, at, now[j], g);
+      if (j < there) {
+        if (at >= 0 && at + 8 <= s.count)
+          put_chunk<DT, true>(a, row * a.ldg + s.first, s, at, now[j], g);
+        else
+          put_chunk<DT, false>(a, row * a.ldg + s.first, s, at, now[j], g);
+      }
       now[j] = next[j];
     }
+    there = there_next;
   }
   __syncthreads();
   put_taught<DT>(a, row, mine, r, w);
 }
 
-template <int DT, bool TAIL>
-__global__ __launch_bounds__(kThreads) void k_distill_rows(const DistillArgs a) {
-  __shared__ Taught t;
+// A block a row that its registers hold (T threads, N chunks each, counted from the row's first
+// element): all of it in flight at once, read once, there for the largest entry, the sum and the
+// gradient.  The chunk that a row's end may cut is one more of thread 64.
+template <int T, int N>
+struct RowRoom {
+  int32_t id[kVocabTop];
+  float p[kVocabTop];
+  double sums[T / 64];
+  Stat stats[T / 64];
+  uint8_t in_chunk[N * T + 4];  // taught entries of each chunk
+};
+
+template <int DT, bool TAIL, int T, int N>
+__global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
+  __shared__ __align__(16) RowRoom<T, N> t;
+  constexpr uint32_t kNone = DT == 0 ? 0xFF800000u : 0xFF80FF80u;
+  constexpr int kElem = DT == 0 ? 4 : 2;
+  const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
-  const double sum_p = load_taught(a, row, t);
-  const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, 0, a.vocab);
-  const Stat rest = rest_stat<DT, TAIL>(a, s, t);
-  const RowStat r = finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t);
-  if (a.grad) grad_stream<DT>(a, row, s, r, t);
+  Slice s = slice_of(a.logits, kElem, row, a.ld, a.vocab, 0, a.vocab);
+  s.lead = 0;
+  const float cl = a.inv_t * kLog2e;
+  Chunk<DT> c[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+#pragma unroll
+    for (auto &w : c[j].w) w = u32x4{kNone, kNone, kNone, kNone};
+    if ((j * T + tid) * 8 + 8 <= s.count) {
+      const u32x4_e2 *p = reinterpret_cast<const u32x4_e2 *>(
+          static_cast<const char *>(s.row) + j * T * 8 * kElem + (uint32_t)(tid * 8 * kElem));
+      c[j].w[0] = p[0];
+      if constexpr (DT == 0) c[j].w[1] = p[1];
+    }
+  }
+  const bool cut = tid == 64 && (s.count & 7) != 0;
+  const double sum_p = load_taught<T>(a, row, t);
+  if constexpr (TAIL) {
+    uint32_t *zero = reinterpret_cast<uint32_t *>(t.in_chunk);
+    for (int i = tid; i < (N * T + 4) / 4; i += T) zero[i] = 0;
+    __syncthreads();
+    if (tid < a.top && t.id[tid] >= 0)
+      atomicOr(&zero[t.id[tid] >> 5], 1u << (t.id[tid] & 31));  // byte id / 8, bit id mod 8
+    __syncthreads();
+  }
+  // with a tail, taught entries leave the registers: their gradient is written apart
+  auto strip = [&](Chunk<DT> &x, int chunk) {
+    const uint32_t mask = t.in_chunk[chunk];
+    if (mask == 0) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!(mask >> i & 1u)) continue;
+      if constexpr (DT == 0)
+        x.w[i / 4][i % 4] = 0xFF800000u;
+      else
+        x.w[0][i / 2] = i % 2 ? (x.w[0][i / 2] & 0xFFFFu) | 0xFF800000u
+                              : (x.w[0][i / 2] & 0xFFFF0000u) | 0xFF80u;
+    }
+  };
+  auto cut_chunk = [&]() {
+    Chunk<DT> x = load_chunk<DT>(s, s.count & ~7);
+    if constexpr (TAIL) strip(x, s.count >> 3);
+    return x;
+  };
+  if constexpr (TAIL) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) strip(c[j], j * T + tid);
+  }
+  // Keeps the entries as they were loaded: kept widened from one use to the next, bf16 would take
+  // twice the registers.
+  auto repack = [&]() {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (auto &w : c[j].w) asm volatile("" : "+v"(w));
+  };
+  float m = max_of(c);
+  repack();
+  if (cut) {
+    const Chunk<DT> x[1] = {cut_chunk()};
+    m = fmaxf(m, max_of(x));
+  }
+  m = block_max<T>(m == m ? m : -INFINITY, t.stats);
+  const float ref = ref_of(m);
+  float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 8 * N; ++i) sum[i & 1] += exp_of(c[i / 8].get(i % 8) - ref, cl);
+  repack();
+  if (cut) {
+    const Chunk<DT> x = cut_chunk();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i & 1] += exp_of(x.get(i) - ref, cl);
+  }
+  const Stat rest = {m, (float)block_sum<T>((double)(sum[0] + sum[1]), t.sums), 0.0f};
+  const RowStat r = finish_row<DT, TAIL, T>(a, row, rest, sum_p, t);
+  if (!a.grad) return;
+  const TaughtEntry mine = taught_entry<DT>(a, s, t);
+  __syncthreads();
+  const float w = row_weight(a, row);
+  const RowGrad g = row_grad(a, r, w);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if ((j * T + tid) * 8 + 8 <= s.count)
+      put_chunk<DT, true>(a, row * a.ldg, s, (j * T + tid) * 8, c[j], g);
+  if (cut) put_chunk<DT, false>(a, row * a.ldg, s, s.count & ~7, cut_chunk(), g);
+  __syncthreads();
+  put_taught<DT>(a, row, mine, r, w);
 }
 
 // A block a slice: the slice's statistic.
@@ -799,10 +952,24 @@ void distill_grad_of(const DistillArgs &a, int slices, int64_t each, hipStream_t
   k_distill_grad<DT><<<(unsigned)(a.rows * slices), kThreads, 0, s>>>(a, slices, each);
 }
 
+// The longest row that a block's registers hold: 16 chunks of bf16, 8 of fp32 a thread.
+template <int DT>
+constexpr int64_t kRowMax = 1024 * (DT == 0 ? 64 : 128);
+
 template <int DT, bool TAIL>
 void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
-  if (slices == 1) {
-    k_distill_rows<DT, TAIL><<<(unsigned)a.rows, kThreads, 0, s>>>(a);
+  if (slices == 1 && a.vocab < kRowMax<DT>) {
+    const unsigned rows = (unsigned)a.rows;
+    if (a.vocab < 256 * 64)
+      k_distill_row<DT, TAIL, 256, 8><<<rows, 256, 0, s>>>(a);
+    else if (a.vocab < 512 * 64)
+      k_distill_row<DT, TAIL, 512, 8><<<rows, 512, 0, s>>>(a);
+    else if constexpr (DT == 0)
+      k_distill_row<DT, TAIL, 1024, 8><<<rows, 1024, 0, s>>>(a);
+    else if (a.vocab < 512 * 128)
+      k_distill_row<DT, TAIL, 512, 16><<<rows, 512, 0, s>>>(a);
+    else
+      k_distill_row<DT, TAIL, 1024, 16><<<rows, 1024, 0, s>>>(a);
     return;
   }
   DistillArgs b = a;
