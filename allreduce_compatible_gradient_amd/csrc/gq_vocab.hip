@@ -32,6 +32,7 @@ constexpr int kSweep = 4 * kPart;           // elements of one group of every th
 constexpr int kSweeps = 16;                 // groups of a thread in a slice, at most
 constexpr int64_t kSlice = (int64_t)kSweep * kSweeps;
 constexpr int kMaxSlices = 64;
+constexpr int64_t kFill = 1024;             // blocks of a call, where its rows allow slices
 constexpr int kCandidates = 1024;           // entries at or above the threshold, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -146,12 +147,6 @@ __device__ __forceinline__ Stat moved(const Stat &a, float m, float cl) {  // to
   return Stat{m, f * a.s, f == 0.0f ? 0.0f : f * (a.w + d * a.s)};
 }
 
-__device__ __forceinline__ Stat joined(const Stat &a, const Stat &b, float cl) {
-  const float m = fmaxf(a.m, b.m);
-  const Stat x = moved(a, m, cl), y = moved(b, m, cl);
-  return Stat{m, x.s + y.s, x.w + y.w};
-}
-
 template <int DT, int N>
 __device__ __forceinline__ float max_of(const Chunk<DT> (&c)[N]) {
   float m = c[0].get(0);
@@ -233,6 +228,19 @@ __device__ __forceinline__ Stat block_join(Stat a, float cl, Stat *room) {
     if constexpr (W) a.w += __shfl_xor(a.w, d);
   }
   return a;
+}
+
+// A row's slices' statistics, joined: the same in every thread.
+template <bool W>
+__device__ __forceinline__ Stat join_slices(const Stat *in, int slices, float cl, Stat *room) {
+  Stat a = {-INFINITY, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < slices; i += kThreads) {
+    const Stat b = in[i];
+    const float m = fmaxf(a.m, b.m);
+    const Stat x = moved(a, m, cl), y = moved(b, m, cl);
+    a = Stat{m, x.s + y.s, x.w + y.w};
+  }
+  return block_join<W>(a, cl, room);
 }
 
 template <int T = kThreads>
@@ -463,24 +471,56 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
   }
 }
 
-// A block a row: the slices' statistics in their order; an entry's place is the number of larger
-// ones, found in every slice's ordered list by bisection.
+// A block a row: joins the slices.  With d = ceil(top / slices), the ceil(top / d)-th largest of
+// the lists' d-th entries has `top` entries at or above it, so smaller ones are left out.  What is
+// left is gathered in LDS, and an entry's place is the number of larger ones there; where more
+// is left than fits (the largest entries all in a few slices), that number is found in every
+// slice's ordered list by bisection.
+constexpr int kJoinKeys = 512;
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_logprobs_join(const LogprobArgs a, int slices) {
-  const int tid = threadIdx.x;
+  __shared__ Stat stats[kThreads / 64];
+  __shared__ uint64_t near[kJoinKeys];
+  __shared__ int count;
+  const int tid = threadIdx.x, lane = tid & 63, n = slices * a.top;
   const int64_t row = blockIdx.x;
-  const float cl = a.inv_t * kLog2e;
   const Stat *in = static_cast<const Stat *>(a.scratch);
-  const uint64_t *keys =
-      reinterpret_cast<const uint64_t *>(in + ((a.rows * slices + 1) & ~1ll)) + row * slices * a.top;
-  in += row * slices;
-  Stat all = in[0];
-  for (int i = 1; i < slices; ++i) all = joined(all, in[i], cl);
-  if (tid == 0) put_token<DT>(a, row, all);
-  const float ref = ref_of(all.m), log_s = logf(all.s);
-  for (int i = tid; i < slices * a.top; i += kThreads) {
+  const uint64_t *keys = reinterpret_cast<const uint64_t *>(in + ((a.rows * slices + 1) & ~1ll)) + row * n;
+  uint32_t depth_key = 0;
+  const int d = (a.top + slices - 1) / slices;
+  if (a.top > 0 && slices <= 64 && lane < slices) depth_key = (uint32_t)(keys[lane * a.top + d - 1] >> 32);
+  if (tid == 0) count = 0;
+  const Stat all = join_slices<true>(in + row * slices, slices, a.inv_t * kLog2e, stats);
+  if (tid == kThreads - 1) put_token<DT>(a, row, all);
+  if (a.top == 0) return;
+  uint32_t t = 0;
+  const int want = (a.top + d - 1) / d;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = t | 1u << bit;
+    if (__popcll(__ballot(depth_key >= c)) >= want) t = c;
+  }
+  const uint64_t least = t != 0 ? (uint64_t)t << 32 : 1;  // 0 fills a list that is too short
+  for (int i = tid; i < n; i += kThreads) {
     const uint64_t key = keys[i];
-    if (key == 0) continue;
+    if (key < least) continue;
+    const int at = atomicAdd(&count, 1);
+    if (at < kJoinKeys) near[at] = key;
+  }
+  __syncthreads();
+  const float ref = ref_of(all.m), log_s = logf(all.s);
+  const int left = count;
+  if (left <= kJoinKeys) {
+    for (int i = tid; i < left; i += kThreads) {
+      const uint64_t key = near[i];
+      int place = 0;
+      for (int j = 0; j < left; ++j) place += near[j] > key;
+      if (place < a.top) put_top(a, row, place, key, ref, log_s);
+    }
+    return;
+  }
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t key = keys[i];
+    if (key < least) continue;
     int place = 0;
     for (int p = 0; p < slices && place < a.top; ++p) {
       const uint64_t *list = keys + p * a.top;
@@ -695,6 +735,9 @@ __device__ __forceinline__ RowGrad row_grad(const DistillArgs &a, const RowStat 
 }
 
 // Gradient of the chunk whose first entry is entry `at` of the slice; out: the row's gradient.
+// Whole chunks are stored non-temporally: the gradient is not read again here, and past the
+// Infinity Cache it does not push out logits (4096 x 50257 bf16: 222 us with plain stores, 209 us
+// so; 1021 x 131071, loss and gradient apart: 228 and 198 us).
 template <int DT, bool WHOLE>
 __device__ __forceinline__ void put_chunk(const DistillArgs &a, int64_t out, const Slice &s, int at,
                                           const Chunk<DT> &c, const RowGrad &g) {
@@ -708,12 +751,13 @@ __device__ __forceinline__ void put_chunk(const DistillArgs &a, int64_t out, con
   if constexpr (WHOLE) {
     if constexpr (DT == 0) {
       f32x4_e4 *o = reinterpret_cast<f32x4_e4 *>(static_cast<float *>(a.grad) + out + at);
-      o[0] = f32x4{y[0], y[1], y[2], y[3]};
-      o[1] = f32x4{y[4], y[5], y[6], y[7]};
+      __builtin_nontemporal_store(f32x4_e4{y[0], y[1], y[2], y[3]}, o);
+      __builtin_nontemporal_store(f32x4_e4{y[4], y[5], y[6], y[7]}, o + 1);
     } else {
-      *reinterpret_cast<u32x4_e2 *>(static_cast<uint16_t *>(a.grad) + out + at) =
-          u32x4{to_bf16_pair(y[0], y[1]), to_bf16_pair(y[2], y[3]), to_bf16_pair(y[4], y[5]),
-                to_bf16_pair(y[6], y[7])};
+      __builtin_nontemporal_store(
+          u32x4_e2{to_bf16_pair(y[0], y[1]), to_bf16_pair(y[2], y[3]), to_bf16_pair(y[4], y[5]),
+                   to_bf16_pair(y[6], y[7])},
+          reinterpret_cast<u32x4_e2 *>(static_cast<uint16_t *>(a.grad) + out + at));
     }
   } else {
 #pragma unroll
@@ -781,9 +825,10 @@ __device__ __forceinline__ void grad_stream(const DistillArgs &a, int64_t row, c
   put_taught<DT>(a, row, mine, r, w);
 }
 
-// A block a row that its registers hold (T threads, N chunks each, counted from the row's first
-// element): all of it in flight at once, read once, there for the largest entry, the sum and the
-// gradient.  The chunk that a row's end may cut is one more of thread 64.
+// A block a row that its registers hold (T threads, N chunks each): all of it in flight at once,
+// read once, there for the largest entry, the sum and the gradient.  Chunks are counted from the
+// 128-byte line that the row begins in, so that a wave's stores cover whole lines.  The chunks
+// that the row's ends may cut are one more of threads 64 and 128.
 template <int T, int N>
 struct RowRoom {
   int32_t id[kVocabTop];
@@ -801,28 +846,34 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   Slice s = slice_of(a.logits, kElem, row, a.ld, a.vocab, 0, a.vocab);
-  s.lead = 0;
+  s.lead = (int32_t)((reinterpret_cast<uintptr_t>(s.row) & 127) / kElem);
   const float cl = a.inv_t * kLog2e;
+  const int end = s.lead + s.count;
+  const char *lines = static_cast<const char *>(s.row) - s.lead * kElem;
   Chunk<DT> c[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
 #pragma unroll
     for (auto &w : c[j].w) w = u32x4{kNone, kNone, kNone, kNone};
-    if ((j * T + tid) * 8 + 8 <= s.count) {
-      const u32x4_e2 *p = reinterpret_cast<const u32x4_e2 *>(
-          static_cast<const char *>(s.row) + j * T * 8 * kElem + (uint32_t)(tid * 8 * kElem));
+    const int v = (j * T + tid) * 8;
+    if (v >= s.lead && v + 8 <= end) {
+      const u32x4 *p = reinterpret_cast<const u32x4 *>(lines + j * T * 8 * kElem +
+                                                       (uint32_t)(tid * 8 * kElem));
       c[j].w[0] = p[0];
       if constexpr (DT == 0) c[j].w[1] = p[1];
     }
   }
-  const bool cut = tid == 64 && (s.count & 7) != 0;
+  // the chunk of the row's end, and that of its beginning if it is another
+  const bool cut = (tid == 64 && (end & 7) != 0) ||
+                   (tid == 128 && (s.lead & 7) != 0 && ((s.lead ^ end) & ~7) != 0);
+  const int cut_v = (tid == 64 ? end : s.lead) & ~7;
   const double sum_p = load_taught<T>(a, row, t);
   if constexpr (TAIL) {
     uint32_t *zero = reinterpret_cast<uint32_t *>(t.in_chunk);
     for (int i = tid; i < (N * T + 4) / 4; i += T) zero[i] = 0;
     __syncthreads();
     if (tid < a.top && t.id[tid] >= 0)
-      atomicOr(&zero[t.id[tid] >> 5], 1u << (t.id[tid] & 31));  // byte id / 8, bit id mod 8
+      atomicOr(&zero[(t.id[tid] + s.lead) >> 5], 1u << ((t.id[tid] + s.lead) & 31));
     __syncthreads();
   }
   // with a tail, taught entries leave the registers: their gradient is written apart
@@ -840,8 +891,8 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
     }
   };
   auto cut_chunk = [&]() {
-    Chunk<DT> x = load_chunk<DT>(s, s.count & ~7);
-    if constexpr (TAIL) strip(x, s.count >> 3);
+    Chunk<DT> x = load_chunk<DT>(s, cut_v);
+    if constexpr (TAIL) strip(x, cut_v >> 3);
     return x;
   };
   if constexpr (TAIL) {
@@ -881,10 +932,11 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
   const float w = row_weight(a, row);
   const RowGrad g = row_grad(a, r, w);
 #pragma unroll
-  for (int j = 0; j < N; ++j)
-    if ((j * T + tid) * 8 + 8 <= s.count)
-      put_chunk<DT, true>(a, row * a.ldg, s, (j * T + tid) * 8, c[j], g);
-  if (cut) put_chunk<DT, false>(a, row * a.ldg, s, s.count & ~7, cut_chunk(), g);
+  for (int j = 0; j < N; ++j) {
+    const int v = (j * T + tid) * 8;
+    if (v >= s.lead && v + 8 <= end) put_chunk<DT, true>(a, row * a.ldg, s, v - s.lead, c[j], g);
+  }
+  if (cut) put_chunk<DT, false>(a, row * a.ldg, s, cut_v - s.lead, cut_chunk(), g);
   __syncthreads();
   put_taught<DT>(a, row, mine, r, w);
 }
@@ -907,9 +959,8 @@ __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, 
   __shared__ Taught t;
   const int64_t row = blockIdx.x;
   const double sum_p = load_taught(a, row, t);
-  const Stat *in = static_cast<const Stat *>(a.scratch) + row * slices;
-  Stat rest = in[0];
-  for (int i = 1; i < slices; ++i) rest = joined(rest, in[i], a.inv_t * kLog2e);
+  const Stat rest = join_slices<false>(static_cast<const Stat *>(a.scratch) + row * slices, slices,
+                                       a.inv_t * kLog2e, t.stats);
   finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t);
 }
 
@@ -925,9 +976,10 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
   grad_stream<DT>(a, row, s, RowStat{q.x, q.y, q.z, q.w}, t);
 }
 
-// Slices of a row: as many as fill the GPU, at least 2048 entries each, at most kSlice.
-int slices_of(int64_t rows, int64_t vocab, int64_t *each) {
-  int64_t n = 1024 / rows;
+// Slices of a row: as many as fill the GPU a few times over, at least 2048 entries each, at most
+// kSlice.
+int slices_of(int64_t rows, int64_t vocab, int64_t *each, int64_t fill = kFill) {
+  int64_t n = fill / rows;
   if (n > vocab / kPart) n = vocab / kPart;
   if (n > kMaxSlices) n = kMaxSlices;
   const int64_t least = (vocab + kSlice - 9) / (kSlice - 8);
@@ -954,19 +1006,19 @@ void distill_grad_of(const DistillArgs &a, int slices, int64_t each, hipStream_t
 
 // The longest row that a block's registers hold: 16 chunks of bf16, 8 of fp32 a thread.
 template <int DT>
-constexpr int64_t kRowMax = 1024 * (DT == 0 ? 64 : 128);
+constexpr int64_t kRowMax = 1024 * (DT == 0 ? 64 : 128) - 64;
 
 template <int DT, bool TAIL>
 void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
-  if (slices == 1 && a.vocab < kRowMax<DT>) {
+  if (slices == 1 && a.vocab <= kRowMax<DT>) {
     const unsigned rows = (unsigned)a.rows;
-    if (a.vocab < 256 * 64)
+    if (a.vocab <= 256 * 64 - 64)
       k_distill_row<DT, TAIL, 256, 8><<<rows, 256, 0, s>>>(a);
-    else if (a.vocab < 512 * 64)
+    else if (a.vocab <= 512 * 64 - 64)
       k_distill_row<DT, TAIL, 512, 8><<<rows, 512, 0, s>>>(a);
     else if constexpr (DT == 0)
       k_distill_row<DT, TAIL, 1024, 8><<<rows, 1024, 0, s>>>(a);
-    else if (a.vocab < 512 * 128)
+    else if (a.vocab <= 512 * 128 - 64)
       k_distill_row<DT, TAIL, 512, 16><<<rows, 512, 0, s>>>(a);
     else
       k_distill_row<DT, TAIL, 1024, 16><<<rows, 1024, 0, s>>>(a);
@@ -1000,15 +1052,22 @@ hipError_t launch_token_logprobs(const LogprobArgs &a, int dtype, hipStream_t s)
   return hipGetLastError();
 }
 
-size_t distill_scratch(int64_t rows, int64_t vocab) {
+// Slices of the distillation loss.  With the gradient, a block a row from a block a CU on: a row
+// that registers hold is read once (measured at 512 x 50257 bf16: 48 us in two slices, 32 us so).
+int distill_slices(int64_t rows, int64_t vocab, int dtype, bool grad, int64_t *each) {
+  const bool held = vocab <= (dtype == 0 ? kRowMax<0> : kRowMax<1>);
+  return slices_of(rows, vocab, each, grad && held ? 256 : kFill);
+}
+
+size_t distill_scratch(int64_t rows, int64_t vocab, int dtype, bool grad) {
   int64_t each;
-  const int n = slices_of(rows, vocab, &each);
+  const int n = distill_slices(rows, vocab, dtype, grad, &each);
   return n == 1 ? 0 : (((size_t)rows * n * sizeof(Stat) + 15) & ~(size_t)15) + (size_t)rows * 16;
 }
 
 hipError_t launch_distill_loss(const DistillArgs &a, int dtype, hipStream_t s) {
   int64_t each;
-  const int n = slices_of(a.rows, a.vocab, &each);
+  const int n = distill_slices(a.rows, a.vocab, dtype, a.grad != nullptr, &each);
   if (dtype == 0)
     a.tail ? distill_of<0, true>(a, n, each, s) : distill_of<0, false>(a, n, each, s);
   else

@@ -69,6 +69,18 @@ def test_logprobs_ties(vocab, rows):
     _check_logprobs(z, tokens, 17)
 
 
+@pytest.mark.parametrize("vocab,top", [(50257, 20), (140001, 128), (200000, 128)])
+def test_logprobs_largest_together(vocab, top):
+    """The largest entries next to each other, in one of the slices of a row that is joined from
+    many, or spread so that every slice has as many."""
+    say("logprobs together", vocab, top)
+    z = torch.zeros(3, vocab)
+    z[0] = torch.arange(vocab) * 1e-3
+    z[1] = -torch.arange(vocab) * 1e-3
+    z[2, :: vocab // 997] = torch.arange(len(z[2, :: vocab // 997])) % 7 * 1.0
+    _check_logprobs(z, np.zeros(3, np.int64), top)
+
+
 @pytest.mark.parametrize("rows", [8, 1200])
 def test_logprobs_masks(rows):
     """Rows that a mask leaves nothing or one entry, lowest finite values, infinities and NaN."""
