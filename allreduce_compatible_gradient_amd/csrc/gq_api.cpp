@@ -1084,7 +1084,7 @@ GQ_EXPORT gq_status gq_mx_matmul(gq_ctx *c, const void *a, int32_t a_dtype,
   m.out_dtype = out_dtype;
   m.accumulate = accumulate;
   // scratch: A's packed rows (unless the product packs them itself), then partial products
-  const bool pack = !packed && !gq::mx_matmul_packs_rows(M);
+  const bool pack = !packed && !gq::mx_matmul_packs_rows(M, K);
   const size_t blocks = pack ? (size_t)M * (size_t)gq::mx_pitch(K) : 0;
   const size_t rows_bytes = align256(blocks * 16) + align256(blocks);
   const size_t partial = gq::mx_matmul_scratch(M, N, K);

@@ -48,7 +48,7 @@ hipError_t launch_mx_quantize(const MxQuantArgs &a, int dtype, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxDequantArgs &a, int out_dtype, hipStream_t s);
 // Whether the product of these sizes quantises fp32 / bf16 rows of A by itself; otherwise the
 // caller packs them first.
-bool mx_matmul_packs_rows(int64_t M);
+bool mx_matmul_packs_rows(int64_t M, int64_t K);
 // Bytes of scratch for partial products (0: none).
 size_t mx_matmul_scratch(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_matmul(const MxMatmulArgs &a, hipStream_t s);

@@ -125,22 +125,6 @@ __device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// A whole block to nearest in one lane: its scale byte, its codes.
-__device__ __forceinline__ uint32_t encode_block(const float (&x)[32], i32x4 &codes) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  if (top >= 0x7F800000u) {
-    codes = i32x4{0, 0, 0, 0};
-    return 255;
-  }
-  const int s = scale_byte<false>(top);
-  const float inv = inverse_scale(s);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) codes[q] = (int)nearest_codes(x + 8 * q, inv);
-  return (uint32_t)s;
-}
-
 // ---------------------------------------------------------------- quantisation
 // Largest over the lane's neighbours: quads, then 16 lanes (a block's lanes in the two kernels).
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
@@ -160,6 +144,25 @@ __device__ __forceinline__ void row_max(uint32_t (&v)[4]) {
 #undef GQ_DPP_MAX
 }
 
+// Eight elements of a row from `first` on, zeros past its end.
+template <int DT>
+__device__ __forceinline__ void load_word(const void *x, int64_t row_at, int64_t first, int64_t cols,
+                                          float (&v)[8]) {
+  if (first + 8 <= cols) {
+    load_eight<DT>(x, row_at + first, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = first + i < cols ? load_one<DT>(x, row_at + first + i) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return top;
+}
+
 // By rows: a lane holds eight elements (one 16-byte load of bf16), four lanes a block.  Threads
 // run over the words of a packed row, padding included.
 template <int DT, bool STOCH>
@@ -168,18 +171,9 @@ __global__ __launch_bounds__(256) void k_mx_rows(const MxQuantArgs a, int pitch)
   const int word = blockIdx.x * blockDim.x + threadIdx.x;
   if (row >= a.rows || word >= pitch * 4) return;  // whole quads
   const int64_t first = (int64_t)word * 8;
-  float x[8] = {};
-  if (first + 8 <= a.cols) {
-    load_eight<DT>(a.x, row * a.ld + first, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (first + i < a.cols) x[i] = load_one<DT>(a.x, row * a.ld + first + i);
-  }
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  top = quad_max(top);
+  float x[8];
+  load_word<DT>(a.x, row * a.ld, first, a.cols, x);
+  const uint32_t top = quad_max(top_of(x));
   const int s = scale_byte<STOCH>(top);
   const float inv = inverse_scale(s);
   uint32_t codes = 0;
@@ -705,50 +699,76 @@ __global__ __launch_bounds__(256) void k_mx_join(const MxMatmulArgs a, int split
 // Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it, so
 // each block streams 16 rows of B straight to registers, its waves on interleaved K steps of
 // 256, and nothing of B is shared.  v_mfma_scale_f32_16x16x128: lane l holds 32 elements of row
-// l mod 16, block l / 16 of the step.  That is one whole block of A, so a lane quantises its own
-// block of fp32 / bf16 rows to nearest in registers.  The waves' sums meet in LDS, in order.
+// l mod 16, block l / 16 of the step.  fp32 / bf16 rows are packed by the block into LDS, eight
+// elements a lane, while its first weights are on their way (a lane packing its own operand's 32
+// elements, with the lanes of absent rows idle, took 12 us of 1 x 4096 by 11008 x 4096, so 8).
+// The waves' sums meet in LDS, in order.
 constexpr int kFewWaves = 8;
+// LDS of M packed rows: a row is padded by a chunk, so that 16 rows lie on different banks.
+inline size_t few_lds(int64_t M, int64_t pitch) { return (size_t)M * (size_t)(pitch * 17 + 16); }
+
 template <int AT>
 __global__ __launch_bounds__(kFewWaves * 64) void k_mx_matmul_few(const MxMatmulArgs a, int pitch) {
   __shared__ f32x4 sums[kFewWaves][64];
+  extern __shared__ __align__(16) uint8_t packed[];  // M rows of codes, then of scales
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, quarter = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int64_t n = min(n0 + r16, a.N - 1);
   const uint8_t *b = a.b + n * pitch * 16, *bs = a.b_scales + n * pitch;
+  // a wave's step of B, the next one loaded before this one is used
+  struct Step {
+    i32x4 codes[2];
+    u32x2 scales;
+  };
+  auto load = [&](int blk) {
+    Step s;
+    s.codes[0] = *reinterpret_cast<const i32x4 *>(b + (int64_t)(blk + quarter) * 16);
+    s.codes[1] = *reinterpret_cast<const i32x4 *>(b + (int64_t)(blk + 4 + quarter) * 16);
+    s.scales = *reinterpret_cast<const u32x2 *>(bs + blk);
+    return s;
+  };
+  Step now = {}, next = {};
+  if (wave * 8 < pitch) now = load(wave * 8);
+  const int row_bytes = AT == 2 ? pitch * 16 : pitch * 16 + 16;
+  const uint8_t *rows = static_cast<const uint8_t *>(a.a), *scales = a.a_scales;
+  if constexpr (AT != 2) {
+    uint8_t *out_scales = packed + (int)a.M * row_bytes;
+    const int words = pitch * 4;
+    for (int i = threadIdx.x; i < (int)a.M * words; i += kFewWaves * 64) {
+      const int m = i / words, word = i % words;
+      float x[8];
+      load_word<AT>(a.a, m * a.lda, (int64_t)word * 8, a.K, x);
+      const uint32_t top = quad_max(top_of(x));
+      const int s = scale_byte<false>(top);
+      const uint32_t codes = nearest_codes(x, inverse_scale(s));
+      const bool bad = top >= 0x7F800000u;
+      reinterpret_cast<uint32_t *>(packed + m * row_bytes)[word] = bad ? 0u : codes;
+      if ((word & 3) == 0) out_scales[m * pitch + word / 4] = bad ? 255 : (uint8_t)s;
+    }
+    rows = packed;
+    scales = out_scales;
+    __syncthreads();
+  }
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int blk = wave * 8; blk < pitch; blk += kFewWaves * 8) {
+    if (blk + kFewWaves * 8 < pitch) next = load(blk + kFewWaves * 8);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int at = blk + 4 * h + quarter;
-      const i32x4 fb = *reinterpret_cast<const i32x4 *>(b + (int64_t)at * 16);
-      const int sb = bs[at];
+      const i32x4 fb = now.codes[h];
+      const int sb = (int)(now.scales[h] >> (8 * quarter));
       i32x4 fa = {0, 0, 0, 0};
       int sa = 0;
       if (r16 < a.M) {
-        if constexpr (AT == 2) {
-          fa = *reinterpret_cast<const i32x4 *>(static_cast<const uint8_t *>(a.a) +
-                                                ((int64_t)r16 * pitch + at) * 16);
-          sa = a.a_scales[(int64_t)r16 * pitch + at];
-        } else {
-          const int64_t k0 = (int64_t)at * kMxBlock;
-          float x[32];
-          if (k0 + kMxBlock <= a.K) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              load_eight<AT>(a.a, r16 * a.lda + k0 + 8 * q, *reinterpret_cast<float(*)[8]>(x + 8 * q));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              x[i] = k0 + i < a.K ? load_one<AT>(a.a, r16 * a.lda + k0 + i) : 0.0f;
-          }
-          sa = (int)encode_block(x, fa);
-        }
+        fa = *reinterpret_cast<const i32x4 *>(rows + (int64_t)r16 * row_bytes + at * 16);
+        sa = scales[(int64_t)r16 * pitch + at];
       }
       const i32x8 x = __builtin_shufflevector(fa, fa, 0, 1, 2, 3, -1, -1, -1, -1);
       const i32x8 y = __builtin_shufflevector(fb, fb, 0, 1, 2, 3, -1, -1, -1, -1);
       acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(y, x, acc, 4, 4, 0, sb, 0, sa);
     }
+    now = next;
   }
   sums[wave][lane] = acc;
   __syncthreads();
@@ -849,7 +869,9 @@ hipError_t launch_mx_dequantize(const MxDequantArgs &a, int out_dtype, hipStream
   return hipGetLastError();
 }
 
-bool mx_matmul_packs_rows(int64_t M) { return M <= kFewRows; }
+bool mx_matmul_packs_rows(int64_t M, int64_t K) {
+  return M <= kFewRows && few_lds(M, mx_pitch(K)) <= 49152;
+}
 
 size_t mx_matmul_scratch(int64_t M, int64_t N, int64_t K) {
   if (M <= kFewRows) return 0;
@@ -861,10 +883,11 @@ hipError_t launch_mx_matmul(const MxMatmulArgs &a, hipStream_t s) {
   const int pitch = (int)mx_pitch(a.K);
   if (a.M <= kFewRows) {
     const unsigned blocks = (unsigned)((a.N + 15) / 16);
+    const size_t lds = few_lds(a.M, pitch);
     if (a.a_dtype == 0)
-      k_mx_matmul_few<0><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+      k_mx_matmul_few<0><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
     else if (a.a_dtype == 1)
-      k_mx_matmul_few<1><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+      k_mx_matmul_few<1><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
     else
       k_mx_matmul_few<2><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
     return hipGetLastError();

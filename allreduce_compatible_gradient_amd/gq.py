@@ -134,8 +134,11 @@ def version() -> str:
 
 
 # ----------------------------------------------------------------------------- marshalling
+_raw_stream = torch._C._cuda_getCurrentRawStream  # 0.1 us; a torch.cuda.Stream object takes 3
+
+
 def _stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
@@ -478,8 +481,11 @@ class MXTensor:
     @staticmethod
     def empty(rows: int, cols: int, device) -> "MXTensor":
         pitch = mx_pitch(cols)
-        return MXTensor(torch.empty(rows, 16 * pitch, dtype=torch.uint8, device=device),
-                        torch.empty(rows, pitch, dtype=torch.uint8, device=device), cols)
+        t = MXTensor.__new__(MXTensor)
+        t.codes = torch.empty(rows, 16 * pitch, dtype=torch.uint8, device=device)
+        t.scales = torch.empty(rows, pitch, dtype=torch.uint8, device=device)
+        t.rows, t.cols = rows, cols
+        return t
 
 
 def mx_pitch(cols: int) -> int:
@@ -491,11 +497,15 @@ def _rows(t: torch.Tensor, name: str, dtype=None):
     """(address, row stride) of a matrix whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be a matrix with contiguous rows" % name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError("%s must be a matrix with contiguous rows" % name)
+    return t.data_ptr(), (ld if rows > 1 else max(ld, cols))
 
 
 def mx_quantize(x, rounding=MX_NEAREST, seed=0, worker=0, index_base=0, by_rows=True,
@@ -508,9 +518,10 @@ def mx_quantize(x, rounding=MX_NEAREST, seed=0, worker=0, index_base=0, by_rows=
     rows, cols = x.shape
     q = (out or MXTensor.empty(rows, cols, x.device)) if by_rows else None
     qt = (out_t or MXTensor.empty(cols, rows, x.device)) if by_cols else None
-    for t, shape, name in ((q, (rows, cols), "out"), (qt, (cols, rows), "out_t")):
-        if t is not None and (t.rows, t.cols) != shape:
-            raise ValueError("%s must be a packed %d x %d matrix" % (name, *shape))
+    if q is not None and (q.rows != rows or q.cols != cols):
+        raise ValueError("out must be a packed %d x %d matrix" % (rows, cols))
+    if qt is not None and (qt.rows != cols or qt.cols != rows):
+        raise ValueError("out_t must be a packed %d x %d matrix" % (cols, rows))
     ctx.check(_lib.gq_mx_quantize(
         ctx.handle, p, _elt(x), rows, cols, ld, rounding, seed, worker, index_base,
         None if q is None else _dev(q.codes, "out.codes", torch.uint8),

@@ -107,7 +107,7 @@ def _operands(m, n, k, seed):
     return a, b
 
 
-PRODUCTS = [(1, 1, 1), (1, 130, 100), (3, 17, 257), (16, 513, 1000), (17, 513, 1000), (33, 128, 32),
+PRODUCTS = [(1, 1, 1), (1, 130, 100), (3, 17, 257), (16, 513, 1000), (9, 40, 9000), (2, 300, 5000), (17, 513, 1000), (33, 128, 32),
             (64, 200, 4100), (65, 31, 513), (128, 128, 256), (257, 300, 768), (300, 1031, 520),
             (700, 2100, 300), (2048, 2304, 512), (2100, 2050, 777)]
 
