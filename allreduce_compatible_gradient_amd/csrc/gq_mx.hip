@@ -787,18 +787,28 @@ struct MatmulPlan {
   int splits, each;    // K splits and steps of each
 };
 
-// Tile and K splits of a product of more than kFewRows rows.
+// Tile and K splits of a product of more than kFewRows rows.  Tiles of 256 x 256 where they give
+// nearly every CU one (4096 x 4096 x 4096: 37.5 us, of 128 x 128 44.7; 2048 x 4096 x 4096, half a
+// GPU of them: 30.7 and 24.4); tiles of 64 x 128 below 64 of 128 x 128 (128 x 4096 x 4096: 8.7 and
+// 11.9).  Splits only where tiles are few and K is long: partial products cost a second kernel and
+// their bytes (64 x 4096 x 11008: 17 us whole, 13.2 in 4; 64 x 4096 x 4096 is no faster in 2).
 MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K) {
   MatmulPlan p;
   const int64_t steps = mx_pitch(K) / 8;
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  p.bm = 256, p.bn = 256;
-  if (tiles(256, 256) < 256) p.bm = 128, p.bn = 128;
-  if (M <= 64) p.bm = 64, p.bn = 128;
-  int64_t splits = 512 / tiles(p.bm, p.bn);
-  if (splits > steps / 2) splits = steps / 2;
-  if (splits > 16) splits = 16;
-  if (splits < 1) splits = 1;
+  if (tiles(256, 256) >= 224)
+    p.bm = 256, p.bn = 256;
+  else if (tiles(128, 128) >= 64)
+    p.bm = 128, p.bn = 128;
+  else
+    p.bm = 64, p.bn = 128;
+  int64_t splits = 1;
+  if (steps >= 24) {
+    splits = 256 / tiles(p.bm, p.bn);
+    if (splits > steps / 8) splits = steps / 8;
+    if (splits > 16) splits = 16;
+    if (splits < 1) splits = 1;
+  }
   p.each = (int)((steps + splits - 1) / splits);
   p.splits = (int)((steps + p.each - 1) / p.each);
   return p;

@@ -109,7 +109,8 @@ def _operands(m, n, k, seed):
 
 PRODUCTS = [(1, 1, 1), (1, 130, 100), (3, 17, 257), (16, 513, 1000), (9, 40, 9000), (2, 300, 5000), (17, 513, 1000), (33, 128, 32),
             (64, 200, 4100), (65, 31, 513), (128, 128, 256), (257, 300, 768), (300, 1031, 520),
-            (700, 2100, 300), (2048, 2304, 512), (2100, 2050, 777)]
+            (700, 2100, 300), (2048, 2304, 512), (2100, 2050, 777),
+            (4000, 3900, 777), (40, 300, 9000), (100, 90, 40000)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
