@@ -1,0 +1,83 @@
+"""Training a language model's layers in 4 bits from a teacher's answers, under torch autograd.
+
+Two functions over the library's operators (``gq``): a linear layer whose three products run on
+microscaled 4-bit operands, and the distillation loss from a teacher's top log probabilities.
+The gradients they leave on fp32 master weights are what the gradient quantisers exchange.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from allreduce_compatible_gradient_amd import gq
+
+
+def _code(dtype: torch.dtype) -> int:
+    if dtype == torch.float32:
+        return gq.F32
+    if dtype == torch.bfloat16:
+        return gq.BF16
+    raise TypeError("float32 or bfloat16 expected, got %s" % dtype)
+
+
+class _Linear(torch.autograd.Function):
+    """y = x W^T + b.  Activations and weights are rounded to nearest, along the products' inner
+    axis: by rows for y, by columns for dX = dY W and dW = dY^T X.  dY is rounded stochastically,
+    both ways in one read, so that the gradients are unbiased in it."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, seed, worker):
+        qx, qxt = gq.mx_quantize(x, by_cols=ctx.needs_input_grad[1])
+        qw, qwt = gq.mx_quantize(weight, by_cols=ctx.needs_input_grad[0])
+        ctx.operands = qxt, qwt
+        ctx.draws = seed, worker
+        ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
+        return gq.mx_matmul(qx, qw, bias=None if bias is None else bias.float(),
+                            out_dtype=_code(x.dtype))
+
+    @staticmethod
+    def backward(ctx, dy):
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        qxt, qwt = ctx.operands
+        dtype_x, dtype_w, dtype_b = ctx.dtypes
+        dx = dw = db = None
+        if need_x or need_w:
+            q, qt = gq.mx_quantize(dy.contiguous(), gq.MX_STOCHASTIC, *ctx.draws, by_rows=need_x,
+                                   by_cols=need_w)
+            if need_x:
+                dx = gq.mx_matmul(q, qwt, out_dtype=_code(dtype_x))
+            if need_w:
+                dw = gq.mx_matmul(qt, qxt, out_dtype=_code(dtype_w))
+        if need_b:
+            db = dy.float().sum(0).to(dtype_b)
+        return dx, dw, db, None, None
+
+
+def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+              seed: int = 0, worker: int = 0) -> torch.Tensor:
+    """A linear layer (x: tokens x in, weight: out x in) in microscaled 4-bit floating point.
+    ``seed`` has to differ from one step and layer to the next; workers draw apart by ``worker``."""
+    return _Linear.apply(x, weight, bias, seed, worker)
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_ids, top_logprobs, temperature, tail):
+        logits = logits.detach()
+        loss, stats = gq.distill_loss(logits, top_ids, top_logprobs, temperature, tail)
+        ctx.save_for_backward(logits, top_ids, top_logprobs, stats)
+        ctx.form = temperature, tail
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad_loss):
+        logits, top_ids, top_logprobs, stats = ctx.saved_tensors
+        return gq.distill_grad(logits, top_ids, top_logprobs, *ctx.form, stats,
+                               grad_loss.float().contiguous()), None, None, None, None
+
+
+def distill(logits: torch.Tensor, top_ids: torch.Tensor, top_logprobs: torch.Tensor,
+            temperature: float = 1.0, tail: bool = False) -> torch.Tensor:
+    """Each row's distillation loss (gq.distill_loss), differentiable in ``logits``."""
+    return _Distill.apply(logits, top_ids, top_logprobs, temperature, tail)
