@@ -561,26 +561,32 @@ struct RowStat {  // what the gradient needs of a row
   float scale;    // p_j = scale e^(lp_j)
 };
 
-// Loads the row's ids and e^(lp); returns the sum of the latter, in 64 bits: p_R is 1 less it.
-template <int T = kThreads, typename Room>
-__device__ __forceinline__ double load_taught(const DistillArgs &a, int64_t row, Room &t) {
+// Loads the row's ids: t.id[j] is -1 where entry j is not taught.
+template <typename Room>
+__device__ __forceinline__ bool load_ids(const DistillArgs &a, int64_t row, Room &t) {
   const int tid = threadIdx.x;
   __syncthreads();
   if (tid < a.top) t.id[tid] = a.top_ids[row * a.top + tid];
   __syncthreads();
   bool ok = false;
-  double p = 0.0;
   if (tid < a.top) {
     const int32_t id = t.id[tid];
     ok = id >= 0 && id < a.vocab;
-    for (int i = 0; i < tid && ok; ++i) ok = t.id[i] != id;
-    if (ok) p = exp((double)a.top_logprobs[row * a.top + tid]);
+#pragma unroll 8
+    for (int i = 0; i < a.top; ++i) ok = ok && !(i < tid && t.id[i] == id);
   }
   __syncthreads();
-  if (tid < a.top) {
-    if (!ok) t.id[tid] = -1;
-    t.p[tid] = (float)p;
-  }
+  if (tid < a.top && !ok) t.id[tid] = -1;
+  return ok;
+}
+
+// Loads the row's ids and e^(lp); returns the sum of the latter, in 64 bits: p_R is 1 less it.
+template <int T = kThreads, typename Room>
+__device__ __forceinline__ double load_taught(const DistillArgs &a, int64_t row, Room &t) {
+  const int tid = threadIdx.x;
+  const float lp = tid < a.top ? a.top_logprobs[row * a.top + tid] : 0.0f;
+  const double p = load_ids(a, row, t) ? exp((double)lp) : 0.0;
+  if (tid < a.top) t.p[tid] = (float)p;
   return block_sum<T>(p, t.sums);
 }
 
@@ -593,12 +599,15 @@ __device__ __forceinline__ int place_in(const Slice &s, int64_t id, int *bit) {
 
 // Statistic of the slice's entries in R (tail) or of all of them.
 template <int DT, bool TAIL>
-__device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, Taught &t) {
+__device__ __forceinline__ Stat rest_stat(const DistillArgs &a, int64_t row, const Slice &s, Taught &t) {
   const int tid = threadIdx.x;
+  Chunk<DT> now[4], next[4];
+  int there = load_group<DT>(s, 0, now), there_next = 0;
   const float cl = a.inv_t * kLog2e;
   const int sweeps = sweeps_of(s);
   if constexpr (TAIL) {
     for (int g = 0; g < sweeps; ++g) t.in_group[g * kThreads + tid] = 0;
+    load_ids(a, row, t);
     __syncthreads();
     if (tid < a.top && t.id[tid] >= s.first && t.id[tid] < s.first + s.count) {
       int bit;
@@ -608,8 +617,6 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, 
     __syncthreads();
   }
   Stat mine = {-INFINITY, 0.0f, 0.0f};
-  Chunk<DT> now[4], next[4];
-  int there = load_group<DT>(s, 0, now), there_next = 0;
   for (int g = 0; g < sweeps; ++g) {
     if (g + 1 < sweeps) there_next = load_group<DT>(s, g + 1, next);
     if (!TAIL || t.in_group[g * kThreads + tid] == 0) add_group<false>(mine, now, there, cl);
@@ -651,7 +658,7 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, const Slice &s, 
 // terms at most) is held in 64 bits: an error of R's sum then counts q_R - p_R times only.
 template <int DT, bool TAIL, int T, typename Room>
 __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row, Stat rest,
-                                              double sum_p, Room &t) {
+                                              double sum_p, Room &t, bool write = true) {
   const int tid = threadIdx.x;
   const float cl = a.inv_t * kLog2e;
   const bool mine = tid < a.top && t.id[tid] >= 0;
@@ -692,7 +699,7 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
   }
   const bool none = taught == 0.0 || (!TAIL && sum_p == 0.0);
   if (none) r = RowStat{ref, 0.0f, 0.0f, 0.0f};
-  if (tid == 0) {
+  if (write && tid == 0) {
     a.loss[row] = none ? 0.0f : (float)(loss * a.temperature * a.temperature);
     if (a.stats) reinterpret_cast<f32x4 *>(a.stats)[row] = f32x4{r.ref, r.inv_s, r.rest, r.scale};
   }
@@ -947,9 +954,8 @@ __global__ __launch_bounds__(kThreads) void k_distill_slices(const DistillArgs a
                                                              int64_t each) {
   __shared__ Taught t;
   const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
-  if constexpr (TAIL) load_taught(a, row, t);
   const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
-  const Stat rest = rest_stat<DT, TAIL>(a, s, t);
+  const Stat rest = rest_stat<DT, TAIL>(a, row, s, t);
   if (threadIdx.x == 0) static_cast<Stat *>(a.scratch)[blockIdx.x] = rest;
 }
 
@@ -964,16 +970,25 @@ __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, 
   finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t);
 }
 
-// A block a slice: the gradient from the rows' constants.
-template <int DT>
+// A block a slice: the gradient from the rows' constants, or (JOIN) from the slices' statistics:
+// every block joins its row's for itself, one kernel less than with the constants in between.
+template <int DT, bool JOIN, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, int slices,
                                                            int64_t each) {
   __shared__ Taught t;
   const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
-  load_taught(a, row, t);
   const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
-  const f32x4 q = reinterpret_cast<const f32x4 *>(a.stats)[row];
-  grad_stream<DT>(a, row, s, RowStat{q.x, q.y, q.z, q.w}, t);
+  const double sum_p = load_taught(a, row, t);
+  RowStat r;
+  if constexpr (JOIN) {
+    const Stat rest = join_slices<false>(static_cast<const Stat *>(a.scratch) + row * slices, slices,
+                                         a.inv_t * kLog2e, t.stats);
+    r = finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t, part == 0);
+  } else {
+    const f32x4 q = reinterpret_cast<const f32x4 *>(a.stats)[row];
+    r = RowStat{q.x, q.y, q.z, q.w};
+  }
+  grad_stream<DT>(a, row, s, r, t);
 }
 
 // Slices of a row: as many as fill the GPU a few times over, at least 2048 entries each, at most
@@ -999,11 +1014,6 @@ void logprobs_of(const LogprobArgs &a, int slices, int64_t each, hipStream_t s) 
   if (slices > 1) k_logprobs_join<DT><<<(unsigned)a.rows, kThreads, 0, s>>>(a, slices);
 }
 
-template <int DT>
-void distill_grad_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
-  k_distill_grad<DT><<<(unsigned)(a.rows * slices), kThreads, 0, s>>>(a, slices, each);
-}
-
 // The longest row that a block's registers hold: 16 chunks of bf16, 8 of fp32 a thread.
 template <int DT>
 constexpr int64_t kRowMax = 1024 * (DT == 0 ? 64 : 128) - 64;
@@ -1024,13 +1034,19 @@ void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
       k_distill_row<DT, TAIL, 1024, 16><<<rows, 1024, 0, s>>>(a);
     return;
   }
+  const unsigned blocks = (unsigned)(a.rows * slices);
+  k_distill_slices<DT, TAIL><<<blocks, kThreads, 0, s>>>(a, slices, each);
+  // in place, a block's gradient would replace taught logits that another block still reads
+  if (a.grad && a.grad != a.logits) {
+    k_distill_grad<DT, true, TAIL><<<blocks, kThreads, 0, s>>>(a, slices, each);
+    return;
+  }
   DistillArgs b = a;
   if (!b.stats)
     b.stats = reinterpret_cast<float *>(static_cast<char *>(a.scratch) +
                                         (((size_t)a.rows * slices * sizeof(Stat) + 15) & ~(size_t)15));
-  k_distill_slices<DT, TAIL><<<(unsigned)(a.rows * slices), kThreads, 0, s>>>(b, slices, each);
   k_distill_join<DT, TAIL><<<(unsigned)a.rows, kThreads, 0, s>>>(b, slices);
-  if (a.grad) distill_grad_of<DT>(b, slices, each, s);
+  if (a.grad) k_distill_grad<DT, false, false><<<blocks, kThreads, 0, s>>>(b, slices, each);
 }
 
 }  // namespace
@@ -1078,10 +1094,11 @@ hipError_t launch_distill_loss(const DistillArgs &a, int dtype, hipStream_t s) {
 hipError_t launch_distill_grad(const DistillArgs &a, int dtype, hipStream_t s) {
   int64_t each;
   const int n = slices_of(a.rows, a.vocab, &each);
+  const unsigned blocks = (unsigned)(a.rows * n);
   if (dtype == 0)
-    distill_grad_of<0>(a, n, each, s);
+    k_distill_grad<0, false, false><<<blocks, kThreads, 0, s>>>(a, n, each);
   else
-    distill_grad_of<1>(a, n, each, s);
+    k_distill_grad<1, false, false><<<blocks, kThreads, 0, s>>>(a, n, each);
   return hipGetLastError();
 }
 
