@@ -1158,7 +1158,7 @@ GQ_EXPORT gq_status gq_distill_loss(gq_ctx *c, const void *logits, int32_t dtype
   a.stats = stats_or_null;
   a.grad = dlogits_or_null;
   a.ldg = ldd;
-  const size_t bytes = gq::distill_scratch(rows, vocab, dtype, dlogits_or_null != nullptr);
+  const size_t bytes = gq::distill_scratch(rows, vocab, dtype);
   if (bytes) TRY(ensure_scratch(c, bytes, s));
   a.scratch = c->scratch;
   const hipError_t e = gq::launch_distill_loss(a, dtype, s);

@@ -88,7 +88,7 @@ struct DistillArgs {
 
 size_t logprobs_scratch(int64_t rows, int64_t vocab, int top);
 hipError_t launch_token_logprobs(const LogprobArgs &a, int dtype, hipStream_t s);
-size_t distill_scratch(int64_t rows, int64_t vocab, int dtype, bool grad);
+size_t distill_scratch(int64_t rows, int64_t vocab, int dtype);
 hipError_t launch_distill_loss(const DistillArgs &a, int dtype, hipStream_t s);
 hipError_t launch_distill_grad(const DistillArgs &a, int dtype, hipStream_t s);
 

@@ -110,6 +110,21 @@ __device__ __forceinline__ Chunk<DT> load_chunk(const Slice &s, int v) {
   return c;
 }
 
+// Entries of the chunk whose bit is set become -inf.
+template <int DT>
+__device__ __forceinline__ void strip(Chunk<DT> &x, uint32_t mask) {
+  if (mask == 0) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (!(mask >> i & 1u)) continue;
+    if constexpr (DT == 0)
+      x.w[i / 4][i % 4] = 0xFF800000u;
+    else
+      x.w[0][i / 2] = i % 2 ? (x.w[0][i / 2] & 0xFFFFu) | 0xFF800000u
+                            : (x.w[0][i / 2] & 0xFFFF0000u) | 0xFF80u;
+  }
+}
+
 // A thread's four chunks of sweep g; returns how many of them its wave has anything of.  Whether
 // they are whole is one question a wave.
 template <int DT>
@@ -544,8 +559,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(const LogprobArgs a,
 // mass p_R = 1 - sum p_j is matched with q_R = sum of q over R.
 //   loss = T^2 (sum p_j (log p_j - log q_j) + p_R (log p_R - log q_R))
 //   dz_v = w T (q_v - p_v) in S,  w T q_v (1 - p_R / q_R) in R
-// q_R is summed over R itself: the groups that hold a taught entry are left out of the stream
-// and added entry by entry, so nothing is subtracted.
+// q_R is summed over R itself, taught entries becoming -inf on the way, so nothing is subtracted.
 struct Taught {
   int32_t id[kVocabTop];     // -1: not taught
   float p[kVocabTop];
@@ -619,36 +633,16 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, int64_t row, con
   Stat mine = {-INFINITY, 0.0f, 0.0f};
   for (int g = 0; g < sweeps; ++g) {
     if (g + 1 < sweeps) there_next = load_group<DT>(s, g + 1, next);
-    if (!TAIL || t.in_group[g * kThreads + tid] == 0) add_group<false>(mine, now, there, cl);
+    if constexpr (TAIL) {
+      const uint32_t mask = t.in_group[g * kThreads + tid];
+      if (mask != 0)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) strip(now[j], mask >> (8 * j) & 0xFFu);
+    }
+    add_group<false>(mine, now, there, cl);
 #pragma unroll
     for (int j = 0; j < 4; ++j) now[j] = next[j];
     there = there_next;
-  }
-  if constexpr (TAIL) {
-    // the group of taught entry j, if no earlier one is in it
-    if (tid < a.top && t.id[tid] >= s.first && t.id[tid] < s.first + s.count) {
-      int bit;
-      const int g = place_in(s, t.id[tid], &bit);
-      bool first = true;
-      for (int i = 0; i < tid && first; ++i)
-        if (t.id[i] >= s.first && t.id[i] < s.first + s.count) {
-          int b;
-          first = place_in(s, t.id[i], &b) != g;
-        }
-      if (first) {
-        const uint32_t mask = t.in_group[g];
-        for (int j = 0; j < 4; ++j) {
-          Chunk<0> c[1];
-          const Chunk<DT> raw =
-              load_chunk<DT>(s, (g / kThreads) * kSweep + j * kPart + (g % kThreads) * 8);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            c[0].w[i / 4][i % 4] =
-                __float_as_uint(mask >> (8 * j + i) & 1u ? -INFINITY : raw.get(i));
-          add_chunks<false>(mine, c, max_of(c), cl);
-        }
-      }
-    }
   }
   return block_join<false>(mine, cl, t.stats);
 }
@@ -884,27 +878,14 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
     __syncthreads();
   }
   // with a tail, taught entries leave the registers: their gradient is written apart
-  auto strip = [&](Chunk<DT> &x, int chunk) {
-    const uint32_t mask = t.in_chunk[chunk];
-    if (mask == 0) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!(mask >> i & 1u)) continue;
-      if constexpr (DT == 0)
-        x.w[i / 4][i % 4] = 0xFF800000u;
-      else
-        x.w[0][i / 2] = i % 2 ? (x.w[0][i / 2] & 0xFFFFu) | 0xFF800000u
-                              : (x.w[0][i / 2] & 0xFFFF0000u) | 0xFF80u;
-    }
-  };
   auto cut_chunk = [&]() {
     Chunk<DT> x = load_chunk<DT>(s, cut_v);
-    if constexpr (TAIL) strip(x, cut_v >> 3);
+    if constexpr (TAIL) strip(x, t.in_chunk[cut_v >> 3]);
     return x;
   };
   if constexpr (TAIL) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) strip(c[j], j * T + tid);
+    for (int j = 0; j < N; ++j) strip(c[j], t.in_chunk[j * T + tid]);
   }
   // Keeps the entries as they were loaded: kept widened from one use to the next, bf16 would take
   // twice the registers.
@@ -1020,14 +1001,18 @@ constexpr int64_t kRowMax = 1024 * (DT == 0 ? 64 : 128) - 64;
 
 template <int DT, bool TAIL>
 void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
+  const unsigned rows = (unsigned)a.rows;
+  // Three blocks of 256 threads and 26 chunks a CU where a row fits them (4096 x 50257 bf16: 194 us;
+  // two of 512 and 16: 212 us).
   if (slices == 1 && a.vocab <= kRowMax<DT>) {
-    const unsigned rows = (unsigned)a.rows;
     if (a.vocab <= 256 * 64 - 64)
       k_distill_row<DT, TAIL, 256, 8><<<rows, 256, 0, s>>>(a);
     else if (a.vocab <= 512 * 64 - 64)
       k_distill_row<DT, TAIL, 512, 8><<<rows, 512, 0, s>>>(a);
     else if constexpr (DT == 0)
       k_distill_row<DT, TAIL, 1024, 8><<<rows, 1024, 0, s>>>(a);
+    else if (a.vocab <= 256 * 208 - 64)
+      k_distill_row<DT, TAIL, 256, 26><<<rows, 256, 0, s>>>(a);
     else if (a.vocab <= 512 * 128 - 64)
       k_distill_row<DT, TAIL, 512, 16><<<rows, 512, 0, s>>>(a);
     else
@@ -1068,22 +1053,24 @@ hipError_t launch_token_logprobs(const LogprobArgs &a, int dtype, hipStream_t s)
   return hipGetLastError();
 }
 
-// Slices of the distillation loss.  With the gradient, a block a row from a block a CU on: a row
-// that registers hold is read once (measured at 512 x 50257 bf16: 48 us in two slices, 32 us so).
-int distill_slices(int64_t rows, int64_t vocab, int dtype, bool grad, int64_t *each) {
+// Slices of the distillation loss: a block a row from a block a CU on, where registers hold a row
+// (512 x 50257 bf16 with the gradient: 48 us in two slices, 32 us so).  The loss alone takes the
+// same way, so that it has the same bits (a stream would be faster: 4096 x 50257 bf16, 91 us
+// against 110).
+int distill_slices(int64_t rows, int64_t vocab, int dtype, int64_t *each) {
   const bool held = vocab <= (dtype == 0 ? kRowMax<0> : kRowMax<1>);
-  return slices_of(rows, vocab, each, grad && held ? 256 : kFill);
+  return slices_of(rows, vocab, each, held ? 256 : kFill);
 }
 
-size_t distill_scratch(int64_t rows, int64_t vocab, int dtype, bool grad) {
+size_t distill_scratch(int64_t rows, int64_t vocab, int dtype) {
   int64_t each;
-  const int n = distill_slices(rows, vocab, dtype, grad, &each);
+  const int n = distill_slices(rows, vocab, dtype, &each);
   return n == 1 ? 0 : (((size_t)rows * n * sizeof(Stat) + 15) & ~(size_t)15) + (size_t)rows * 16;
 }
 
 hipError_t launch_distill_loss(const DistillArgs &a, int dtype, hipStream_t s) {
   int64_t each;
-  const int n = distill_slices(a.rows, a.vocab, dtype, a.grad != nullptr, &each);
+  const int n = distill_slices(a.rows, a.vocab, dtype, &each);
   if (dtype == 0)
     a.tail ? distill_of<0, true>(a, n, each, s) : distill_of<0, false>(a, n, each, s);
   else

@@ -377,7 +377,8 @@ gq_status gq_token_logprobs(gq_ctx *ctx, const void *logits, int32_t dtype, int6
  * (p_R counts as 0 where S is the whole vocabulary, and below 2^-16 where q_R = 0).  A row that
  * is taught nothing has loss 0 and gradient 0.
  * The gradient of sum_rows w_row loss_row is w T (q_v - p_v) in S and w T q_v (1 - p_R / q_R)
- * elsewhere; with dlogits it is written in the same call.
+ * elsewhere; with dlogits it is written in the same call (the loss and the gradient have the same
+ * bits as from gq_distill_loss without it and gq_distill_grad).
  *   logits  rows x vocab of `dtype`, row stride ld;  1 <= top <= 128
  *   loss    rows fp32;  stats_or_null  rows x 4 fp32, what gq_distill_grad needs
  *   row_weight_or_null  rows fp32 (NULL: 1);  dlogits_or_null  rows x vocab of `dtype`, row
