@@ -194,12 +194,14 @@ __global__ __launch_bounds__(256) void k_mx_rows(const MxQuantArgs a, int pitch)
   if ((threadIdx.x & 3) == 0) a.scales[row * pitch + word / 4] = bad ? 255 : (uint8_t)s;
 }
 
-// By columns, or both ways (ROWS) in one read.  A block takes 256 rows x 128 columns, a wave 64
-// rows of it, 32 at a time; a lane holds two neighbouring columns of the 32 rows, so a column's
-// block is a lane's own and a row's block lies in 16 lanes.  The draw of an element is shared by
-// its two codes.  Row codes (a byte a lane and row) and the scales of both ways are gathered in
-// LDS and leave as 16-byte, 4-byte and 8-byte pieces; a column's eight blocks of the 256 rows are
-// one 128-byte line of codes_t, written by one block.
+// By columns, or both ways (ROWS) in one read.  A block takes 128 rows x 128 columns, a wave 32
+// rows of it; a lane holds two neighbouring columns of the 32 rows, so a column's block is a lane's
+// own and a row's block lies in 16 lanes.  The draw of an element is shared by its two codes.  Row
+// codes (a byte a lane and row) and the scales of both ways are gathered in LDS and leave as
+// 16-byte and 4-byte pieces.  Measured both ways: 4096 x 11008 fp32 to nearest 54 us (229 MB, 4.2
+// TB/s), 2047 x 50257 bf16 stochastic 132 us, bound by the vector ALUs (some 45 issue slots an
+// element, 15 of them the draw).  Waves of 64 rows, which write whole lines of codes_t, took 59
+// and 144 us: fewer waves at a time.
 template <int DT>
 struct Pair;  // two neighbouring elements as loaded
 template <>
@@ -227,143 +229,140 @@ __device__ __forceinline__ Pair<DT> load_pair(const void *p, int i) {
   }
 }
 
-constexpr int kBothRows = 256, kBothCols = 128;
+constexpr int kBothRows = 128, kBothCols = 128;
 template <int DT, bool STOCH, bool ROWS>
-__global__ __launch_bounds__(256, DT == 0 && STOCH && ROWS ? 2 : 3) void k_mx_both(const MxQuantArgs a, int pitch, int pitch_t) {
+__global__ __launch_bounds__(256, DT == 0 && !STOCH ? 4 : 3) void k_mx_both(const MxQuantArgs a, int pitch, int pitch_t) {
   __shared__ __align__(16) uint8_t row_codes[ROWS ? 4 : 1][ROWS ? 32 : 1][80];
   __shared__ __align__(16) uint8_t row_scales[ROWS ? 4 : 1][ROWS ? 32 : 1][4];
-  __shared__ __align__(16) uint8_t col_scales[kBothCols][8];
+  __shared__ __align__(16) uint8_t col_scales[kBothCols][4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t col0 = (int64_t)blockIdx.x * kBothCols, col = col0 + 2 * lane;
   const bool cols_whole = (int64_t)(blockIdx.x + 1) * kBothCols <= a.cols;
-#pragma unroll 1
-  for (int it = 0; it < 2; ++it) {
-    const int64_t row0 = (int64_t)blockIdx.y * kBothRows + wave * 64 + it * 32;
-    const char *tile = static_cast<const char *>(a.x) + (row0 * a.ld + col0) * (DT == 0 ? 4 : 2);
-    const int64_t step = a.ld * (DT == 0 ? 4 : 2);  // rows are uniform: scalar addresses
-    Pair<DT> x[32];
-    if (cols_whole && row0 + 32 <= a.rows) {
+  const int64_t row0 = (int64_t)blockIdx.y * kBothRows + wave * 32;
+  const char *tile = static_cast<const char *>(a.x) + (row0 * a.ld + col0) * (DT == 0 ? 4 : 2);
+  const int64_t step = a.ld * (DT == 0 ? 4 : 2);  // rows are uniform: scalar addresses
+  Pair<DT> x[32];
+  if (cols_whole && row0 + 32 <= a.rows) {
 #pragma unroll
-      for (int r = 0; r < 32; ++r) x[r] = load_pair<DT>(tile + r * step, 2 * lane);
-    } else {
+    for (int r = 0; r < 32; ++r) x[r] = load_pair<DT>(tile + r * step, 2 * lane);
+  } else {
 #if defined(__HIP_DEVICE_COMPILE__)  // buffer resources are a type of the device only
-      // a resource a row, as long as what is there of it: what is outside loads as 0
-      constexpr int kBytes = DT == 0 ? 4 : 2;
+    // a resource a row, as long as what is there of it: what is outside loads as 0
+    constexpr int kBytes = DT == 0 ? 4 : 2;
 #pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        const bool there = row0 + r < a.rows && col0 < a.cols;
-        const auto row = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(there ? tile + r * step : tile), 0, there ? (int)(a.cols - col0) * kBytes : 0, 0x00027000);
-        if constexpr (DT == 0)
-          x[r] = Pair<0>{{__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row, lane * 8, 0, 0)),
-                          __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row, lane * 8 + 4, 0, 0))}};
-        else
-          x[r] = Pair<1>{(uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, lane * 4, 0, 0) |
-                         (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, lane * 4 + 2, 0, 0) << 16};
-      }
+    for (int r = 0; r < 32; ++r) {
+      const bool there = row0 + r < a.rows && col0 < a.cols;
+      const auto row = __builtin_amdgcn_make_buffer_rsrc(
+          (void *)(there ? tile + r * step : tile), 0, there ? (int)(a.cols - col0) * kBytes : 0, 0x00027000);
+      if constexpr (DT == 0)
+        x[r] = Pair<0>{{__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row, lane * 8, 0, 0)),
+                        __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row, lane * 8 + 4, 0, 0))}};
+      else
+        x[r] = Pair<1>{(uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, lane * 4, 0, 0) |
+                       (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, lane * 4 + 2, 0, 0) << 16};
+    }
 #endif
-    }
-    uint32_t top[2] = {0, 0};
+  }
+  uint32_t top[2] = {0, 0};
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 4) {
-      uint32_t row_top[4];
+  for (int r0 = 0; r0 < 32; r0 += 4) {
+    uint32_t row_top[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t b0 = __float_as_uint(x[r0 + i].get(0)) & 0x7FFFFFFFu;
-        const uint32_t b1 = __float_as_uint(x[r0 + i].get(1)) & 0x7FFFFFFFu;
-        top[0] = max(top[0], b0);
-        top[1] = max(top[1], b1);
-        row_top[i] = max(b0, b1);
-      }
-      if constexpr (ROWS) {
-        row_max(row_top);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + i;
-          const bool bad = row_top[i] >= 0x7F800000u;
-          const int s = scale_byte<STOCH>(row_top[i]);
-          if ((lane & 15) == 0) row_scales[wave][r][lane >> 4] = bad ? 255 : (uint8_t)s;
-          if constexpr (!STOCH) {
-            const float f = inverse_scale(s);
-            const uint32_t two = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[r].get(0) * f, x[r].get(1) * f, 1.0f, 0);
-            row_codes[wave][r][lane] = bad ? 0 : (uint8_t)two;
-          }
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);  // keeps the live rows' temporaries few
-    }
-    __builtin_amdgcn_wave_barrier();
-    const int s0 = scale_byte<STOCH>(top[0]), s1 = scale_byte<STOCH>(top[1]);
-    const float inv[2] = {inverse_scale(s0), inverse_scale(s1)};
-    u32x4 codes[2];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t w[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = 8 * q + j;
-        uint32_t h[2] = {0, 0};
-        if constexpr (STOCH) {
-          const uint32_t counter = a.index_base + (uint32_t)((row0 + r) * a.cols + col0);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            h[i] = draw(counter + 2 * lane + i, a.key_mix);
-            w[i] += (stochastic_code(x[r].get(i), inv[i], h[i]) << (4 * j)) +
-                    (sign_bit(x[r].get(i)) << (4 * j + 3));
-          }
-        } else if (j % 2 == 0) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float lo = x[r].get(i) * inv[i], hi = x[r + 1].get(i) * inv[i];
-            if (j == 0) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 0);
-            if (j == 2) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 1);
-            if (j == 4) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 2);
-            if (j == 6) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 3);
-          }
-        }
-        if constexpr (ROWS && STOCH) {
-          const uint32_t s = row_scales[wave][r][lane >> 4];
-          const float f = inverse_scale((int)s);
-          const uint32_t two =
-              stochastic_code(x[r].get(0), f, h[0]) + (stochastic_code(x[r].get(1), f, h[1]) << 4) +
-              (sign_bit(x[r].get(0)) << 3) + (sign_bit(x[r].get(1)) << 7) - 254u * 0x11u;
-          row_codes[wave][r][lane] = s == 255 ? 0 : (uint8_t)two;
-        }
-        if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) codes[i][q] = STOCH ? w[i] - kCodeBias : w[i];
-    }
-    const int64_t blk = row0 / kMxBlock;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool bad = top[i] >= 0x7F800000u;
-      if (bad) codes[i] = u32x4{0, 0, 0, 0};
-      if (col + i < a.cols)
-        *reinterpret_cast<u32x4 *>(a.codes_t + ((col + i) * pitch_t + blk) * 16) = codes[i];
-      col_scales[2 * lane + i][wave * 2 + it] = bad ? 255 : (uint8_t)(i ? s1 : s0);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b0 = __float_as_uint(x[r0 + i].get(0)) & 0x7FFFFFFFu;
+      const uint32_t b1 = __float_as_uint(x[r0 + i].get(1)) & 0x7FFFFFFFu;
+      top[0] = max(top[0], b0);
+      top[1] = max(top[1], b1);
+      row_top[i] = max(b0, b1);
     }
     if constexpr (ROWS) {
-      __builtin_amdgcn_wave_barrier();  // the wave's own part of LDS, in order
+      row_max(row_top);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = half * 16 + (lane >> 2);
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(&row_codes[wave][r][(lane & 3) * 16]);
-        if (row0 + r < a.rows)
-          *reinterpret_cast<u32x4 *>(a.codes + ((row0 + r) * pitch + blockIdx.x * 4 + (lane & 3)) * 16) = v;
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i;
+        const bool bad = row_top[i] >= 0x7F800000u;
+        const int s = scale_byte<STOCH>(row_top[i]);
+        if ((lane & 15) == 0) row_scales[wave][r][lane >> 4] = bad ? 255 : (uint8_t)s;
+        if constexpr (!STOCH) {
+          const float f = inverse_scale(s);
+          const uint32_t two = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[r].get(0) * f, x[r].get(1) * f, 1.0f, 0);
+          row_codes[wave][r][lane] = bad ? 0 : (uint8_t)two;
+        }
       }
-      if (lane < 32 && row0 + lane < a.rows)
-        *reinterpret_cast<uint32_t *>(a.scales + (row0 + lane) * pitch + blockIdx.x * 4) =
-            *reinterpret_cast<const uint32_t *>(row_scales[wave][lane]);
-      __builtin_amdgcn_wave_barrier();
     }
+    __builtin_amdgcn_sched_barrier(0);  // keeps the live rows' temporaries few
+  }
+  __builtin_amdgcn_wave_barrier();
+  const int s0 = scale_byte<STOCH>(top[0]), s1 = scale_byte<STOCH>(top[1]);
+  const float inv[2] = {inverse_scale(s0), inverse_scale(s1)};
+  u32x4 codes[2];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = 8 * q + j;
+      uint32_t h[2] = {0, 0};
+      if constexpr (STOCH) {
+        const uint32_t counter = a.index_base + (uint32_t)((row0 + r) * a.cols + col0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          h[i] = draw(counter + 2 * lane + i, a.key_mix);
+          w[i] += (stochastic_code(x[r].get(i), inv[i], h[i]) << (4 * j)) +
+                  (sign_bit(x[r].get(i)) << (4 * j + 3));
+        }
+      } else if (j % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float lo = x[r].get(i) * inv[i], hi = x[r + 1].get(i) * inv[i];
+          if (j == 0) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 0);
+          if (j == 2) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 1);
+          if (j == 4) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 2);
+          if (j == 6) w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], lo, hi, 1.0f, 3);
+        }
+      }
+      if constexpr (ROWS && STOCH) {
+        const uint32_t s = row_scales[wave][r][lane >> 4];
+        const float f = inverse_scale((int)s);
+        const uint32_t two =
+            stochastic_code(x[r].get(0), f, h[0]) + (stochastic_code(x[r].get(1), f, h[1]) << 4) +
+            (sign_bit(x[r].get(0)) << 3) + (sign_bit(x[r].get(1)) << 7) - 254u * 0x11u;
+        row_codes[wave][r][lane] = s == 255 ? 0 : (uint8_t)two;
+      }
+      if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) codes[i][q] = STOCH ? w[i] - kCodeBias : w[i];
+  }
+  const int64_t blk = row0 / kMxBlock;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool bad = top[i] >= 0x7F800000u;
+    if (bad) codes[i] = u32x4{0, 0, 0, 0};
+    if (col + i < a.cols)
+      *reinterpret_cast<u32x4 *>(a.codes_t + ((col + i) * pitch_t + blk) * 16) = codes[i];
+    col_scales[2 * lane + i][wave] = bad ? 255 : (uint8_t)(i ? s1 : s0);
+  }
+  if constexpr (ROWS) {
+    __builtin_amdgcn_wave_barrier();  // the wave's own part of LDS, in order
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = half * 16 + (lane >> 2);
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(&row_codes[wave][r][(lane & 3) * 16]);
+      if (row0 + r < a.rows)
+        *reinterpret_cast<u32x4 *>(a.codes + ((row0 + r) * pitch + blockIdx.x * 4 + (lane & 3)) * 16) = v;
+    }
+    if (lane < 32 && row0 + lane < a.rows)
+      *reinterpret_cast<uint32_t *>(a.scales + (row0 + lane) * pitch + blockIdx.x * 4) =
+          *reinterpret_cast<const uint32_t *>(row_scales[wave][lane]);
+    __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
   if (threadIdx.x < kBothCols) {
     const int64_t c = (int64_t)blockIdx.x * kBothCols + threadIdx.x;
     if (c < a.cols)
-      *reinterpret_cast<u32x2 *>(a.scales_t + c * pitch_t + blockIdx.y * 8) =
-          *reinterpret_cast<const u32x2 *>(col_scales[threadIdx.x]);
+      *reinterpret_cast<uint32_t *>(a.scales_t + c * pitch_t + blockIdx.y * 4) =
+          *reinterpret_cast<const uint32_t *>(col_scales[threadIdx.x]);
   }
 }
 
@@ -885,7 +884,7 @@ RowGrid row_grid(int64_t rows, int64_t words, int64_t most_rows) {
 template <int DT, bool STOCH>
 void quantize_of(const MxQuantArgs &a, hipStream_t s) {
   const int pitch = (int)mx_pitch(a.cols), pitch_t = (int)mx_pitch(a.rows);
-  const dim3 grid((unsigned)(pitch / 4), (unsigned)(pitch_t / 8));
+  const dim3 grid((unsigned)(pitch / 4), (unsigned)(pitch_t / 4));
   if (a.codes && a.codes_t) {
     k_mx_both<DT, STOCH, true><<<grid, 256, 0, s>>>(a, pitch, pitch_t);
   } else if (a.codes_t) {
