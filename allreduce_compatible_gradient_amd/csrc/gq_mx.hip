@@ -838,29 +838,44 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_mx_matmul_few(const MxMatmul
   }
 }
 
+constexpr int kCus = 256;
+
 struct MatmulPlan {
   int bm, bn;          // tile
   int splits, each;    // K splits and steps of each
 };
 
-// Tile and K splits of a product of more than kFewRows rows.  Tiles of 256 x 256 where they give
-// nearly every CU one (4096 x 4096 x 4096: 37.5 us, of 128 x 128 44.7; 2048 x 4096 x 4096, half a
-// GPU of them: 30.7 and 24.4); tiles of 64 x 128 below 64 of 128 x 128 (128 x 4096 x 4096: 8.7 and
-// 11.9).  Splits only where tiles are few and K is long: partial products cost a second kernel and
+// Tile and K splits of a product of more than kFewRows rows.  The tile is the one of the least
+// expected time: with n blocks on the fullest CU, n (step K / 256 + rest) + wait K / 256, the three
+// constants of each tile (in us) fitted to 260 sizes (M 17 to 8192, N 768 to 51200, K 256 to
+// 11008; the operands not in L2), where the tile so chosen takes 1.03 times the best one's time in
+// the mean; bounds on the numbers of tiles took 1.06 (248 x 36032 x 4561: 256 x 256 31.6 us, 128 x
+// 128 44.3; 333 x 50257 x 768: 27.6 and 30.4; 128 x 4096 x 4096: 64 x 128 8.7, 128 x 128 11.9).
+// Splits only where tiles are few and K is long: partial products cost a second kernel and
 // their bytes (64 x 4096 x 11008: 17 us whole, 13.2 in 4; 64 x 4096 x 4096 is no faster in 2).
 MatmulPlan plan_matmul(int64_t M, int64_t N, int64_t K) {
-  MatmulPlan p;
+  struct Tile {
+    int bm, bn;
+    float step, rest, wait;
+  };
+  constexpr Tile kTiles[3] = {
+      {256, 256, 1.8f, 3.5f, 0.0f}, {128, 128, 0.54f, 1.7f, 0.47f}, {64, 128, 0.44f, 2.2f, 0.45f}};
+  MatmulPlan p = {};
   const int64_t steps = mx_pitch(K) / 8;
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 224)
-    p.bm = 256, p.bn = 256;
-  else if (tiles(128, 128) >= 64)
-    p.bm = 128, p.bn = 128;
-  else
-    p.bm = 64, p.bn = 128;
+  float least = INFINITY;
+  for (const Tile &t : kTiles) {
+    const float each = (float)((tiles(t.bm, t.bn) + kCus - 1) / kCus);
+    const float us = each * ((float)steps * t.step + t.rest) + (float)steps * t.wait;
+    if (us < least) {
+      least = us;
+      p.bm = t.bm;
+      p.bn = t.bn;
+    }
+  }
   int64_t splits = 1;
   if (steps >= 24) {
-    splits = 256 / tiles(p.bm, p.bn);
+    splits = kCus / tiles(p.bm, p.bn);
     if (splits > steps / 8) splits = steps / 8;
     if (splits > 16) splits = 16;
     if (splits < 1) splits = 1;
