@@ -42,16 +42,19 @@ struct Slice {
   const void *row;   // the row's first element
   int64_t first;     // slice's first entry in the row
   int32_t count;     // entries
-  int32_t lead;      // 0..7
+  int32_t lead;      // entries from that place to the first
 };
 
+// The aligned place: a multiple of `grain` entries from the first row's beginning, 8, or a line of
+// 128 bytes (log probabilities of 4095 x 50257 bf16: 92.6 us from chunks, 90.6 us from lines; the
+// gradient of 1021 x 131071: 116 and 122 us).
 __device__ __forceinline__ Slice slice_of(const void *logits, int elem, int64_t row, int64_t ld,
-                                          int64_t vocab, int64_t part, int64_t each) {
+                                          int64_t vocab, int64_t part, int64_t each, int grain = 8) {
   Slice s;
   s.row = static_cast<const char *>(logits) + row * ld * elem;
   s.first = part * each;
   s.count = (int32_t)min(each, vocab - s.first);
-  s.lead = (int32_t)((row * ld + s.first) & 7);
+  s.lead = (int32_t)((row * ld + s.first) & (grain - 1));
   return s;
 }
 
@@ -451,7 +454,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
   __shared__ typename std::conditional<TOP, TopRoom, int>::type room;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
-  const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
+  const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each, DT == 0 ? 32 : 64);
   const float cl = a.inv_t * kLog2e;
   Stat mine = {-INFINITY, 0.0f, 0.0f};
   float my_max = -INFINITY;
@@ -857,8 +860,7 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
   constexpr int kElem = DT == 0 ? 4 : 2;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
-  Slice s = slice_of(a.logits, kElem, row, a.ld, a.vocab, 0, a.vocab);
-  s.lead = (int32_t)((reinterpret_cast<uintptr_t>(s.row) & 127) / kElem);
+  const Slice s = slice_of(a.logits, kElem, row, a.ld, a.vocab, 0, a.vocab, 128 / kElem);
   const float cl = a.inv_t * kLog2e;
   const int end = s.lead + s.count;
   const char *lines = static_cast<const char *>(s.row) - s.lead * kElem;
@@ -995,7 +997,7 @@ int slices_of(int64_t rows, int64_t vocab, int64_t *each, int64_t fill = kFill) 
   int64_t n = fill / rows;
   if (n > vocab / kPart) n = vocab / kPart;
   if (n > kMaxSlices) n = kMaxSlices;
-  const int64_t least = (vocab + kSlice - 9) / (kSlice - 8);
+  const int64_t least = (vocab + kSlice - 65) / (kSlice - 64);
   if (n < least) n = least;
   if (n < 1) n = 1;
   *each = ((vocab + n - 1) / n + 7) & ~7ll;
