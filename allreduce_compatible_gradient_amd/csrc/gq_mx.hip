@@ -165,8 +165,10 @@ __device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
   return top;
 }
 
-// By rows: a lane holds eight elements (one 16-byte load of bf16), four lanes a block.  Threads
-// run over the words of a packed row, padding included.
+// By rows: a lane holds eight elements (one 16-byte load of bf16), four lanes a block, so a block's
+// maximum takes two steps and its codes leave as one word a lane.  Threads run over the words of a
+// packed row, padding included.  333 x 768 bf16, an operand of a product, takes 4.8 us and
+// 1 x 4096 1.8 us: a launch's latency; larger matrices are bound by their bytes.
 template <int DT, bool STOCH>
 __global__ __launch_bounds__(256) void k_mx_rows(const MxQuantArgs a, int pitch) {
   const int64_t row = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
@@ -199,9 +201,9 @@ __global__ __launch_bounds__(256) void k_mx_rows(const MxQuantArgs a, int pitch)
 // own and a row's block lies in 16 lanes.  The draw of an element is shared by its two codes.  Row
 // codes (a byte a lane and row) and the scales of both ways are gathered in LDS and leave as
 // 16-byte and 4-byte pieces.  Measured both ways: 4096 x 11008 fp32 to nearest 54 us (229 MB, 4.2
-// TB/s), 2047 x 50257 bf16 stochastic 132 us, bound by the vector ALUs (some 45 issue slots an
-// element, 15 of them the draw).  Waves of 64 rows, which write whole lines of codes_t, took 59
-// and 144 us: fewer waves at a time.
+// TB/s), 2047 x 50257 bf16 stochastic 132-150 us by the card, bound by the vector ALUs (some 45
+// issue slots an element, 15 of them the draw).  Waves of 64 rows, which write whole lines of
+// codes_t, took 59 and 144 us where these took 54 and 132: fewer waves at a time.
 template <int DT>
 struct Pair;  // two neighbouring elements as loaded
 template <>
@@ -482,7 +484,13 @@ __device__ __forceinline__ void put_one(const Sink &s, int64_t m, int64_t n, flo
   }
 }
 
-// Tiled product: a block of WM x WN waves, a wave FM x FN tiles of 32 x 32, K in steps of 256
+// Tiled product, C = A B^T on packed operands, for more than kFewRows rows:
+// 8192 x 11008 x 4096 takes 190-195 us, 3.8-3.9 PFLOP/s; a step of
+// K takes a CU 1.8-1.9 us on random operands and 1.4-1.7 us on zeros, as the card lowers its clock
+// (to 2.0 GHz) under load; a loop of nothing but this instruction reaches 6.6 PFLOP/s on random
+// data.  Some 40 us of the whole are the first loads and the stores.  Tried and not faster: 16x16x128 instructions, four waves of 128 x 128 each, operands fetched across the
+// barrier.
+// A block of WM x WN waves, a wave FM x FN tiles of 32 x 32, K in steps of 256
 // (128 bytes of a row).  v_mfma_scale_f32_32x32x64: lane l holds 32 elements of row l mod 32,
 // those of block l / 32, and that block's scale; the result has column l mod 32 and rows
 // 8 i + 4 (l / 32) + 0..3.  The weights (B) are the first operand, so a lane ends with four
@@ -743,7 +751,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
 #endif
 }
 
-// The partial products of the K splits, added in their order.
+// The partial products of the K splits, added in their order: they are few and small
+// where splits are used (64 x 4096 x 11008 in 4: 4 MB), so a launch's latency bounds it.
 __global__ __launch_bounds__(256) void k_mx_join(const MxMatmulArgs a, int splits) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (t >= a.M * a.N) return;
@@ -752,12 +761,13 @@ __global__ __launch_bounds__(256) void k_mx_join(const MxMatmulArgs a, int split
   put_one(sink_of(a), t / a.N, t % a.N, v);
 }
 
-// Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it, so
+// Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it (1 x 4096
+// by 11008 x 4096, 24 MB: 6.9 us, 3.5 TB/s, a launch and the packing before the first product), so
 // each block streams 16 rows of B straight to registers, its waves on interleaved K steps of
 // 256, and nothing of B is shared.  v_mfma_scale_f32_16x16x128: lane l holds 32 elements of row
 // l mod 16, block l / 16 of the step.  fp32 / bf16 rows are packed by the block into LDS, eight
 // elements a lane, while its first weights are on their way (a lane packing its own operand's 32
-// elements, with the lanes of absent rows idle, took 12 us of 1 x 4096 by 11008 x 4096, so 8).
+// elements, with the lanes of absent rows idle, took 12 us in that case).
 // The waves' sums meet in LDS, in order.
 constexpr int kFewWaves = 8;
 // LDS of M packed rows: a row is padded by a chunk, so that 16 rows lie on different banks.

@@ -446,7 +446,12 @@ __device__ __forceinline__ void put_token(const LogprobArgs &a, int64_t row, con
 }
 
 // A block a slice.  One slice a row: the row's results; else the slice's statistic and its
-// largest entries in order, for k_logprobs_join.
+// largest entries in order, for k_logprobs_join.  One pass: the maximum of each group is kept, so
+// that the largest entries are looked for in the few groups that can hold them (a thread's maxima
+// bound the k-th largest from below) and not in the row again.  4095 x 50257 bf16 with 20 entries:
+// 91 us, 412 MB at 4.5 TB/s; the vector ALUs are some 70% busy with 12 instructions an entry, and
+// the selection at a row's end is hidden by the other blocks of the CU.  1 x 50257 fp32 in 24
+// slices: 6.5 us, and 3.5 us to join them.
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int slices,
                                                        int64_t each) {
@@ -500,7 +505,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
   }
 }
 
-// A block a row: joins the slices.  With d = ceil(top / slices), the ceil(top / d)-th largest of
+// A block a row: joins the slices; a few dozen KB, bound by latency.  With d = ceil(top / slices), the ceil(top / d)-th largest of
 // the lists' d-th entries has `top` entries at or above it, so smaller ones are left out.  What is
 // left is gathered in LDS, and an entry's place is the number of larger ones there; where more
 // is left than fits (the largest entries all in a few slices), that number is found in every
@@ -809,8 +814,7 @@ __device__ __forceinline__ void put_taught(const DistillArgs &a, int64_t row, co
   put_grad<DT>(a, row * a.ldg + e.id, r.inv_s == 0.0f ? 0.0f : w * (q - e.p * r.scale));
 }
 
-// A block a row: the loss, and the gradient where it is asked for, from a second read of the row
-// (which the Infinity Cache still holds: the rows in flight are some 100 MB).
+// The gradient of a slice, from another read of it.
 template <int DT>
 __device__ __forceinline__ void grad_stream(const DistillArgs &a, int64_t row, const Slice &s,
                                             const RowStat &r, const Taught &t) {
@@ -843,7 +847,11 @@ __device__ __forceinline__ void grad_stream(const DistillArgs &a, int64_t row, c
 // A block a row that its registers hold (T threads, N chunks each): all of it in flight at once,
 // read once, there for the largest entry, the sum and the gradient.  Chunks are counted from the
 // 128-byte line that the row begins in, so that a wave's stores cover whole lines.  The chunks
-// that the row's ends may cut are one more of threads 64 and 128.
+// that the row's ends may cut are one more of threads 64 and 128.  4096 x 50257 bf16, loss and
+// gradient: 190 us, 823 MB at 4.3 TB/s.  What is left is the time between a row's last load and its
+// first store, two joins over the block, which the CU's two other blocks cover in part; an
+// entry's two exponentials come on top of it.  A stream that reads the row again took
+// 259 us, one block of 1024 threads a CU 346 us.
 template <int T, int N>
 struct RowRoom {
   int32_t id[kVocabTop];
@@ -948,7 +956,7 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
   put_taught<DT>(a, row, mine, r, w);
 }
 
-// A block a slice: the slice's statistic.
+// A block a slice: the slice's statistic.  1021 x 131071 bf16: 60 us, 268 MB at 4.5 TB/s.
 template <int DT, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_slices(const DistillArgs a, int slices,
                                                              int64_t each) {
@@ -960,6 +968,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_slices(const DistillArgs a
 }
 
 // A block a row: the slices' statistics in their order, the loss and the gradient's constants.
+// 1021 rows: 11.6 us, the latency of the taught entries' loads and of the joins in 64 bits.
 template <int DT, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, int slices) {
   __shared__ Taught t;
@@ -972,6 +981,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, 
 
 // A block a slice: the gradient from the rows' constants, or (JOIN) from the slices' statistics:
 // every block joins its row's for itself, one kernel less than with the constants in between.
+// 1021 x 131071 bf16: 116 us, 536 MB at 4.6 TB/s; with JOIN, 5 x 50257 fp32: 9.7 us.
 template <int DT, bool JOIN, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, int slices,
                                                            int64_t each) {
@@ -1021,7 +1031,7 @@ constexpr int64_t kRowMax = 1024 * (DT == 0 ? 64 : 128) - 64;
 template <int DT, bool TAIL>
 void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
   const unsigned rows = (unsigned)a.rows;
-  // Three blocks of 256 threads and 26 chunks a CU where a row fits them (4096 x 50257 bf16: 194 us;
+  // Three blocks of 256 threads and 26 chunks a CU where a row fits them (4096 x 50257 bf16: 190 us;
   // two of 512 and 16: 212 us).
   if (slices == 1 && a.vocab <= kRowMax<DT>) {
     if (a.vocab <= 256 * 64 - 64)

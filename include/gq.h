@@ -382,7 +382,7 @@ gq_status gq_token_logprobs(gq_ctx *ctx, const void *logits, int32_t dtype, int6
  *   logits  rows x vocab of `dtype`, row stride ld;  1 <= top <= 128
  *   loss    rows fp32;  stats_or_null  rows x 4 fp32, what gq_distill_grad needs
  *   row_weight_or_null  rows fp32 (NULL: 1);  dlogits_or_null  rows x vocab of `dtype`, row
- *           stride ldd; it may be `logits` itself (with ldd = ld) */
+ *           stride ldd; it may be `logits` itself (with ldd = ld), else the two do not overlap */
 gq_status gq_distill_loss(gq_ctx *ctx, const void *logits, int32_t dtype, int64_t rows,
                           int64_t vocab, int64_t ld, const int32_t *top_ids,
                           const float *top_logprobs, int32_t top, float temperature,
