@@ -31,6 +31,32 @@ def test_longest_slices(vocab):
     assert np.all(np.abs(lps[some].cpu().numpy() - rlps) <= eps + np.abs(rlps) * 2.0 ** -22)
 
 
+@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 65473), (torch.float32, 70001), (torch.bfloat16, 131009)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_long_rows_of_one_slice(dtype, vocab, tail):
+    """Rows that registers do not hold and that are so many that none is cut: a context of its own,
+    whose scratch memory no other call has brought to size."""
+    say("long rows", dtype, vocab, tail)
+    g = gq()
+    rows, top = 1030, 5
+    gen = torch.Generator("cuda").manual_seed(vocab)
+    z = torch.empty(rows, vocab, dtype=dtype, device="cuda").normal_(generator=gen)
+    ids = torch.arange(rows * top, device="cuda", dtype=torch.int32).reshape(rows, top) * 13 % vocab
+    lps = torch.log_softmax(torch.empty(rows, top + 1, device="cuda").normal_(generator=gen), 1)[:, :top].contiguous()
+    ctx = g.Context()
+    w = torch.ones(rows, device="cuda")
+    loss, grad = g.distill_loss(z, ids, lps, 1.0, tail, row_weight=w, ctx=ctx)
+    some = [0, 1, 511, 1029]
+    rl, rg, _ = lm.distill(z[some].float().cpu().numpy(), ids[some].cpu().numpy(), lps[some].cpu().numpy(), 1.0, tail)
+    eps = (vocab / 256 + 64) * 2.0 ** -22
+    assert np.all(np.abs(loss[some].cpu().numpy() - rl) <= eps + np.abs(rl) * 2.0 ** -22)
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23
+    assert np.all(np.abs(grad[some].double().cpu().numpy() - rg) <= (2 * eps + half) * np.abs(rg).max())
+    again, stats = g.distill_loss(z, ids, lps, 1.0, tail, ctx=g.Context())
+    assert torch.equal(again, loss)
+    assert torch.equal(g.distill_grad(z, ids, lps, 1.0, tail, stats, w), grad)
+
+
 def test_most_rows():
     """2^23 rows of one element, both ways: the codes by columns are those of the transpose by rows."""
     say("most rows")
