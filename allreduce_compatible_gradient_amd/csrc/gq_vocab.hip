@@ -1024,9 +1024,12 @@ void logprobs_of(const LogprobArgs &a, int slices, int64_t each, hipStream_t s) 
   if (slices > 1) k_logprobs_join<DT><<<(unsigned)a.rows, kThreads, 0, s>>>(a, slices);
 }
 
-// The longest row that a block's registers hold: 16 chunks of bf16, 8 of fp32 a thread.
+// The longest row that is held in registers: two blocks of 512 threads a CU with 16 chunks of bf16,
+// 8 of fp32 a thread.  One block of 1024 for rows twice as long left the CU idle in its joins: 663
+// x 68328 bf16 84 us, as slices 62 us; 2048 x 40000 fp32 244 and 209; 2000 x 128000 bf16 291 and
+// 325, but its loss alone 203 and 110.
 template <int DT>
-constexpr int64_t kRowMax = 1024 * (DT == 0 ? 64 : 128) - 64;
+constexpr int64_t kRowMax = 512 * (DT == 0 ? 64 : 128) - 64;
 
 // Whether a block's registers hold a row; else its slices, one or more, leave their statistics in
 // the scratch memory.
@@ -1042,16 +1045,14 @@ void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
   if (row_held(slices, a.vocab, DT)) {
     if (a.vocab <= 256 * 64 - 64)
       k_distill_row<DT, TAIL, 256, 8><<<rows, 256, 0, s>>>(a);
-    else if (a.vocab <= 512 * 64 - 64)
+    else if (DT == 0 || a.vocab <= 512 * 64 - 64)
       k_distill_row<DT, TAIL, 512, 8><<<rows, 512, 0, s>>>(a);
-    else if constexpr (DT == 0)
-      k_distill_row<DT, TAIL, 1024, 8><<<rows, 1024, 0, s>>>(a);
-    else if (a.vocab <= 256 * 208 - 64)
-      k_distill_row<DT, TAIL, 256, 26><<<rows, 256, 0, s>>>(a);
-    else if (a.vocab <= 512 * 128 - 64)
-      k_distill_row<DT, TAIL, 512, 16><<<rows, 512, 0, s>>>(a);
-    else
-      k_distill_row<DT, TAIL, 1024, 16><<<rows, 1024, 0, s>>>(a);
+    else if constexpr (DT == 1) {
+      if (a.vocab <= 256 * 208 - 64)
+        k_distill_row<DT, TAIL, 256, 26><<<rows, 256, 0, s>>>(a);
+      else
+        k_distill_row<DT, TAIL, 512, 16><<<rows, 512, 0, s>>>(a);
+    }
     return;
   }
   const unsigned blocks = (unsigned)(a.rows * slices);
