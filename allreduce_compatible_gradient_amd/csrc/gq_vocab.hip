@@ -23,6 +23,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_e4 __attribute__((aligned(4)));
 
@@ -580,7 +581,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(const LogprobArgs a,
 //   dz_v = w T (q_v - p_v) in S,  w T q_v (1 - p_R / q_R) in R
 // q_R is summed over R itself, taught entries becoming -inf on the way, so nothing is subtracted.
 struct Taught {
-  int32_t id[kVocabTop];     // -1: not taught
+  alignas(16) int32_t id[kVocabTop];     // -1: not taught
   float p[kVocabTop];
   uint32_t in_group[kSweeps * kThreads];  // taught entries of each group of the slice
   double sums[kThreads / 64];
@@ -594,7 +595,9 @@ struct RowStat {  // what the gradient needs of a row
   float scale;    // p_j = scale e^(lp_j)
 };
 
-// Loads the row's ids: t.id[j] is -1 where entry j is not taught.
+// Loads the row's ids: t.id[j] is -1 where entry j is not taught.  Comparisons four at a time and
+// without a branch wait for LDS a few times, not once an entry (4096 x 50257 bf16, 64 taught: 190
+// us with a branch each, 180 us so; 33 x 24553 fp32, 128 taught: 30 and 17 us).
 template <typename Room>
 __device__ __forceinline__ bool load_ids(const DistillArgs &a, int64_t row, Room &t) {
   const int tid = threadIdx.x;
@@ -604,9 +607,14 @@ __device__ __forceinline__ bool load_ids(const DistillArgs &a, int64_t row, Room
   bool ok = false;
   if (tid < a.top) {
     const int32_t id = t.id[tid];
-    ok = id >= 0 && id < a.vocab;
-#pragma unroll 8
-    for (int i = 0; i < a.top; ++i) ok = ok && !(i < tid && t.id[i] == id);
+    bool again = false;
+#pragma unroll 4
+    for (int i = 0; i < a.top; i += 4) {  // places past the last are not before tid
+      const i32x4 four = *reinterpret_cast<const i32x4 *>(&t.id[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) again |= (i + j < tid) & (four[j] == id);
+    }
+    ok = id >= 0 && id < a.vocab && !again;
   }
   __syncthreads();
   if (tid < a.top && !ok) t.id[tid] = -1;
@@ -848,13 +856,13 @@ __device__ __forceinline__ void grad_stream(const DistillArgs &a, int64_t row, c
 // read once, there for the largest entry, the sum and the gradient.  Chunks are counted from the
 // 128-byte line that the row begins in, so that a wave's stores cover whole lines.  The chunks
 // that the row's ends may cut are one more of threads 64 and 128.  4096 x 50257 bf16, loss and
-// gradient: 190 us, 823 MB at 4.3 TB/s.  What is left is the time between a row's last load and its
+// gradient: 180 us, 823 MB at 4.6 TB/s.  What is left is the time between a row's last load and its
 // first store, two joins over the block, which the CU's two other blocks cover in part; an
 // entry's two exponentials come on top of it.  A stream that reads the row again took
 // 259 us, one block of 1024 threads a CU 346 us.
 template <int T, int N>
 struct RowRoom {
-  int32_t id[kVocabTop];
+  alignas(16) int32_t id[kVocabTop];
   float p[kVocabTop];
   double sums[T / 64];
   Stat stats[T / 64];
@@ -1040,8 +1048,8 @@ bool row_held(int slices, int64_t vocab, int dtype) {
 template <int DT, bool TAIL>
 void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
   const unsigned rows = (unsigned)a.rows;
-  // Three blocks of 256 threads and 26 chunks a CU where a row fits them (4096 x 50257 bf16: 190 us;
-  // two of 512 and 16: 212 us).
+  // Three blocks of 256 threads and 26 chunks a CU where a row fits them (4096 x 50257 bf16: 194 us
+  // when two of 512 and 16 took 212 us).
   if (row_held(slices, a.vocab, DT)) {
     if (a.vocab <= 256 * 64 - 64)
       k_distill_row<DT, TAIL, 256, 8><<<rows, 256, 0, s>>>(a);
