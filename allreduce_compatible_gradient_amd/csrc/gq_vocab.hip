@@ -580,6 +580,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(const LogprobArgs a,
 //   loss = T^2 (sum p_j (log p_j - log q_j) + p_R (log p_R - log q_R))
 //   dz_v = w T (q_v - p_v) in S,  w T q_v (1 - p_R / q_R) in R
 // q_R is summed over R itself, taught entries becoming -inf on the way, so nothing is subtracted.
+// With m_R the largest logit of R and s_R = sum_R e^(c (z - m_R)) >= 1, R's terms are formed as
+//   log q_R = c (m_R - m) + log s_R - log s,   dz_v = w T e^(c (z_v - m_R)) (q_R - p_R) / s_R
+// so that they stand where q_R is below fp32's range, or below fp64's.
 struct Taught {
   alignas(16) int32_t id[kVocabTop];     // -1: not taught
   float p[kVocabTop];
@@ -588,12 +591,22 @@ struct Taught {
   Stat stats[kThreads / 64];
 };
 
-struct RowStat {  // what the gradient needs of a row
-  float ref;      // largest logit
-  float inv_s;    // 1 / sum e^(c (z - ref)); 0: the row is not taught
-  float rest;     // 1 - p_R / q_R
-  float scale;    // p_j = scale e^(lp_j)
+struct RowStat {   // what the gradient needs of a row
+  float ref;       // largest logit
+  float inv_s;     // 1 / sum e^(c (z - ref)); 0: the row is not taught
+  float rest_ref;  // largest logit of R; without a tail `ref`
+  float rest;      // (q_R - p_R) / s_R; without a tail `inv_s`
+  float scale;     // p_j = scale e^(lp_j); with a tail 1
 };
+
+// As four numbers a row, for a gradient that is taken later.
+__device__ __forceinline__ f32x4 pack_stat(const RowStat &r, bool tail) {
+  return tail ? f32x4{r.ref, r.inv_s, r.rest_ref, r.rest} : f32x4{r.ref, r.inv_s, r.scale, 0.0f};
+}
+
+__device__ __forceinline__ RowStat unpack_stat(f32x4 q, bool tail) {
+  return tail ? RowStat{q.x, q.y, q.z, q.w, 1.0f} : RowStat{q.x, q.y, q.x, q.y, q.z};
+}
 
 // Loads the row's ids: t.id[j] is -1 where entry j is not taught.  Comparisons four at a time and
 // without a branch wait for LDS a few times, not once an entry (4096 x 50257 bf16, 64 taught: 190
@@ -693,8 +706,8 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
   if constexpr (TAIL) m = block_max<T>(mine ? fmaxf(x, rest.m) : rest.m, t.stats);
   const float ref = ref_of(m);
   const double inv_t = 1.0 / (double)a.temperature;
-  const double rest_s =
-      rest.s == 0.0f ? 0.0 : (double)rest.s * exp(((double)ref_of(rest.m) - ref) * inv_t);
+  const double shift = ((double)ref_of(rest.m) - ref) * inv_t;
+  const double rest_s = rest.s == 0.0f ? 0.0 : (double)rest.s * exp(shift);
   double all_s = rest_s;
   if constexpr (TAIL) all_s += block_sum<T>(mine ? (double)exp_of(x - ref, cl) : 0.0, t.sums);
   const double log_s = log(all_s);
@@ -710,19 +723,23 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
   double loss = block_sum<T>(term, t.sums);
   const double taught = block_sum<T>(mine ? 1.0 : 0.0, t.sums);
   // a row masked everywhere has q = 0, not 0 / 0
-  RowStat r = {ref, all_s == 0.0 ? 1.0f : (float)(1.0 / all_s), 1.0f, (float)scale};
-  // no entry is left for the rest, or the student has none there and p_R is the sum's rounding
-  if (TAIL && (taught == (double)a.vocab || (rest_s == 0.0 && p_rest < 0x1p-16))) p_rest = 0.0;
-  if (TAIL && p_rest > 0.0) {
-    const double q_rest = rest_s == 0.0 ? 0.0 : rest_s / all_s;
-    loss += p_rest * log(p_rest / q_rest);
-    r.rest = (float)(1.0 - p_rest / q_rest);
+  const float inv_s = all_s == 0.0 ? 1.0f : (float)(1.0 / all_s);
+  RowStat r = {ref, inv_s, ref, inv_s, (float)scale};
+  if constexpr (TAIL) {
+    // no entry is left for the rest, or q_R is 0 in 64 bits and p_R is the sum's rounding
+    if (taught == (double)a.vocab || (rest_s == 0.0 && p_rest < 0x1p-16)) p_rest = 0.0;
+    if (p_rest > 0.0) {
+      const double log_q = rest.s == 0.0f && all_s == all_s ? -INFINITY : shift + log((double)rest.s) - log_s;
+      loss += p_rest * (log(p_rest) - log_q);
+    }
+    r.rest_ref = ref_of(rest.m);
+    r.rest = rest.s == 0.0f ? 0.0f : (float)((rest_s / all_s - p_rest) / rest.s);
   }
   const bool none = taught == 0.0 || (!TAIL && sum_p == 0.0);
-  if (none) r = RowStat{ref, 0.0f, 0.0f, 0.0f};
+  if (none) r = RowStat{ref, 0.0f, ref, 0.0f, 0.0f};
   if (write && tid == 0) {
     a.loss[row] = none ? 0.0f : (float)(loss * a.temperature * a.temperature);
-    if (a.stats) reinterpret_cast<f32x4 *>(a.stats)[row] = f32x4{r.ref, r.inv_s, r.rest, r.scale};
+    if (a.stats) reinterpret_cast<f32x4 *>(a.stats)[row] = pack_stat(r, TAIL);
   }
   return r;
 }
@@ -747,7 +764,7 @@ __device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// What a row's entries outside S get: f e^(c (z - ref)).
+// What a row's entries outside S get: f e^(c (z - ref)), ref their largest.
 struct RowGrad {
   float f, ref, cl;
   bool plain;  // f is finite; else an entry without probability must not become 0 times it
@@ -758,8 +775,8 @@ __device__ __forceinline__ float row_weight(const DistillArgs &a, int64_t row) {
 }
 
 __device__ __forceinline__ RowGrad row_grad(const DistillArgs &a, const RowStat &r, float w) {
-  const float f = r.inv_s == 0.0f ? 0.0f : w * r.rest * r.inv_s;
-  return RowGrad{f, r.inv_s == 0.0f ? 0.0f : r.ref, a.inv_t * kLog2e, r.inv_s != 0.0f && fabsf(f) < INFINITY};
+  const float f = r.inv_s == 0.0f ? 0.0f : w * r.rest;
+  return RowGrad{f, r.inv_s == 0.0f ? 0.0f : r.rest_ref, a.inv_t * kLog2e, r.inv_s != 0.0f && fabsf(f) < INFINITY};
 }
 
 // Gradient of the chunk whose first entry is entry `at` of the slice; out: the row's gradient.
@@ -1003,8 +1020,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
                                          a.inv_t * kLog2e, t.stats);
     r = finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t, part == 0);
   } else {
-    const f32x4 q = reinterpret_cast<const f32x4 *>(a.stats)[row];
-    r = RowStat{q.x, q.y, q.z, q.w};
+    r = unpack_stat(reinterpret_cast<const f32x4 *>(a.stats)[row], a.tail);
   }
   grad_stream<DT>(a, row, s, r, t);
 }

@@ -374,8 +374,10 @@ gq_status gq_token_logprobs(gq_ctx *ctx, const void *logits, int32_t dtype, int6
  *   tail = 0: p is divided by its sum;            loss = T^2 sum_S p_j (log p_j - log q_j)
  *   tail = 1: the rest is one entry with p_R = max(0, 1 - sum_S p_j), q_R = sum over the rest:
  *             loss = T^2 (sum_S p_j (log p_j - log q_j) + p_R (log p_R - log q_R))
- * (p_R counts as 0 where S is the whole vocabulary, and below 2^-16 where q_R = 0).  A row that
- * is taught nothing has loss 0 and gradient 0.
+ * (p_R counts as 0 where S is the whole vocabulary, and below 2^-16 where q_R is 0 in 64 bits;
+ * log q_R and q_v / q_R are formed from logarithms, so they stand where q_R is that small, and the
+ * loss is infinite only where every entry of the rest is -inf).  A row that is taught nothing has
+ * loss 0 and gradient 0.
  * The gradient of sum_rows w_row loss_row is w T (q_v - p_v) in S and w T q_v (1 - p_R / q_R)
  * elsewhere; with dlogits it is written in the same call (the loss and the gradient have the same
  * bits as from gq_distill_loss without it and gq_distill_grad).

@@ -126,6 +126,13 @@ def distill(z, ids, lps, temperature=1.0, tail=False, weight=None):
         outside[at] = False
         q = np.exp(lq[i])
         q_r = q[outside].sum()
+        # the rest's logarithm and each entry's share of it, also where q_r is below 64 bits' range
+        log_qr, share = -np.inf, np.zeros(vocab)
+        if outside.any() and not np.isneginf(lq[i][outside].max()):
+            top = lq[i][outside].max()
+            share[outside] = np.exp(lq[i][outside] - top)
+            log_qr = top + np.log(share.sum())
+            share /= share.sum()
         p_r = 0.0
         if tail:
             p_r = max(0.0, 1.0 - p.sum()) if outside.any() else 0.0
@@ -139,8 +146,8 @@ def distill(z, ids, lps, temperature=1.0, tail=False, weight=None):
         with np.errstate(all="ignore"):
             loss[i] = temperature ** 2 * (p[p > 0] * (np.log(p[p > 0]) - lq[i, at][p > 0])).sum()
             if p_r > 0:
-                loss[i] += temperature ** 2 * p_r * (np.log(p_r) - np.log(q_r))
-            g = np.where(q > 0, q * (1.0 - (p_r / q_r if p_r > 0 else 0.0)), 0.0)
+                loss[i] += temperature ** 2 * p_r * (np.log(p_r) - log_qr)
+            g = q - p_r * share                      # q (1 - p_R / q_R)
         g[at] = q[at] - p
         grad[i] = g * temperature * (1.0 if weight is None else weight[i])
     return loss, grad, rest
