@@ -596,7 +596,7 @@ struct RowStat {   // what the gradient needs of a row
   float inv_s;     // 1 / sum e^(c (z - ref)); 0: the row is not taught
   float rest_ref;  // largest logit of R; without a tail `ref`
   float rest;      // (q_R - p_R) / s_R; without a tail `inv_s`
-  float scale;     // p_j = scale e^(lp_j); with a tail 1
+  float scale;     // p_j = scale e^(lp_j - shift); with a tail 1
 };
 
 // As four numbers a row, for a gradient that is taken later.
@@ -634,14 +634,28 @@ __device__ __forceinline__ bool load_ids(const DistillArgs &a, int64_t row, Room
   return ok;
 }
 
-// Loads the row's ids and e^(lp); returns the sum of the latter, in 64 bits: p_R is 1 less it.
+struct Mass {    // of a row's taught entries
+  double sum;    // sum of e^(lp - shift), in 64 bits: with a tail p_R is 1 less it
+  double shift;  // with a tail 0
+};
+
+// Loads the row's ids and e^(lp - shift).  Without a tail only the entries' proportions count, so a
+// sum that fp32 cannot hold well (nothing but unlikely entries, or entries that are not divided by
+// their sum) is formed again relative to its largest; what is added for it is one comparison.
 template <int T = kThreads, typename Room>
-__device__ __forceinline__ double load_taught(const DistillArgs &a, int64_t row, Room &t) {
+__device__ __forceinline__ Mass load_taught(const DistillArgs &a, int64_t row, Room &t) {
   const int tid = threadIdx.x;
   const float lp = tid < a.top ? a.top_logprobs[row * a.top + tid] : 0.0f;
-  const double p = load_ids(a, row, t) ? exp((double)lp) : 0.0;
+  const bool ok = load_ids(a, row, t);
+  double p = ok ? exp((double)lp) : 0.0;
+  Mass m = {block_sum<T>(p, t.sums), 0.0};
+  if (!a.tail && !(m.sum >= 0x1p-64 && m.sum <= 0x1p64)) {  // the same in every thread
+    m.shift = ref_of(block_max<T>(ok ? lp : -INFINITY, t.stats));
+    p = ok ? exp((double)lp - m.shift) : 0.0;
+    m.sum = block_sum<T>(p, t.sums);
+  }
   if (tid < a.top) t.p[tid] = (float)p;
-  return block_sum<T>(p, t.sums);
+  return m;
 }
 
 __device__ __forceinline__ int place_in(const Slice &s, int64_t id, int *bit) {
@@ -692,7 +706,7 @@ __device__ __forceinline__ Stat rest_stat(const DistillArgs &a, int64_t row, con
 // terms at most) is held in 64 bits: an error of R's sum then counts q_R - p_R times only.
 template <int DT, bool TAIL, int T, typename Room>
 __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row, Stat rest,
-                                              double sum_p, Room &t, bool write = true) {
+                                              const Mass &mass, Room &t, bool write = true) {
   const int tid = threadIdx.x;
   const float cl = a.inv_t * kLog2e;
   const bool mine = tid < a.top && t.id[tid] >= 0;
@@ -711,11 +725,11 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
   double all_s = rest_s;
   if constexpr (TAIL) all_s += block_sum<T>(mine ? (double)exp_of(x - ref, cl) : 0.0, t.sums);
   const double log_s = log(all_s);
-  double p_rest = TAIL ? fmax(1.0 - sum_p, 0.0) : 0.0;
-  const double scale = TAIL ? 1.0 : 1.0 / sum_p;
+  double p_rest = TAIL ? fmax(1.0 - mass.sum, 0.0) : 0.0;
+  const double scale = TAIL ? 1.0 : 1.0 / mass.sum;
   double term = 0.0;
   if (mine && !(lp == -INFINITY)) {
-    const double log_p = TAIL ? (double)lp : (double)lp - log(sum_p);
+    const double log_p = TAIL ? (double)lp : (double)lp - mass.shift - log(mass.sum);
     const double log_q =
         x == -INFINITY && all_s == all_s ? -INFINITY : ((double)x - ref) * inv_t - log_s;
     term = exp(log_p) * (log_p - log_q);
@@ -735,7 +749,7 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
     r.rest_ref = ref_of(rest.m);
     r.rest = rest.s == 0.0f ? 0.0f : (float)((rest_s / all_s - p_rest) / rest.s);
   }
-  const bool none = taught == 0.0 || (!TAIL && sum_p == 0.0);
+  const bool none = taught == 0.0 || (!TAIL && mass.sum == 0.0);
   if (none) r = RowStat{ref, 0.0f, ref, 0.0f, 0.0f};
   if (write && tid == 0) {
     a.loss[row] = none ? 0.0f : (float)(loss * a.temperature * a.temperature);
@@ -920,7 +934,7 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
   const bool cut = (tid == 64 && (end & 7) != 0) ||
                    (tid == 128 && (s.lead & 7) != 0 && ((s.lead ^ end) & ~7) != 0);
   const int cut_v = (tid == 64 ? end : s.lead) & ~7;
-  const double sum_p = load_taught<T>(a, row, t);
+  const Mass mass = load_taught<T>(a, row, t);
   if constexpr (TAIL) {
     uint32_t *zero = reinterpret_cast<uint32_t *>(t.in_chunk);
     for (int i = tid; i < (N * T + 4) / 4; i += T) zero[i] = 0;
@@ -965,7 +979,7 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
     for (int i = 0; i < 8; ++i) sum[i & 1] += exp_of(x.get(i) - ref, cl);
   }
   const Stat rest = {m, (float)block_sum<T>((double)(sum[0] + sum[1]), t.sums), 0.0f};
-  const RowStat r = finish_row<DT, TAIL, T>(a, row, rest, sum_p, t);
+  const RowStat r = finish_row<DT, TAIL, T>(a, row, rest, mass, t);
   if (!a.grad) return;
   const TaughtEntry mine = taught_entry<DT>(a, s, t);
   __syncthreads();
@@ -998,10 +1012,10 @@ template <int DT, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, int slices) {
   __shared__ Taught t;
   const int64_t row = blockIdx.x;
-  const double sum_p = load_taught(a, row, t);
+  const Mass mass = load_taught(a, row, t);
   const Stat rest = join_slices<false>(static_cast<const Stat *>(a.scratch) + row * slices, slices,
                                        a.inv_t * kLog2e, t.stats);
-  finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t);
+  finish_row<DT, TAIL, kThreads>(a, row, rest, mass, t);
 }
 
 // A block a slice: the gradient from the rows' constants, or (JOIN) from the slices' statistics:
@@ -1013,12 +1027,12 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
   __shared__ Taught t;
   const int64_t row = blockIdx.x / slices, part = blockIdx.x % slices;
   const Slice s = slice_of(a.logits, DT == 0 ? 4 : 2, row, a.ld, a.vocab, part, each);
-  const double sum_p = load_taught(a, row, t);
+  const Mass mass = load_taught(a, row, t);
   RowStat r;
   if constexpr (JOIN) {
     const Stat rest = join_slices<false>(static_cast<const Stat *>(a.scratch) + row * slices, slices,
                                          a.inv_t * kLog2e, t.stats);
-    r = finish_row<DT, TAIL, kThreads>(a, row, rest, sum_p, t, part == 0);
+    r = finish_row<DT, TAIL, kThreads>(a, row, rest, mass, t, part == 0);
   } else {
     r = unpack_stat(reinterpret_cast<const f32x4 *>(a.stats)[row], a.tail);
   }

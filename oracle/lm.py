@@ -121,7 +121,10 @@ def distill(z, ids, lps, temperature=1.0, tail=False, weight=None):
         if not keep:
             continue
         at = np.asarray(ids[i])[keep].astype(int)
-        p = np.exp(np.asarray(lps[i], np.float64)[keep])
+        lp = np.asarray(lps[i], np.float64)[keep]
+        if not tail and lp.max() > -np.inf:
+            lp = lp - lp.max()                       # only proportions count
+        p = np.exp(lp)
         outside = np.ones(vocab, bool)
         outside[at] = False
         q = np.exp(lq[i])

@@ -23,3 +23,12 @@ def test_distill_bucket_far_below(gap):
         down[0, v] -= h
         d = (lm.distill(up, ids, np.log(p), 1.0, True)[0] - lm.distill(down, ids, np.log(p), 1.0, True)[0]) / (2 * h)
         assert abs(d[0] - grad[0, v]) < 1e-6
+
+
+@pytest.mark.parametrize("level", [-2000.0, -100.0, 100.0, 2000.0])
+def test_distill_without_a_tail_knows_proportions_only(level):
+    rng = np.random.default_rng(5)
+    z, lps = rng.normal(size=(1, 8)), np.log([[0.5, 0.3, 0.2]])
+    ids = np.array([[4, 0, 6]])
+    want, got = (lm.distill(z, ids, lps + c, 1.5, False) for c in (0.0, level))
+    assert np.allclose(got[0], want[0], rtol=1e-10) and np.allclose(got[1], want[1], atol=1e-10)
