@@ -578,10 +578,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(const LogprobArgs a,
 // the rest: p_j = e^(lp_j), divided by their sum unless the rest has a bucket of its own, whose
 // mass p_R = 1 - sum p_j is matched with q_R = sum of q over R.
 //   loss = T^2 (sum p_j (log p_j - log q_j) + p_R (log p_R - log q_R))
-//   dz_v = w T (q_v - p_v) in S,  w T q_v (1 - p_R / q_R) in R
+//   dz_v = w T (P q_v - p_v) in S,  w T q_v (P - p_R / q_R) in R,  P = sum p_j + p_R
+// P is 1 unless, with a tail, p_R counts as 0 or the entries sum to more than 1.
 // q_R is summed over R itself, taught entries becoming -inf on the way, so nothing is subtracted.
 // With m_R the largest logit of R and s_R = sum_R e^(c (z - m_R)) >= 1, R's terms are formed as
-//   log q_R = c (m_R - m) + log s_R - log s,   dz_v = w T e^(c (z_v - m_R)) (q_R - p_R) / s_R
+//   log q_R = c (m_R - m) + log s_R - log s,   dz_v = w T e^(c (z_v - m_R)) (P q_R - p_R) / s_R
 // so that they stand where q_R is below fp32's range, or below fp64's.
 struct Taught {
   alignas(16) int32_t id[kVocabTop];     // -1: not taught
@@ -593,9 +594,9 @@ struct Taught {
 
 struct RowStat {   // what the gradient needs of a row
   float ref;       // largest logit
-  float inv_s;     // 1 / sum e^(c (z - ref)); 0: the row is not taught
+  float inv_s;     // P / sum e^(c (z - ref)); 0: the row is not taught
   float rest_ref;  // largest logit of R; without a tail `ref`
-  float rest;      // (q_R - p_R) / s_R; without a tail `inv_s`
+  float rest;      // (P q_R - p_R) / s_R; without a tail `inv_s`
   float scale;     // p_j = scale e^(lp_j - shift); with a tail 1
 };
 
@@ -746,8 +747,10 @@ __device__ __forceinline__ RowStat finish_row(const DistillArgs &a, int64_t row,
       const double log_q = rest.s == 0.0f && all_s == all_s ? -INFINITY : shift + log((double)rest.s) - log_s;
       loss += p_rest * (log(p_rest) - log_q);
     }
+    const double p = mass.sum + p_rest;
+    r.inv_s = all_s == 0.0 ? (float)p : (float)(p / all_s);
     r.rest_ref = ref_of(rest.m);
-    r.rest = rest.s == 0.0f ? 0.0f : (float)((rest_s / all_s - p_rest) / rest.s);
+    r.rest = rest.s == 0.0f ? 0.0f : (float)((p * (rest_s / all_s) - p_rest) / rest.s);
   }
   const bool none = taught == 0.0 || (!TAIL && mass.sum == 0.0);
   if (none) r = RowStat{ref, 0.0f, ref, 0.0f, 0.0f};

@@ -376,11 +376,12 @@ gq_status gq_token_logprobs(gq_ctx *ctx, const void *logits, int32_t dtype, int6
  *             loss = T^2 (sum_S p_j (log p_j - log q_j) + p_R (log p_R - log q_R))
  * (p_R counts as 0 where S is the whole vocabulary, and below 2^-16 where q_R is 0 in 64 bits;
  * log q_R and q_v / q_R are formed from logarithms, so they stand where q_R is that small, and the
- * loss is infinite only where every entry of the rest is -inf).  A row that is taught nothing has
+ * rest makes the loss infinite only where every entry of it is -inf).  A row that is taught nothing has
  * loss 0 and gradient 0.
- * The gradient of sum_rows w_row loss_row is w T (q_v - p_v) in S and w T q_v (1 - p_R / q_R)
- * elsewhere; with dlogits it is written in the same call (the loss and the gradient have the same
- * bits as from gq_distill_loss without it and gq_distill_grad).
+ * The gradient of sum_rows w_row loss_row is w T (P q_v - p_v) in S and w T q_v (P - p_R / q_R)
+ * elsewhere, P = sum_S p + p_R (which is 1 unless p_R counts as 0 or the entries sum to more than 1);
+ * with dlogits it is written in the same call (the loss and the gradient have the same bits as
+ * from gq_distill_loss without it and gq_distill_grad).
  *   logits  rows x vocab of `dtype`, row stride ld;  1 <= top <= 128
  *   loss    rows fp32;  stats_or_null  rows x 4 fp32, what gq_distill_grad needs
  *   row_weight_or_null  rows fp32 (NULL: 1);  dlogits_or_null  rows x vocab of `dtype`, row

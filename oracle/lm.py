@@ -150,7 +150,7 @@ def distill(z, ids, lps, temperature=1.0, tail=False, weight=None):
             loss[i] = temperature ** 2 * (p[p > 0] * (np.log(p[p > 0]) - lq[i, at][p > 0])).sum()
             if p_r > 0:
                 loss[i] += temperature ** 2 * p_r * (np.log(p_r) - log_qr)
-            g = q - p_r * share                      # q (1 - p_R / q_R)
-        g[at] = q[at] - p
+            g = (p.sum() + p_r) * q - p_r * share    # q (P - p_R / q_R)
+        g[at] = (p.sum() + p_r) * q[at] - p
         grad[i] = g * temperature * (1.0 if weight is None else weight[i])
     return loss, grad, rest

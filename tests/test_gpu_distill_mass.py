@@ -76,3 +76,22 @@ def test_nothing_but_impossible_entries():
     lps = np.full((2, 3), -np.inf, np.float32)
     lps[1, 1] = -2000.0
     check(z, ids, lps, False)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", SHAPES)
+@pytest.mark.parametrize("total", [0.4, 1.5, 7.0])
+def test_tail_with_any_mass(rows, vocab, dtype, total):
+    """The gradient is the loss's derivative also where the entries sum to more than one."""
+    say("distill tail mass", rows, vocab, dtype, total)
+    z, ids, rng = rows_of(rows, vocab, dtype, 6, 9)
+    p = rng.random((rows, 6)) + 0.1
+    check(z, ids, np.log(total * p / p.sum(1, keepdims=True)).astype(np.float32), True, 1.5)
+
+
+@pytest.mark.parametrize("total", [0.4, 1.0, 1.5])
+def test_tail_without_a_rest(total):
+    """The whole vocabulary is taught: no entry is left for the bucket."""
+    say("distill whole vocabulary", total)
+    z, ids, rng = rows_of(4, 9, torch.float32, 9, 10)
+    p = rng.random((4, 9)) + 0.1
+    check(z, ids, np.log(total * p / p.sum(1, keepdims=True)).astype(np.float32), True, 1.5)

@@ -32,3 +32,19 @@ def test_distill_without_a_tail_knows_proportions_only(level):
     ids = np.array([[4, 0, 6]])
     want, got = (lm.distill(z, ids, lps + c, 1.5, False) for c in (0.0, level))
     assert np.allclose(got[0], want[0], rtol=1e-10) and np.allclose(got[1], want[1], atol=1e-10)
+
+
+@pytest.mark.parametrize("vocab,total", [(12, 0.4), (12, 1.5), (5, 0.4), (5, 1.0), (5, 1.5)])
+def test_distill_gradient_with_any_mass(vocab, total):
+    """Entries that sum to less or more than one, with a rest and (5 of 5 taught) without."""
+    rng = np.random.default_rng(6)
+    z, p = rng.normal(size=(1, vocab)), rng.random((1, 5)) + 0.1
+    ids, lps = np.arange(5)[None], np.log(total * p / p.sum())
+    _, grad, _ = lm.distill(z, ids, lps, 1.5, True)
+    h = 1e-5
+    for v in range(vocab):
+        up, down = z.copy(), z.copy()
+        up[0, v] += h
+        down[0, v] -= h
+        d = (lm.distill(up, ids, lps, 1.5, True)[0] - lm.distill(down, ids, lps, 1.5, True)[0]) / (2 * h)
+        assert abs(d[0] - grad[0, v]) < 1e-8
