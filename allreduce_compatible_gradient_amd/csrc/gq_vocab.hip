@@ -429,7 +429,8 @@ __device__ __forceinline__ void put_top(const LogprobArgs &a, int64_t row, int p
   const float x = key_value((uint32_t)(key >> 32));
   const float d = (x - ref) * a.inv_t - log_s;
   a.top_ids[row * a.top + place] = (int32_t)~(uint32_t)key;
-  a.top_logprobs[row * a.top + place] = x == -INFINITY ? -INFINITY : d;
+  // a masked entry; in a row whose sum is NaN it is NaN like the others
+  a.top_logprobs[row * a.top + place] = x == -INFINITY && log_s == log_s ? -INFINITY : d;
 }
 
 template <int DT>
