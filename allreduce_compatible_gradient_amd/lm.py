@@ -21,6 +21,18 @@ def _code(dtype: torch.dtype) -> int:
     raise TypeError("float32 or bfloat16 expected, got %s" % dtype)
 
 
+def _laid(t: Optional[torch.Tensor], strided: bool = False) -> Optional[torch.Tensor]:
+    """t, or a copy of it where the library does not take it as it lies: no gaps (``strided``: none
+    within a row) and 16-byte alignment.  Views come at any element: rows after the first of an odd
+    length, pieces of a flat buffer, the gradients of a torch.cat."""
+    if t is None:
+        return None
+    rows = strided and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]
+    if (rows or t.is_contiguous()) and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class _Linear(torch.autograd.Function):
     """y = x W^T + b.  Activations and weights are rounded to nearest, along the products' inner
     axis: by rows for y, by columns for dX = dY W and dW = dY^T X.  dY is rounded stochastically,
@@ -28,12 +40,12 @@ class _Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, seed, worker):
-        qx, qxt = gq.mx_quantize(x, by_cols=ctx.needs_input_grad[1])
-        qw, qwt = gq.mx_quantize(weight, by_cols=ctx.needs_input_grad[0])
+        qx, qxt = gq.mx_quantize(_laid(x, strided=True), by_cols=ctx.needs_input_grad[1])
+        qw, qwt = gq.mx_quantize(_laid(weight, strided=True), by_cols=ctx.needs_input_grad[0])
         ctx.operands = qxt, qwt
         ctx.draws = seed, worker
         ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
-        return gq.mx_matmul(qx, qw, bias=None if bias is None else bias.float(),
+        return gq.mx_matmul(qx, qw, bias=None if bias is None else _laid(bias.float()),
                             out_dtype=_code(x.dtype))
 
     @staticmethod
@@ -43,7 +55,7 @@ class _Linear(torch.autograd.Function):
         dtype_x, dtype_w, dtype_b = ctx.dtypes
         dx = dw = db = None
         if need_x or need_w:
-            q, qt = gq.mx_quantize(dy.contiguous(), gq.MX_STOCHASTIC, *ctx.draws, by_rows=need_x,
+            q, qt = gq.mx_quantize(_laid(dy), gq.MX_STOCHASTIC, *ctx.draws, by_rows=need_x,
                                    by_cols=need_w)
             if need_x:
                 dx = gq.mx_matmul(q, qwt, out_dtype=_code(dtype_x))
@@ -64,7 +76,8 @@ def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_ids, top_logprobs, temperature, tail):
-        logits = logits.detach()
+        logits = _laid(logits.detach(), strided=True)
+        top_ids, top_logprobs = _laid(top_ids), _laid(top_logprobs)
         loss, stats = gq.distill_loss(logits, top_ids, top_logprobs, temperature, tail)
         ctx.save_for_backward(logits, top_ids, top_logprobs, stats)
         ctx.form = temperature, tail
@@ -74,7 +87,7 @@ class _Distill(torch.autograd.Function):
     def backward(ctx, grad_loss):
         logits, top_ids, top_logprobs, stats = ctx.saved_tensors
         return gq.distill_grad(logits, top_ids, top_logprobs, *ctx.form, stats,
-                               grad_loss.float().contiguous()), None, None, None, None
+                               _laid(grad_loss.float())), None, None, None, None
 
 
 def distill(logits: torch.Tensor, top_ids: torch.Tensor, top_logprobs: torch.Tensor,

@@ -1,0 +1,43 @@
+"""The autograd functions on tensors that begin at any element: the same bits as from whole copies."""
+import pytest
+import torch
+
+from tests.gpu_helpers import gq, say
+
+pytestmark = pytest.mark.gpu
+
+
+def parts(*shape, seed=0, dtype=torch.float32):
+    return torch.randn(*shape, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_outputs_joined(dtype):
+    from allreduce_compatible_gradient_amd import lm
+    say("lm cat", dtype)
+    g = gq()
+    w = parts(7, 45, seed=1).requires_grad_()
+    x = [parts(n, 45, seed=n, dtype=dtype).requires_grad_() for n in (5, 6)]
+    weight = parts(11, 7, seed=4, dtype=dtype)
+    got = torch.autograd.grad((torch.cat([lm.mx_linear(t, w, seed=9) for t in x]) * weight).sum(), [w] + x)
+    each = [torch.autograd.grad(lm.mx_linear(t, w, seed=9), (t, w), d.clone()) for t, d in zip(x, weight.split([5, 6]))]
+    assert torch.equal(got[1], each[0][0]) and torch.equal(got[2], each[1][0])
+    assert torch.equal(got[0], each[0][1] + each[1][1])
+    z = [parts(n, 333, seed=n, dtype=dtype).requires_grad_() for n in (5, 7)]
+    teacher = [g.token_logprobs(parts(n, 333, seed=20 + n), torch.zeros(n, dtype=torch.int64, device="cuda"), 9)[2:]
+               for n in (5, 7)]
+    weight = parts(12, seed=8)
+    got = torch.autograd.grad((torch.cat([lm.distill(t, *a, tail=True) for t, a in zip(z, teacher)]) * weight).sum(), z)
+    for d, t, a, v in zip(got, z, teacher, weight.split([5, 7])):
+        assert torch.equal(d, g.distill_loss(t.detach(), *a, tail=True, row_weight=v.clone())[1])
+
+
+def test_views():
+    from allreduce_compatible_gradient_amd import lm
+    say("lm views")
+    flat = parts(1 + 63 + 7, seed=1)
+    w, b = flat[1:64].view(7, 9), flat[64:]
+    for x in (parts(6, 9, seed=3)[1:], parts(9, 12, seed=2).T, parts(6, 13, seed=4)[:, 2:11]):
+        assert torch.equal(lm.mx_linear(x, w, b), lm.mx_linear(x.clone(memory_format=torch.contiguous_format), w.clone(), b.clone()))
+    z, ids, lps = parts(6, 333, seed=6), torch.arange(30, dtype=torch.int32, device="cuda").view(6, 5), parts(6, 5, seed=7)
+    assert torch.equal(lm.distill(z[1:], ids[1:], lps[1:]), lm.distill(z, ids, lps)[1:])
