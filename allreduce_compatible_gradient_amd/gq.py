@@ -503,7 +503,7 @@ def _rows(t: torch.Tensor, name: str, dtype=None):
         raise ValueError("%s must be a matrix" % name)
     rows, cols = t.shape
     ld, inner = t.stride()
-    if inner != 1 and cols > 1:
+    if inner != 1 and cols > 1 and rows > 0:
         raise ValueError("%s must be a matrix with contiguous rows" % name)
     return t.data_ptr(), (ld if rows > 1 else max(ld, cols))
 

@@ -44,6 +44,7 @@ class _Linear(torch.autograd.Function):
         qw, qwt = gq.mx_quantize(_laid(weight, strided=True), by_cols=ctx.needs_input_grad[0])
         ctx.operands = qxt, qwt
         ctx.draws = seed, worker
+        ctx.device, ctx.shape = weight.device, weight.shape
         ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
         return gq.mx_matmul(qx, qw, bias=None if bias is None else _laid(bias.float()),
                             out_dtype=_code(x.dtype))
@@ -59,7 +60,9 @@ class _Linear(torch.autograd.Function):
                                    by_cols=need_w)
             if need_x:
                 dx = gq.mx_matmul(q, qwt, out_dtype=_code(dtype_x))
-            if need_w:
+            if need_w and len(dy) == 0:  # a product has at least one column
+                dw = torch.zeros(ctx.shape, dtype=dtype_w, device=ctx.device)
+            elif need_w:
                 dw = gq.mx_matmul(qt, qxt, out_dtype=_code(dtype_w))
         if need_b:
             db = dy.float().sum(0).to(dtype_b)

@@ -41,3 +41,17 @@ def test_views():
         assert torch.equal(lm.mx_linear(x, w, b), lm.mx_linear(x.clone(memory_format=torch.contiguous_format), w.clone(), b.clone()))
     z, ids, lps = parts(6, 333, seed=6), torch.arange(30, dtype=torch.int32, device="cuda").view(6, 5), parts(6, 5, seed=7)
     assert torch.equal(lm.distill(z[1:], ids[1:], lps[1:]), lm.distill(z, ids, lps)[1:])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_no_tokens(dtype):
+    from allreduce_compatible_gradient_amd import lm
+    say("lm no tokens", dtype)
+    x, w, b = (parts(*s, dtype=d).requires_grad_() for s, d in (((0, 45), dtype), ((7, 45), torch.float32), ((7,), torch.float32)))
+    y = lm.mx_linear(x, w, b)
+    assert y.shape == (0, 7) and y.dtype == dtype
+    dx, dw, db = torch.autograd.grad(y.sum(), (x, w, b))
+    assert dx.shape == x.shape and dw.shape == w.shape and not dw.any() and not db.any()
+    z = parts(0, 333, dtype=dtype).requires_grad_()
+    loss = lm.distill(z, torch.zeros(0, 3, dtype=torch.int32, device="cuda"), torch.zeros(0, 3, device="cuda"), tail=True)
+    assert loss.shape == (0,) and torch.autograd.grad(loss.sum(), z)[0].shape == z.shape

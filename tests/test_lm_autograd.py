@@ -113,3 +113,15 @@ def test_inputs_that_start_anywhere(calls):
         got, = torch.autograd.grad(lm.distill(z, *teacher, 2.0).sum(), z)
         want, = torch.autograd.grad(plain_distill(z, *teacher, 2.0).sum(), z)
         assert torch.allclose(got, want, atol=1e-5)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_no_tokens(calls, bias):
+    """An empty batch leaves gradients of zero."""
+    x, w = parts(0, 9).requires_grad_(), parts(7, 9).requires_grad_()
+    b = parts(7).requires_grad_() if bias else None
+    y = lm.mx_linear(x, w, b)
+    assert y.shape == (0, 7)
+    dx, dw, *db = torch.autograd.grad(y.sum(), [t for t in (x, w, b) if t is not None])
+    assert dx.shape == (0, 9) and dw.shape == (7, 9) and dw.dtype == w.dtype and not dw.any()
+    assert all(d.shape == (7,) and not d.any() for d in db)
