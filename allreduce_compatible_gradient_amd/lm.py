@@ -2,7 +2,8 @@
 
 Two functions over the library's operators (``gq``): a linear layer whose three products run on
 microscaled 4-bit operands, and the distillation loss from a teacher's top log probabilities.
-The gradients they leave on fp32 master weights are what the gradient quantisers exchange.
+The gradients they leave on fp32 master weights are what the gradient quantisers exchange.  They
+are differentiable once: a derivative of their gradients raises.
 """
 from __future__ import annotations
 
@@ -33,6 +34,27 @@ def _laid(t: Optional[torch.Tensor], strided: bool = False) -> Optional[torch.Te
     return t.clone(memory_format=torch.contiguous_format)
 
 
+class _Once(torch.autograd.Function):
+    """A gradient as it is, hanging on what it was made of: taking its derivative raises, where
+    without a graph its terms would be missing from what it is added to."""
+
+    @staticmethod
+    def forward(ctx, grad, *made_of):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("mx_linear and distill are differentiable once: their gradients have no derivative")
+
+
+def _once(ctx, incoming, grad):
+    """A gradient that a backward pass returns.  What the node's inputs are is reached through its
+    own empty second output, which holds none of their memory."""
+    if grad is None or not torch.is_grad_enabled():
+        return grad
+    return _Once.apply(grad, incoming, *ctx.saved_tensors[:1])
+
+
 class _Linear(torch.autograd.Function):
     """y = x W^T + b.  Activations and weights are rounded to nearest, along the products' inner
     axis: by rows for y, by columns for dX = dY W and dW = dY^T X.  dY is rounded stochastically,
@@ -46,11 +68,13 @@ class _Linear(torch.autograd.Function):
         ctx.draws = seed, worker
         ctx.device, ctx.shape = weight.device, weight.shape
         ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
+        link = torch.empty(0, device=weight.device)
+        ctx.save_for_backward(link)
         return gq.mx_matmul(qx, qw, bias=None if bias is None else _laid(bias.float()),
-                            out_dtype=_code(x.dtype))
+                            out_dtype=_code(x.dtype)), link
 
     @staticmethod
-    def backward(ctx, dy):
+    def backward(ctx, dy, _):
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
         qxt, qwt = ctx.operands
         dtype_x, dtype_w, dtype_b = ctx.dtypes
@@ -66,14 +90,14 @@ class _Linear(torch.autograd.Function):
                 dw = gq.mx_matmul(qt, qxt, out_dtype=_code(dtype_w))
         if need_b:
             db = dy.float().sum(0).to(dtype_b)
-        return dx, dw, db, None, None
+        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None
 
 
 def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
               seed: int = 0, worker: int = 0) -> torch.Tensor:
     """A linear layer (x: tokens x in, weight: out x in) in microscaled 4-bit floating point.
     ``seed`` has to differ from one step and layer to the next; workers draw apart by ``worker``."""
-    return _Linear.apply(x, weight, bias, seed, worker)
+    return _Linear.apply(x, weight, bias, seed, worker)[0]
 
 
 class _Distill(torch.autograd.Function):
@@ -82,18 +106,19 @@ class _Distill(torch.autograd.Function):
         logits = _laid(logits.detach(), strided=True)
         top_ids, top_logprobs = _laid(top_ids), _laid(top_logprobs)
         loss, stats = gq.distill_loss(logits, top_ids, top_logprobs, temperature, tail)
-        ctx.save_for_backward(logits, top_ids, top_logprobs, stats)
+        link = torch.empty(0, device=logits.device)
+        ctx.save_for_backward(link, logits, top_ids, top_logprobs, stats)
         ctx.form = temperature, tail
-        return loss
+        return loss, link
 
     @staticmethod
-    def backward(ctx, grad_loss):
-        logits, top_ids, top_logprobs, stats = ctx.saved_tensors
-        return gq.distill_grad(logits, top_ids, top_logprobs, *ctx.form, stats,
-                               _laid(grad_loss.float())), None, None, None, None
+    def backward(ctx, grad_loss, _):
+        _, logits, top_ids, top_logprobs, stats = ctx.saved_tensors
+        d = gq.distill_grad(logits, top_ids, top_logprobs, *ctx.form, stats, _laid(grad_loss.float()))
+        return _once(ctx, grad_loss, d), None, None, None, None
 
 
 def distill(logits: torch.Tensor, top_ids: torch.Tensor, top_logprobs: torch.Tensor,
             temperature: float = 1.0, tail: bool = False) -> torch.Tensor:
     """Each row's distillation loss (gq.distill_loss), differentiable in ``logits``."""
-    return _Distill.apply(logits, top_ids, top_logprobs, temperature, tail)
+    return _Distill.apply(logits, top_ids, top_logprobs, temperature, tail)[0]

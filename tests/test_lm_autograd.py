@@ -125,3 +125,43 @@ def test_no_tokens(calls, bias):
     dx, dw, *db = torch.autograd.grad(y.sum(), [t for t in (x, w, b) if t is not None])
     assert dx.shape == (0, 9) and dw.shape == (7, 9) and dw.dtype == w.dtype and not dw.any()
     assert all(d.shape == (7,) and not d.any() for d in db)
+
+
+def test_derivatives_of_gradients_raise(calls):
+    """The backward passes have no derivative of their own.  A gradient that is used as a number is
+    as before; a derivative that reaches it, by whatever way, raises and does not leave it out."""
+    x, w = parts(4, 9, seed=1).requires_grad_(), parts(7, 9, seed=2).requires_grad_()
+    v = parts(7, seed=3).requires_grad_()
+    for loss in (lambda y: y.sum(), lambda y: y.square().sum(), lambda y: (y * v).sum()):
+        dx, dw = torch.autograd.grad(loss(lm.mx_linear(x, w)), (x, w), create_graph=True)
+        want = torch.autograd.grad(loss(x @ w.T), (x, w))
+        assert torch.allclose(dx, want[0], atol=1e-5) and torch.allclose(dw, want[1], atol=1e-5)
+        for of, to in ((dx, w), (dw, x), (dx, x)):
+            with pytest.raises(RuntimeError, match="differentiable once"):
+                torch.autograd.grad(of.square().sum() + to.sum(), to, retain_graph=True)
+    z, ids, lps = parts(4, 33).requires_grad_(), torch.arange(12, dtype=torch.int32).view(4, 3), parts(4, 3)
+    dz, = torch.autograd.grad(lm.distill(z, ids, lps).sum(), z, create_graph=True)
+    assert torch.allclose(dz, torch.autograd.grad(plain_distill(z, ids, lps, 1.0).sum(), z)[0], atol=1e-5)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(dz.square().sum() + z.sum(), z)
+
+
+def test_derivative_through_the_incoming_gradient_raises(calls):
+    """v weighs the outputs, so the gradient of x depends on it through what arrives."""
+    x, w, v = parts(4, 9).requires_grad_(), parts(7, 9).requires_grad_(), parts(7).requires_grad_()
+    dx, = torch.autograd.grad((lm.mx_linear(x, w) * v).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(dx.square().sum() + v.sum(), v)
+
+
+def test_gradients_hold_none_of_the_activations(calls):
+    """Between the passes a layer keeps its packed operands, not its input."""
+    import weakref
+    w = parts(7, 9, seed=2).requires_grad_()
+    x = parts(4, 9, seed=1) * 2
+    alive = weakref.ref(x)
+    y = lm.mx_linear(x, w)
+    del x
+    assert alive() is None
+    y.sum().backward()
+    assert w.grad.shape == w.shape
