@@ -4,6 +4,10 @@ Two functions over the library's operators (``gq``): a linear layer whose three 
 microscaled 4-bit operands, and the distillation loss from a teacher's top log probabilities.
 The gradients they leave on fp32 master weights are what the gradient quantisers exchange.  They
 are differentiable once: a derivative of their gradients raises.
+
+``ctx`` is the library's context of a call and of its backward pass; by default it is gq.context()
+of the thread that runs each, which all streams share.  Work on two streams at the same time needs
+a gq.Context for each: the calls' scratch memory is the context's.
 """
 from __future__ import annotations
 
@@ -61,17 +65,17 @@ class _Linear(torch.autograd.Function):
     both ways in one read, so that the gradients are unbiased in it."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, seed, worker):
-        qx, qxt = gq.mx_quantize(_laid(x, strided=True), by_cols=ctx.needs_input_grad[1])
-        qw, qwt = gq.mx_quantize(_laid(weight, strided=True), by_cols=ctx.needs_input_grad[0])
+    def forward(ctx, x, weight, bias, seed, worker, context):
+        qx, qxt = gq.mx_quantize(_laid(x, strided=True), by_cols=ctx.needs_input_grad[1], ctx=context)
+        qw, qwt = gq.mx_quantize(_laid(weight, strided=True), by_cols=ctx.needs_input_grad[0], ctx=context)
         ctx.operands = qxt, qwt
-        ctx.draws = seed, worker
+        ctx.draws, ctx.context = (seed, worker), context
         ctx.device, ctx.shape = weight.device, weight.shape
         ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
         link = torch.empty(0, device=weight.device)
         ctx.save_for_backward(link)
         return gq.mx_matmul(qx, qw, bias=None if bias is None else _laid(bias.float()),
-                            out_dtype=_code(x.dtype)), link
+                            out_dtype=_code(x.dtype), ctx=context), link
 
     @staticmethod
     def backward(ctx, dy, _):
@@ -81,44 +85,46 @@ class _Linear(torch.autograd.Function):
         dx = dw = db = None
         if need_x or need_w:
             q, qt = gq.mx_quantize(_laid(dy), gq.MX_STOCHASTIC, *ctx.draws, by_rows=need_x,
-                                   by_cols=need_w)
+                                   by_cols=need_w, ctx=ctx.context)
             if need_x:
-                dx = gq.mx_matmul(q, qwt, out_dtype=_code(dtype_x))
+                dx = gq.mx_matmul(q, qwt, out_dtype=_code(dtype_x), ctx=ctx.context)
             if need_w and len(dy) == 0:  # a product has at least one column
                 dw = torch.zeros(ctx.shape, dtype=dtype_w, device=ctx.device)
             elif need_w:
-                dw = gq.mx_matmul(qt, qxt, out_dtype=_code(dtype_w))
+                dw = gq.mx_matmul(qt, qxt, out_dtype=_code(dtype_w), ctx=ctx.context)
         if need_b:
             db = dy.float().sum(0).to(dtype_b)
-        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None
+        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None, None
 
 
 def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
-              seed: int = 0, worker: int = 0) -> torch.Tensor:
+              seed: int = 0, worker: int = 0, ctx: Optional[gq.Context] = None) -> torch.Tensor:
     """A linear layer (x: tokens x in, weight: out x in) in microscaled 4-bit floating point.
     ``seed`` has to differ from one step and layer to the next; workers draw apart by ``worker``."""
-    return _Linear.apply(x, weight, bias, seed, worker)[0]
+    return _Linear.apply(x, weight, bias, seed, worker, ctx)[0]
 
 
 class _Distill(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, top_ids, top_logprobs, temperature, tail):
+    def forward(ctx, logits, top_ids, top_logprobs, temperature, tail, context):
         logits = _laid(logits.detach(), strided=True)
         top_ids, top_logprobs = _laid(top_ids), _laid(top_logprobs)
-        loss, stats = gq.distill_loss(logits, top_ids, top_logprobs, temperature, tail)
+        loss, stats = gq.distill_loss(logits, top_ids, top_logprobs, temperature, tail, ctx=context)
         link = torch.empty(0, device=logits.device)
         ctx.save_for_backward(link, logits, top_ids, top_logprobs, stats)
-        ctx.form = temperature, tail
+        ctx.form, ctx.context = (temperature, tail), context
         return loss, link
 
     @staticmethod
     def backward(ctx, grad_loss, _):
         _, logits, top_ids, top_logprobs, stats = ctx.saved_tensors
-        d = gq.distill_grad(logits, top_ids, top_logprobs, *ctx.form, stats, _laid(grad_loss.float()))
-        return _once(ctx, grad_loss, d), None, None, None, None
+        d = gq.distill_grad(logits, top_ids, top_logprobs, *ctx.form, stats, _laid(grad_loss.float()),
+                            ctx=ctx.context)
+        return _once(ctx, grad_loss, d), None, None, None, None, None
 
 
 def distill(logits: torch.Tensor, top_ids: torch.Tensor, top_logprobs: torch.Tensor,
-            temperature: float = 1.0, tail: bool = False) -> torch.Tensor:
+            temperature: float = 1.0, tail: bool = False,
+            ctx: Optional[gq.Context] = None) -> torch.Tensor:
     """Each row's distillation loss (gq.distill_loss), differentiable in ``logits``."""
-    return _Distill.apply(logits, top_ids, top_logprobs, temperature, tail)[0]
+    return _Distill.apply(logits, top_ids, top_logprobs, temperature, tail, ctx)[0]

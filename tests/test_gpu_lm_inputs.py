@@ -55,3 +55,34 @@ def test_no_tokens(dtype):
     z = parts(0, 333, dtype=dtype).requires_grad_()
     loss = lm.distill(z, torch.zeros(0, 3, dtype=torch.int32, device="cuda"), torch.zeros(0, 3, device="cuda"), tail=True)
     assert loss.shape == (0,) and torch.autograd.grad(loss.sum(), z)[0].shape == z.shape
+
+
+def test_two_streams_with_a_context_each():
+    """Layers whose products are split along K (their partial products lie in the context's scratch
+    memory) and distillation in slices, on two streams at once: the bits of one after the other."""
+    from allreduce_compatible_gradient_amd import lm
+    say("lm two streams")
+    g = gq()
+    teacher = [g.token_logprobs(parts(3, 9001, seed=s), torch.zeros(3, dtype=torch.int64, device="cuda"), 9)[2:] for s in (1, 2)]
+    x = [parts(40, 9000, seed=10 + s, dtype=torch.bfloat16) for s in (1, 2)]
+    z = [parts(3, 9001, seed=20 + s) for s in (1, 2)]
+    w = parts(300, 9000, seed=30)
+
+    def both(i, ctx):
+        a, b, c = x[i].detach().requires_grad_(), w.detach().requires_grad_(), z[i].detach().requires_grad_()
+        y = lm.mx_linear(a, b, seed=i, ctx=ctx)
+        loss = lm.distill(c, *teacher[i], tail=True, ctx=ctx)
+        return [y, loss, *torch.autograd.grad((y.float().square().sum() + loss.sum()), (a, b, c))]
+
+    ctxs = [g.Context(), g.Context()]
+    want = [both(i, ctxs[i]) for i in (0, 1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [None, None]
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i] = both(i, ctxs[i])
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))

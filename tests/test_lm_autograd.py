@@ -165,3 +165,17 @@ def test_gradients_hold_none_of_the_activations(calls):
     assert alive() is None
     y.sum().backward()
     assert w.grad.shape == w.shape
+
+
+def test_a_context_of_ones_own(calls):
+    """Work on two streams at once needs a context for each: the one that is given serves every call
+    of the forward and of the backward pass."""
+    mine = object()
+    x, w = parts(4, 9).requires_grad_(), parts(7, 9).requires_grad_()
+    lm.mx_linear(x, w, ctx=mine).sum().backward()
+    z = parts(4, 33).requires_grad_()
+    lm.distill(z, torch.arange(12, dtype=torch.int32).view(4, 3), parts(4, 3), ctx=mine).sum().backward()
+    assert len(calls) == 8 and all(kw["ctx"] is mine for _, kw in calls)
+    del calls[:]
+    lm.mx_linear(x, w).sum().backward()
+    assert len(calls) == 6 and all(kw["ctx"] is None for _, kw in calls)
