@@ -28,6 +28,15 @@ typedef f32x4 f32x4_e4 __attribute__((aligned(4)));
 
 #define LDS_PTR __attribute__((address_space(3)))
 
+// Between writes of a wave's lanes to its own part of LDS and other lanes' reads of them, and back.
+// The hardware executes a wave's LDS accesses in order; the fences keep the compiler from moving
+// them across (the barrier alone is nothing to memory), and cost no instruction.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // ---------------------------------------------------------------- one block's encoding
 // Scale byte of a block whose largest magnitude has the bits `top` (sign cleared).  To nearest:
 // floor(log2 a) - 2, so that a lies in [4, 8) scales and what exceeds 6 saturates.  Stochastic:
@@ -294,7 +303,7 @@ __global__ __launch_bounds__(256, DT == 0 && !STOCH ? 4 : 3) void k_mx_both(cons
     }
     __builtin_amdgcn_sched_barrier(0);  // keeps the live rows' temporaries few
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_exchange();
   const int s0 = scale_byte<STOCH>(top[0]), s1 = scale_byte<STOCH>(top[1]);
   const float inv[2] = {inverse_scale(s0), inverse_scale(s1)};
   u32x4 codes[2];
@@ -346,7 +355,7 @@ __global__ __launch_bounds__(256, DT == 0 && !STOCH ? 4 : 3) void k_mx_both(cons
     col_scales[2 * lane + i][wave] = bad ? 255 : (uint8_t)(i ? s1 : s0);
   }
   if constexpr (ROWS) {
-    __builtin_amdgcn_wave_barrier();  // the wave's own part of LDS, in order
+    wave_exchange();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = half * 16 + (lane >> 2);
@@ -357,7 +366,7 @@ __global__ __launch_bounds__(256, DT == 0 && !STOCH ? 4 : 3) void k_mx_both(cons
     if (lane < 32 && row0 + lane < a.rows)
       *reinterpret_cast<uint32_t *>(a.scales + (row0 + lane) * pitch + blockIdx.x * 4) =
           *reinterpret_cast<const uint32_t *>(row_scales[wave][lane]);
-    __builtin_amdgcn_wave_barrier();
+    wave_exchange();
   }
   __syncthreads();
   if (threadIdx.x < kBothCols) {
@@ -704,7 +713,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
               *reinterpret_cast<f32x4 *>(own + r32 * kRowBytes + chunk * 16) = f32x4{v[0], v[1], v[2], v[3]};
             }
           }
-        __builtin_amdgcn_wave_barrier();
+        wave_exchange();
 #pragma unroll
         for (int p = 0; p < kCpr / 2; ++p) {
           const int row = p * (64 / kCpr) + lrow;
@@ -717,7 +726,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
               *reinterpret_cast<u32x4_e2 *>(out + at * row_bytes) = v;
           }
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_exchange();
       }
     };
     const bool lines = ((reinterpret_cast<uintptr_t>(sink.out) | (uint64_t)sink.ld * (sink.dtype == 0 ? 4 : 2)) & 127) == 0;
@@ -738,7 +747,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
         *reinterpret_cast<f32x4 *>(own + r32 * kRow + chunk * 16) =
             f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
       }
-    __builtin_amdgcn_wave_barrier();
+    wave_exchange();
 #pragma unroll 1
     for (int p = 0; p < kChunks / 4; ++p) {
       const int row = p * (128 / kChunks) + lane / (kChunks / 2), c = lane % (kChunks / 2) * 2;
@@ -746,7 +755,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
       const f32x4 hi = *reinterpret_cast<const f32x4 *>(own + row * kRow + (((c + 1) ^ (row & (kChunks - 1))) * 16));
       put_eight(sink, wm0 + i * 32 + row, wn0 + c * 4, lo, hi);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_exchange();
   }
 #endif
 }
