@@ -56,7 +56,7 @@ hipError_t launch_mx_matmul(const MxMatmulArgs &a, hipStream_t s);
 // ---------------------------------------------------------------- rows of logits
 constexpr int kVocabTop = 128;            // alternatives of a token, at most
 constexpr int64_t kVocabMax = 1 << 30;    // entries of a row
-constexpr int64_t kVocabRows = 1 << 24;   // rows of a call
+constexpr int64_t kVocabRows = (1 << 24) - 1;  // rows of a call: 256 threads each, of a launch's 2^32 - 1
 
 struct LogprobArgs {
   const void *logits;

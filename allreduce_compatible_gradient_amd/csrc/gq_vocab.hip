@@ -1074,9 +1074,11 @@ template <int DT>
 constexpr int64_t kRowMax = 512 * (DT == 0 ? 64 : 128) - 64;
 
 // Whether a block's registers hold a row; else its slices, one or more, leave their statistics in
-// the scratch memory.
-bool row_held(int slices, int64_t vocab, int dtype) {
-  return slices == 1 && vocab <= (dtype == 0 ? kRowMax<0> : kRowMax<1>);
+// the scratch memory.  A launch has fewer than 2^32 threads, so blocks of 512 serve fewer than 2^23
+// rows; kVocabRows is the limit of the others.
+bool row_held(int slices, int64_t rows, int64_t vocab, int dtype) {
+  return slices == 1 && vocab <= (dtype == 0 ? kRowMax<0> : kRowMax<1>) &&
+         (rows < 1 << 23 || vocab <= 256 * 64 - 64);
 }
 
 template <int DT, bool TAIL>
@@ -1084,7 +1086,7 @@ void distill_of(const DistillArgs &a, int slices, int64_t each, hipStream_t s) {
   const unsigned rows = (unsigned)a.rows;
   // Three blocks of 256 threads and 26 chunks a CU where a row fits them (4096 x 50257 bf16: 194 us
   // when two of 512 and 16 took 212 us).
-  if (row_held(slices, a.vocab, DT)) {
+  if (row_held(slices, a.rows, a.vocab, DT)) {
     if (a.vocab <= 256 * 64 - 64)
       k_distill_row<DT, TAIL, 256, 8><<<rows, 256, 0, s>>>(a);
     else if (DT == 0 || a.vocab <= 512 * 64 - 64)
@@ -1136,13 +1138,13 @@ hipError_t launch_token_logprobs(const LogprobArgs &a, int dtype, hipStream_t s)
 // same way, so that it has the same bits (a stream would be faster: 4096 x 50257 bf16, 91 us
 // against 110).
 int distill_slices(int64_t rows, int64_t vocab, int dtype, int64_t *each) {
-  return slices_of(rows, vocab, each, row_held(1, vocab, dtype) ? 256 : kFill);
+  return slices_of(rows, vocab, each, row_held(1, rows, vocab, dtype) ? 256 : kFill);
 }
 
 size_t distill_scratch(int64_t rows, int64_t vocab, int dtype) {
   int64_t each;
   const int n = distill_slices(rows, vocab, dtype, &each);
-  return row_held(n, vocab, dtype) ? 0 : (((size_t)rows * n * sizeof(Stat) + 15) & ~(size_t)15) + (size_t)rows * 16;
+  return row_held(n, rows, vocab, dtype) ? 0 : (((size_t)rows * n * sizeof(Stat) + 15) & ~(size_t)15) + (size_t)rows * 16;
 }
 
 hipError_t launch_distill_loss(const DistillArgs &a, int dtype, hipStream_t s) {

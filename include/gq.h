@@ -303,7 +303,8 @@ gq_status gq_lq_step_workers(gq_ctx *ctx, const float *const *G, float *const *E
  * gradients' exchange above: microscaled 4-bit floating point and its product, the log
  * probabilities of given tokens, and distillation from a teacher's top log probabilities.
  * Row strides are in elements and at least the row's length; rows may start at any element of
- * a 16-byte aligned buffer (a vocabulary of an odd size). */
+ * a 16-byte aligned buffer (a vocabulary of an odd size).  A call on logits has at most 2^24 - 1
+ * rows of at most 2^30 entries. */
 
 /* Packed microscaled matrices (GQ_MX).  A row of `cols` elements is cut into blocks of 32.  A
  * block holds a scale 2^(s - 127), s one byte, and 32 codes of 4 bits: bit 3 the sign, bits 0-2
