@@ -10,6 +10,7 @@ gq.global_norm and gq.fused_mean over the workers' gradients (8-bit codes, int16
 the fp32 master weights.  The workers' data is synthetic; they share one GPU.
 """
 import argparse
+import itertools
 import os
 import sys
 
@@ -33,6 +34,7 @@ def run(steps=30, workers=4, tokens=512, width=256, hidden=512, vocab=4096, top=
     opt = torch.optim.Adam([w1, w2], lr=lr)
     sizes = [w1.numel(), w2.numel()]
     losses, entropy = [], 0.0
+    seeds = itertools.count(seed)   # every rounding of every step draws with a seed of its own
     for step in range(steps):
         flat, mean_loss = [], 0.0
         for k in range(workers):
@@ -40,9 +42,8 @@ def run(steps=30, workers=4, tokens=512, width=256, hidden=512, vocab=4096, top=
             teacher = torch.relu(x.float() @ t1.T) @ t2.T
             sampled = torch.zeros(tokens, dtype=torch.int64, device="cuda")
             _, h, ids, lps = gq.token_logprobs(teacher, sampled, top=top)
-            layer = 2 * (step * workers + k)
-            y = torch.relu(lm.mx_linear(x, w1, seed=seed + layer, worker=k))
-            logits = lm.mx_linear(y, w2, seed=seed + layer + 1, worker=k)
+            y = torch.relu(lm.mx_linear(x, w1, seed=next(seeds), worker=k))
+            logits = lm.mx_linear(y, w2, seed=next(seeds), worker=k)
             loss = lm.distill(logits, ids, lps, tail=True).mean()
             grads = torch.autograd.grad(loss, (w1, w2))
             flat.append(torch.cat([d.reshape(-1) for d in grads]))
@@ -51,7 +52,7 @@ def run(steps=30, workers=4, tokens=512, width=256, hidden=512, vocab=4096, top=
         # the exchange: one scale a layer, codes that add, one decode
         offsets = [0, sizes[0], sizes[0] + sizes[1]]
         scale, _ = gq.global_norm(flat, offsets)
-        mean = gq.fused_mean(flat, scale, gq.UNIFORM, 127, 8, seed=seed + step, acc_bits=16,
+        mean = gq.fused_mean(flat, scale, gq.UNIFORM, 127, 8, seed=next(seeds), acc_bits=16,
                              offsets=offsets)
         for w, d in zip((w1, w2), mean.split(sizes)):
             w.grad = d.view_as(w)
