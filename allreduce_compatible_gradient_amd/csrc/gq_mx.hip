@@ -177,7 +177,9 @@ __device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
 // By rows: a lane holds eight elements (one 16-byte load of bf16), four lanes a block, so a block's
 // maximum takes two steps and its codes leave as one word a lane.  Threads run over the words of a
 // packed row, padding included.  333 x 768 bf16, an operand of a product, takes 4.8 us and
-// 1 x 4096 1.8 us: a launch's latency; larger matrices are bound by their bytes.
+// 1 x 4096 1.8 us: a launch's latency.  At size, to nearest it is bound by its bytes: 4096 x 11008
+// fp32 37 us (204 MB, 5.5 TB/s), 2047 x 50257 bf16 50 us (5.2 TB/s); stochastic by the draws: 42 and
+// 77 us.
 template <int DT, bool STOCH>
 __global__ __launch_bounds__(256) void k_mx_rows(const MxQuantArgs a, int pitch) {
   const int64_t row = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
@@ -210,9 +212,10 @@ __global__ __launch_bounds__(256) void k_mx_rows(const MxQuantArgs a, int pitch)
 // own and a row's block lies in 16 lanes.  The draw of an element is shared by its two codes.  Row
 // codes (a byte a lane and row) and the scales of both ways are gathered in LDS and leave as
 // 16-byte and 4-byte pieces.  Measured both ways: 4096 x 11008 fp32 to nearest 54 us (229 MB, 4.2
-// TB/s), 2047 x 50257 bf16 stochastic 132-150 us by the card, bound by the vector ALUs (some 45
-// issue slots an element, 15 of them the draw).  Waves of 64 rows, which write whole lines of
-// codes_t, took 59 and 144 us where these took 54 and 132: fewer waves at a time.
+// TB/s; codes_t leaves in 64-byte runs, so 71 MB are written for 48), 2047 x 50257 bf16 stochastic
+// 127-158 us by the card, bound by the vector ALUs (51 instructions an element, 15 of them the draw,
+// the rest two codes' encoding); by columns only 47 and 80 us.  Waves of 64 rows, which write whole
+// lines of codes_t, took 59 and 144 us where these took 54 and 132: fewer waves at a time.
 template <int DT>
 struct Pair;  // two neighbouring elements as loaded
 template <>
@@ -379,8 +382,8 @@ __global__ __launch_bounds__(256, DT == 0 && !STOCH ? 4 : 3) void k_mx_both(cons
 
 // ---------------------------------------------------------------- decoding
 // A thread eight elements: one word of codes, one scale, one 16-byte store of bf16, non-temporal:
-// 2047 x 50257 took 59 us with plain stores and takes 39 us (261 MB, 6.7 TB/s), 50257 x 2047 64
-// and 41, 4096 x 11008 18.5 and 17.7.  The decoded values are exact in bf16.
+// 2047 x 50257 took 59 us with plain stores and takes 39-42 us (261 MB, 6.2-6.7 TB/s), 50257 x 2047
+// 64 and 41-52, 4096 x 11008 18.5 and 17.7.  The decoded values are exact in bf16.
 template <int DT>
 __global__ __launch_bounds__(256) void k_mx_dequantize(const MxDequantArgs a, int pitch) {
   const int word = blockIdx.x * blockDim.x + threadIdx.x;
@@ -496,9 +499,12 @@ __device__ __forceinline__ void put_one(const Sink &s, int64_t m, int64_t n, flo
 // Tiled product, C = A B^T on packed operands, for more than kFewRows rows:
 // 8192 x 11008 x 4096 takes 190-195 us, 3.8-3.9 PFLOP/s; a step of
 // K takes a CU 1.8-1.9 us on random operands and 1.4-1.7 us on zeros, as the card lowers its clock
-// (to 2.0 GHz) under load; a loop of nothing but this instruction reaches 6.6 PFLOP/s on random
-// data.  Some 40 us of the whole are the first loads and the stores.  Tried and not faster: 16x16x128 instructions, four waves of 128 x 128 each, operands fetched across the
-// barrier.
+// (to 1.9 GHz by the counters) under load; a loop of nothing but this instruction reaches 6.6 PFLOP/s
+// on random data, 112 us.  The matrix cores are busy 47% of the time, LDS 24%, and waves wait for 31%
+// of theirs: one block a CU, so nothing covers a step's barrier and its wait for the next operands,
+// nor the first loads and the stores (some 40 us of the whole), and 1376 tiles fill 5.4 of 6 rounds.
+// Tried and not faster: 16x16x128 instructions, four waves of 128 x 128 each, operands fetched across
+// the barrier.
 // A block of WM x WN waves, a wave FM x FN tiles of 32 x 32, K in steps of 256
 // (128 bytes of a row).  v_mfma_scale_f32_32x32x64: lane l holds 32 elements of row l mod 32,
 // those of block l / 32, and that block's scale; the result has column l mod 32 and rows
@@ -686,7 +692,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_mx_matmul(const MxMatmulArgs a,
   const int64_t wm0 = m0 + wm * FM * 32, wn0 = n0 + wn * FN * 32;
   if (!sink.bias && !sink.accumulate && n0 + BN <= a.N) {
     // Nothing to add and no row cut short.  (With the general way's questions at each store, the
-    // stores ran at 2 TB/s: 333 x 50257 x 768 took 26 us.)
+    // stores ran at 2 TB/s: 8192 x 11008 x 4096 193 us so, 216 us with a bias, 234 us where old values
+    // are added.)
     // Rows on 128-byte lines are stored non-temporally: every store covers whole lines, and the
     // operands keep their place in the caches (8192 x 11008 x 4096: 225 us with plain stores, 199 us
     // so; rows off the lines lose by it: 4096 x 50257 x 768 205 us plain, 244 us).

@@ -452,8 +452,8 @@ __device__ __forceinline__ void put_token(const LogprobArgs &a, int64_t row, con
 // that the largest entries are looked for in the few groups that can hold them (a thread's maxima
 // bound the k-th largest from below) and not in the row again.  4095 x 50257 bf16 with 20 entries:
 // 91 us, 412 MB at 4.5 TB/s; the vector ALUs are some 70% busy with 12 instructions an entry, and
-// the selection at a row's end is hidden by the other blocks of the CU.  1 x 50257 fp32 in 24
-// slices: 6.5 us, and 3.5 us to join them.
+// the selection at a row's end is hidden by the other blocks of the CU; fp32 152 us, 5.4 TB/s.
+// 1 x 50257 fp32 in 24 slices: 6.6 us, and 3.6 us to join them.
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int slices,
                                                        int64_t each) {
@@ -891,7 +891,7 @@ __device__ __forceinline__ void grad_stream(const DistillArgs &a, int64_t row, c
 // read once, there for the largest entry, the sum and the gradient.  Chunks are counted from the
 // 128-byte line that the row begins in, so that a wave's stores cover whole lines.  The chunks
 // that the row's ends may cut are one more of threads 64 and 128.  4096 x 50257 bf16, loss and
-// gradient: 180 us, 823 MB at 4.6 TB/s.  What is left is the time between a row's last load and its
+// gradient: 177 us, 823 MB at 4.6 TB/s.  What is left is the time between a row's last load and its
 // first store, two joins over the block, which the CU's two other blocks cover in part; an
 // entry's two exponentials come on top of it.  A stream that reads the row again took
 // 259 us, one block of 1024 threads a CU 346 us.
@@ -999,7 +999,7 @@ __global__ __launch_bounds__(T) void k_distill_row(const DistillArgs a) {
   put_taught<DT>(a, row, mine, r, w);
 }
 
-// A block a slice: the slice's statistic.  1021 x 131071 bf16: 60 us, 268 MB at 4.5 TB/s.
+// A block a slice: the slice's statistic.  1021 x 131071 bf16: 58 us, 268 MB at 4.6 TB/s.
 template <int DT, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_slices(const DistillArgs a, int slices,
                                                              int64_t each) {
@@ -1011,7 +1011,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_slices(const DistillArgs a
 }
 
 // A block a row: the slices' statistics in their order, the loss and the gradient's constants.
-// 1021 rows: 11.6 us, the latency of the taught entries' loads and of the joins in 64 bits.
+// 1021 rows: 10.5 us, the latency of the taught entries' loads and of the joins in 64 bits.
 template <int DT, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, int slices) {
   __shared__ Taught t;
@@ -1024,7 +1024,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_join(const DistillArgs a, 
 
 // A block a slice: the gradient from the rows' constants, or (JOIN) from the slices' statistics:
 // every block joins its row's for itself, one kernel less than with the constants in between.
-// 1021 x 131071 bf16: 116 us, 536 MB at 4.6 TB/s; with JOIN, 5 x 50257 fp32: 9.7 us.
+// 1021 x 131071 bf16: 113 us, 536 MB at 4.7 TB/s; with JOIN, 5 x 50257 fp32: 9.0 us.
 template <int DT, bool JOIN, bool TAIL>
 __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, int slices,
                                                            int64_t each) {
@@ -1069,7 +1069,7 @@ void logprobs_of(const LogprobArgs &a, int slices, int64_t each, hipStream_t s) 
 // The longest row that is held in registers: two blocks of 512 threads a CU with 16 chunks of bf16,
 // 8 of fp32 a thread.  One block of 1024 for rows twice as long left the CU idle in its joins: 663
 // x 68328 bf16 84 us, as slices 62 us; 2048 x 40000 fp32 244 and 209; 2000 x 128000 bf16 291 and
-// 325, but its loss alone 203 and 110.
+// 318, but its loss alone 203 and 119.
 template <int DT>
 constexpr int64_t kRowMax = 512 * (DT == 0 ? 64 : 128) - 64;
 
@@ -1136,7 +1136,7 @@ hipError_t launch_token_logprobs(const LogprobArgs &a, int dtype, hipStream_t s)
 // Slices of the distillation loss: a block a row from a block a CU on, where registers hold a row
 // (512 x 50257 bf16 with the gradient: 48 us in two slices, 32 us so).  The loss alone takes the
 // same way, so that it has the same bits (a stream would be faster: 4096 x 50257 bf16, 91 us
-// against 110).
+// against 107).
 int distill_slices(int64_t rows, int64_t vocab, int dtype, int64_t *each) {
   return slices_of(rows, vocab, each, row_held(1, rows, vocab, dtype) ? 256 : kFill);
 }

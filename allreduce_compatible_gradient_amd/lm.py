@@ -101,7 +101,8 @@ def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
               seed: int = 0, worker: int = 0, ctx: Optional[gq.Context] = None) -> torch.Tensor:
     """A linear layer (x: tokens x in, weight: out x in) in microscaled 4-bit floating point.
     ``seed`` has to differ from one step and layer to the next, and from the seeds of the gradients'
-    exchange, which draws by the same hash; workers draw apart by ``worker``."""
+    exchange, which draws by the same hash; workers draw apart by ``worker``.  The backward pass takes
+    at most 2^32 entries of the output, the draws' counter."""
     return _Linear.apply(x, weight, bias, seed, worker, ctx)[0]
 
 
