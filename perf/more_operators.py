@@ -264,14 +264,14 @@ def _own_embed_grad(s, gq):
 
 
 def _own_i8(s, gq):
-    return gq.i8_matmul(s["A"], gq.I8Tensor(*s["W"]), bias=s["bias"],
+    return gq.int_matmul(s["A"], gq.IntTensor(*s["W"]), bias=s["bias"],
                         out_dtype=gq.BF16 if s["out"] == "bf16" else gq.F32)
 
 
 def _own_i8_backward(s, gq):
-    q, qt = gq.i8_quantize(s["dY"], rounding=gq.I8_STOCHASTIC, seed=s["seed"], by_cols=True)
-    return {"dX": gq.i8_matmul(q, gq.I8Tensor(*s["Wt"]), out_dtype=gq.BF16),
-            "dW": gq.i8_matmul(qt, gq.I8Tensor(*s["Xt"]), out_dtype=gq.F32)}
+    q, qt = gq.int_quantize(s["dY"], rounding=gq.INT_STOCHASTIC, seed=s["seed"], by_cols=True)
+    return {"dX": gq.int_matmul(q, gq.IntTensor(*s["Wt"]), out_dtype=gq.BF16),
+            "dW": gq.int_matmul(qt, gq.IntTensor(*s["Xt"]), out_dtype=gq.F32)}
 
 
 def _own_ortho(s, gq):
