@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libgq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["gq_api.cpp", "gq_stream.hip", "gq_lq.hip", "gq_mx.hip", "gq_vocab.hip"]
+SOURCES = ["gq_api.cpp", "gq_stream.hip", "gq_lq.hip", "gq_mx.hip", "gq_vocab.hip",
+           "gq_i8.hip", "gq_embed.hip", "gq_ortho.hip"]
 # measurement probe used by bench.py only (a plain stream of the same memory pattern)
 CEILING_SOURCE = "gq_ceiling.hip"
 CEILING_LIB = os.path.join(PKG, "libgq_ceiling.so")

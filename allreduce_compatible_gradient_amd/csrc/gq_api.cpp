@@ -20,6 +20,7 @@
 
 #include "gq.h"
 #include "gq_internal.h"
+#include "gq_layers.h"
 #include "gq_lm.h"
 #include "gq_lq.h"
 
@@ -1184,4 +1185,232 @@ GQ_EXPORT gq_status gq_distill_grad(gq_ctx *c, const void *logits, int32_t dtype
   a.ldg = ldd;
   const hipError_t e = gq::launch_distill_grad(a, dtype, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GQ_OK : hip_fail(c, e, "distill_grad launch");
+}
+
+// ================================================================ around a model's layers
+GQ_EXPORT int64_t gq_int_pitch(int64_t cols) { return cols < 1 ? 0 : gq::i8_pitch(cols); }
+
+GQ_EXPORT gq_status gq_int_quantize(gq_ctx *c, const void *x, int32_t dtype, int64_t rows,
+                                   int64_t cols, int64_t ld, int32_t rounding, uint64_t seed,
+                                   uint32_t worker, uint32_t index_base, int8_t *codes,
+                                   float *scales, int8_t *codes_t, float *scales_t,
+                                   void *stream) {
+  if (!c) return GQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  TRY(check_dtype(c, dtype, "dtype"));
+  if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
+    return fail(c, GQ_EINVAL, "codes without scales, or scales without codes");
+  TRY(check_matrix(c, rows, cols, ld, codes_t ? gq::kI8MaxCols : gq::kI8MaxRows,
+                   codes ? gq::kI8MaxCols : gq::kI8MaxRows, "x"));
+  if (rounding != GQ_INT_NEAREST && rounding != GQ_INT_STOCHASTIC)
+    return fail(c, GQ_EINVAL, "rounding = %d", rounding);
+  if (rounding == GQ_INT_STOCHASTIC) TRY(check_counter(c, rows * cols, index_base));
+  if (rows > 0 && !codes && !codes_t) return fail(c, GQ_EINVAL, "neither codes nor codes_t is given");
+  TRY(check_ptr(c, x, "x", rows == 0));
+  TRY(check_ptr(c, codes, "codes", true));
+  TRY(check_ptr(c, scales, "scales", true));
+  TRY(check_ptr(c, codes_t, "codes_t", true));
+  TRY(check_ptr(c, scales_t, "scales_t", true));
+  if (rows == 0) return GQ_OK;
+  gq::I8QuantArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.codes = codes;
+  a.scales = scales;
+  a.codes_t = codes_t;
+  a.scales_t = scales_t;
+  a.stochastic = rounding == GQ_INT_STOCHASTIC;
+  if (a.stochastic) a.key_mix = key_mix(worker_key(seed, worker));
+  a.index_base = index_base;
+  const size_t bytes = gq::i8_quantize_scratch(rows, cols, codes_t != nullptr);
+  if (bytes) TRY(ensure_scratch(c, bytes, s));
+  a.tops = static_cast<uint32_t *>(c->scratch);
+  const hipError_t e = gq::launch_i8_quantize(a, dtype, s);
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "int_quantize launch");
+}
+
+GQ_EXPORT gq_status gq_int_matmul(gq_ctx *c, const void *a, int32_t a_dtype, const float *a_scales,
+                                 int64_t lda, const int8_t *b, const float *b_scales, int64_t M,
+                                 int64_t N, int64_t K, const float *bias_or_null,
+                                 int32_t accumulate, int32_t out_dtype, void *out, int64_t ldo,
+                                 void *stream) {
+  if (!c) return GQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool packed = a_dtype == GQ_INT8;
+  if (!packed) TRY(check_dtype(c, a_dtype, "a_dtype"));
+  TRY(check_dtype(c, out_dtype, "out_dtype"));
+  TRY(check_flag(c, accumulate, "accumulate"));
+  TRY(check_matrix(c, M, K, packed ? K : lda, gq::kI8MaxRows, gq::kI8MaxCols, "a"));
+  TRY(check_matrix(c, M, N, ldo, gq::kI8MaxRows, gq::kI8MaxRows, "out"));
+  if (M > 0 && packed != (a_scales != nullptr))
+    return fail(c, GQ_EINVAL, packed ? "a_scales is NULL" : "a_scales is given for rows that are not packed");
+  TRY(check_ptr(c, a, "a", M == 0));
+  TRY(check_ptr(c, a_scales, "a_scales", true));
+  TRY(check_ptr(c, b, "b"));
+  TRY(check_ptr(c, b_scales, "b_scales"));
+  TRY(check_ptr(c, bias_or_null, "bias", true));
+  TRY(check_ptr(c, out, "out", M == 0));
+  if (M > 0 && (out == a || out == b)) return fail(c, GQ_EINVAL, "out is one of the operands");
+  if (M == 0) return GQ_OK;
+  gq::I8MatmulArgs m;
+  std::memset(&m, 0, sizeof m);
+  m.a = a;
+  m.a_scales = a_scales;
+  m.b = b;
+  m.b_scales = b_scales;
+  m.bias = bias_or_null;
+  m.out = out;
+  m.M = M;
+  m.N = N;
+  m.K = K;
+  m.lda = lda;
+  m.ldo = ldo;
+  m.a_dtype = a_dtype;
+  m.out_dtype = out_dtype;
+  m.accumulate = accumulate;
+  // scratch: A's packed rows (unless the product packs them itself), then partial products
+  const bool pack = !packed && !gq::i8_matmul_packs_rows(M, K);
+  const size_t codes = pack ? align256((size_t)M * (size_t)gq::i8_pitch(K)) : 0;
+  const size_t rows_bytes = pack ? codes + align256((size_t)M * sizeof(float)) : 0;
+  const size_t partial = gq::i8_matmul_scratch(M, N, K);
+  if (rows_bytes + partial > 0) TRY(ensure_scratch(c, rows_bytes + partial, s));
+  char *scratch = static_cast<char *>(c->scratch);
+  if (partial) m.partial = reinterpret_cast<int32_t *>(scratch + rows_bytes);
+  hipError_t e = hipSuccess;
+  if (pack) {
+    gq::I8QuantArgs q;
+    std::memset(&q, 0, sizeof q);
+    q.x = a;
+    q.rows = M;
+    q.cols = K;
+    q.ld = lda;
+    q.codes = reinterpret_cast<int8_t *>(scratch);
+    q.scales = reinterpret_cast<float *>(scratch + codes);
+    e = gq::launch_i8_quantize(q, a_dtype, s);
+    if (e != hipSuccess) return hip_fail(c, e, "int_matmul launch");
+    m.a = q.codes;
+    m.a_scales = q.scales;
+    m.a_dtype = GQ_INT8;
+  }
+  e = gq::launch_i8_matmul(m, s);
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "int_matmul launch");
+}
+
+GQ_EXPORT gq_status gq_embedding(gq_ctx *c, const void *table, int32_t dtype, int64_t vocab,
+                                 int64_t dim, int64_t ldt, const int64_t *ids, int64_t tokens,
+                                 float scale, int32_t out_dtype, void *out, int64_t ldo,
+                                 void *stream) {
+  if (!c) return GQ_EINVAL;
+  TRY(check_dtype(c, dtype, "dtype"));
+  TRY(check_dtype(c, out_dtype, "out_dtype"));
+  TRY(check_matrix(c, vocab, dim, ldt, gq::kEmbedMaxVocab, gq::kEmbedMaxDim, "table"));
+  TRY(check_matrix(c, tokens, dim, ldo, gq::kEmbedMaxTokens, gq::kEmbedMaxDim, "out"));
+  TRY(check_ptr(c, table, "table", vocab == 0 || tokens == 0));
+  TRY(check_ptr(c, ids, "ids", tokens == 0));
+  TRY(check_ptr(c, out, "out", tokens == 0));
+  if (tokens > 0 && out == table) return fail(c, GQ_EINVAL, "out is the table");
+  if (tokens == 0) return GQ_OK;
+  const gq::EmbedArgs a = {table, ids, tokens, vocab, dim, ldt, ldo, scale, out};
+  const hipError_t e = gq::launch_embed(a, dtype, out_dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "embedding launch");
+}
+
+GQ_EXPORT gq_status gq_embedding_grad(gq_ctx *c, const void *dout, int32_t dtype, const int64_t *ids,
+                                      int64_t tokens, int64_t dim, int64_t ldd, int64_t vocab,
+                                      float scale, int32_t accumulate, int32_t out_dtype,
+                                      void *dtable, int64_t ldt, void *stream) {
+  if (!c) return GQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  TRY(check_dtype(c, dtype, "dtype"));
+  TRY(check_dtype(c, out_dtype, "out_dtype"));
+  TRY(check_flag(c, accumulate, "accumulate"));
+  TRY(check_matrix(c, tokens, dim, ldd, gq::kEmbedMaxTokens, gq::kEmbedMaxDim, "dout"));
+  TRY(check_matrix(c, vocab, dim, ldt, gq::kEmbedMaxVocab, gq::kEmbedMaxDim, "dtable"));
+  TRY(check_ptr(c, dout, "dout", tokens == 0));
+  TRY(check_ptr(c, ids, "ids", tokens == 0));
+  TRY(check_ptr(c, dtable, "dtable", vocab == 0));
+  if (vocab > 0 && dout == dtable) return fail(c, GQ_EINVAL, "dtable is dout");
+  if (vocab == 0 || (tokens == 0 && accumulate)) return GQ_OK;
+  TRY(ensure_scratch(c, gq::embed_grad_scratch(tokens, vocab, dim), s));
+  const gq::EmbedGradArgs a = {dout, ids, tokens, vocab, dim, ldd, ldt, scale, accumulate, dtable, c->scratch};
+  const hipError_t e = gq::launch_embed_grad(a, dtype, out_dtype, s);
+  return e == hipSuccess ? GQ_OK : hip_fail(c, e, "embedding_grad launch");
+}
+
+namespace {
+
+// Whether singular values that begin in [0, 1] stay in the range of the products' operands: the
+// largest |p(x)| = |a x + b x^3 + c x^5| on [0, top] lies at top or where a + 3 b x^2 + 5 c x^4 = 0,
+// the largest |b x + c x^2| on [0, top^2] at top^2 or at -b / 2c.
+bool ortho_stays(int32_t steps, double a, double b, double c) {
+  auto p = [&](double x) { return std::fabs(x * (a + x * x * (b + x * x * c))); };
+  auto q = [&](double x) { return std::fabs(x * (b + x * c)); };
+  double top = 1.0;
+  for (int32_t i = 0; i < steps; ++i) {
+    const double square = top * top;
+    double most = p(top), off = q(square);
+    if (c != 0.0) {
+      if (-b / (2.0 * c) > 0.0 && -b / (2.0 * c) < square) off = std::fmax(off, q(-b / (2.0 * c)));
+      const double d = 9.0 * b * b - 20.0 * a * c;
+      if (d >= 0.0)
+        for (double root : {(-3.0 * b + std::sqrt(d)) / (10.0 * c), (-3.0 * b - std::sqrt(d)) / (10.0 * c)})
+          if (root > 0.0 && root < square) most = std::fmax(most, p(std::sqrt(root)));
+    } else if (b != 0.0) {
+      const double root = -a / (3.0 * b);
+      if (root > 0.0 && root < square) most = std::fmax(most, p(std::sqrt(root)));
+    }
+    if (!(most <= 7.5) || !(off <= 60.0)) return false;
+    top = most;
+  }
+  return true;
+}
+
+}  // namespace
+
+GQ_EXPORT gq_status gq_orthogonalise(gq_ctx *ctx, const void *g, int32_t dtype, int64_t batch,
+                                     int64_t rows, int64_t cols, int64_t ldg, int64_t stride_g,
+                                     int32_t steps, double a, double b, double c, void *out,
+                                     int64_t ldo, int64_t stride_o, void *stream) {
+  if (!ctx) return GQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  TRY(check_dtype(ctx, dtype, "dtype"));
+  TRY(check_matrix(ctx, rows, cols, ldg, gq::kOrthoMaxDim, gq::kOrthoMaxDim, "g"));
+  TRY(check_matrix(ctx, rows, cols, ldo, gq::kOrthoMaxDim, gq::kOrthoMaxDim, "out"));
+  if (batch < 0 || batch > 65536) return fail(ctx, GQ_EINVAL, "batch = %lld outside [0, 65536]", (long long)batch);
+  const int64_t least_g = (rows - 1) * ldg + cols, least_o = (rows - 1) * ldo + cols;
+  if (batch > 1 && rows > 0 && (stride_g < least_g || stride_o < least_o))
+    return fail(ctx, GQ_EINVAL, "matrices overlap: stride %lld of %lld, %lld of %lld", (long long)stride_g,
+                (long long)least_g, (long long)stride_o, (long long)least_o);
+  if (batch > 1 && (stride_g > (int64_t)1 << 40 || stride_o > (int64_t)1 << 40))
+    return fail(ctx, GQ_EINVAL, "a stride between matrices is above 2^40");
+  if (steps < 1 || steps > 32) return fail(ctx, GQ_EINVAL, "steps = %d outside [1, 32]", steps);
+  if (!ortho_stays(steps, a, b, c))
+    return fail(ctx, GQ_EINVAL, "coefficients (%g, %g, %g) take singular values out of range in %d steps", a, b, c, steps);
+  const bool none = rows == 0 || batch == 0;
+  TRY(check_ptr(ctx, g, "g", none));
+  TRY(check_ptr(ctx, out, "out", none));
+  if (!none && g == out) return fail(ctx, GQ_EINVAL, "out is g");
+  if (none) return GQ_OK;
+  TRY(ensure_scratch(ctx, gq::ortho_scratch(batch, rows, cols), s));
+  gq::OrthoArgs o;
+  std::memset(&o, 0, sizeof o);
+  o.g = g;
+  o.batch = batch;
+  o.rows = rows;
+  o.cols = cols;
+  o.ldg = ldg;
+  o.stride_g = stride_g;
+  o.steps = steps;
+  o.a = (float)a;
+  o.b = (float)b;
+  o.c = (float)c;
+  o.out = out;
+  o.ldo = ldo;
+  o.stride_o = stride_o;
+  o.scratch = ctx->scratch;
+  const hipError_t e = gq::launch_orthogonalise(o, dtype, s);
+  return e == hipSuccess ? GQ_OK : hip_fail(ctx, e, "orthogonalise launch");
 }

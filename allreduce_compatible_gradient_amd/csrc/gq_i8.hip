@@ -1,0 +1,613 @@
+// gq_i8.hip -- gfx950 kernels of 8-bit integer matrices with a scale for each row: quantisation of
+// a matrix by rows and by columns, and the product of two of them.
+//
+// Format.  A row of `cols` elements is `cols` codes of 8 bits in [-127, 127] and a scale, fp32:
+// an element stands for code * scale.  Rows are padded with zero codes to a multiple of 128, so the
+// product's K loop has no tail.  With t the row's largest magnitude, scale = fp32(t / 127) and
+// inv = fp32(127 / t): the uniform grid of 127 levels of the gradient quantisers with the largest
+// magnitude as its scale.  A row whose inv is not finite (t zero, or below 2^-121) has scale 0 and
+// zero codes; one that holds an infinity or NaN has scale NaN and zero codes.
+#include <math.h>
+
+#include <type_traits>
+
+#include "gq_layers.h"
+#include "gq_tiles.h"
+
+namespace gq {
+namespace {
+
+// ---------------------------------------------------------------- quantisation
+struct RowScale {
+  float scale, inv;  // inv 0: all codes are zero
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  if (top >= 0x7F800000u) return RowScale{__uint_as_float(0x7FC00000u), 0.0f};
+  const float t = __uint_as_float(top), inv = 127.0f / t;
+  if (!(inv < INFINITY)) return RowScale{0.0f, 0.0f};
+  return RowScale{t / 127.0f, inv};
+}
+
+// The code's byte, the other bits not cleared.  To nearest, ties to even: x * inv + 1.5 * 2^23 in one
+// rounding, whose unit is 1 there, so that the exact product is rounded.  A row without codes has
+// inv = 0: 0 * inf is NaN, whose byte is 0.
+__device__ __forceinline__ uint32_t nearest_byte(float x, float inv) {
+  return __float_as_uint(fmaf(x, inv, 12582912.0f));
+}
+
+// Up from floor(u) with probability u - floor(u), u = min(fp32(|x| inv), 127), as the gradient
+// quantisers do.
+__device__ __forceinline__ uint32_t drawn_byte(float x, float inv, uint32_t h) {
+  const float u = fminf(fabsf(x) * inv, 127.0f);
+  const int c = (int)u + ((float)h < __builtin_amdgcn_fractf(u) * 4294967296.0f);
+  return (uint32_t)((__float_as_uint(x) >> 31) ? -c : c);
+}
+
+__device__ __forceinline__ uint32_t four_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u),
+                               __builtin_amdgcn_perm(b, a, 0x0C0C0400u), 0x05040100u);
+}
+
+template <bool STOCH>
+__device__ __forceinline__ u32x2 eight_codes(const float (&x)[8], float inv, const uint32_t (&h)[8]) {
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = STOCH ? drawn_byte(x[i], inv, h[i]) : nearest_byte(x[i], inv);
+  return u32x2{four_bytes(c[0], c[1], c[2], c[3]), four_bytes(c[4], c[5], c[6], c[7])};
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+  return v;
+}
+
+// By rows: W waves a row, C groups of eight elements a lane held in registers, so that a row is read
+// once; C = 0: a row too long for that is read twice, the second time mostly from the caches.
+template <int DT, bool STOCH, int W, int C>
+__global__ __launch_bounds__(256) void k_i8_rows(const I8QuantArgs a, int pitch) {
+  constexpr int kThreads = W * 64, kRows = 256 / kThreads;
+  __shared__ uint32_t tops[4];
+  const int lane = threadIdx.x & (kThreads - 1), wave = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kThreads;
+  const bool there = row < a.rows;
+  const int64_t at = (there ? row : 0) * a.ld;
+  const int groups = pitch / 8;
+  float x[C > 0 ? C : 1][8];
+  uint32_t top = 0;
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int g = lane + c * kThreads;
+      if (g * 8 < a.cols) {
+        load_word<DT>(a.x, at, (int64_t)g * 8, a.cols, x[c]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[c][i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) top = max(top, top_of(x[c]));
+  } else {
+    for (int g = lane; g * 8 < a.cols; g += kThreads) {
+      load_word<DT>(a.x, at, (int64_t)g * 8, a.cols, x[0]);
+      top = max(top, top_of(x[0]));
+    }
+  }
+  top = wave_max(top);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) tops[wave] = top;
+    __syncthreads();
+    top = tops[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = max(top, tops[w]);
+  }
+  const RowScale s = row_scale(top);
+  if (!there) return;
+  if (lane == 0) a.scales[row] = s.scale;
+  int8_t *out = a.codes + row * pitch;
+  uint32_t h[8] = {};
+  auto leave = [&](int g, const float (&v)[8]) {
+    if constexpr (STOCH) {
+      const uint32_t first = a.index_base + (uint32_t)(row * a.cols) + (uint32_t)g * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = draw(first + i, a.key_mix);
+    }
+    const u32x2 w = eight_codes<STOCH>(v, s.inv, h);
+    *reinterpret_cast<u32x2 *>(out + (int64_t)g * 8) = s.inv == 0.0f ? u32x2{0u, 0u} : w;
+  };
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int g = lane + c * kThreads;
+      if (g < groups) leave(g, x[c]);
+    }
+  } else {
+    for (int g = lane; g < groups; g += kThreads) {
+      load_word<DT>(a.x, at, (int64_t)g * 8, a.cols, x[0]);
+      leave(g, x[0]);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void k_i8_clear(uint32_t *p, int64_t count) {
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t < count) p[t] = 0;
+}
+
+// Largest magnitudes of rows (ROWS) and columns, as bits: their maximum does not hang on the order in
+// which blocks arrive.  A block takes 64 rows x 512 columns, a wave 16 rows, a lane eight columns.
+template <int DT, bool ROWS>
+__global__ __launch_bounds__(256) void k_i8_tops(const I8QuantArgs a) {
+  __shared__ uint32_t cols_top[4][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c0 = (int64_t)blockIdx.x * 512 + lane * 8, r0 = (int64_t)blockIdx.y * 64 + wave * 16;
+  uint32_t top[8] = {};
+#pragma unroll 4
+  for (int r = 0; r < 16; ++r) {
+    if (r0 + r >= a.rows) break;
+    float x[8];
+    if (c0 < a.cols) {
+      load_word<DT>(a.x, (r0 + r) * a.ld, c0, a.cols, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i] = max(top[i], __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    if constexpr (ROWS) {
+      const uint32_t m = wave_max(top_of(x));
+      if (lane == 0) atomicMax(a.tops + r0 + r, m);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cols_top[wave][lane * 8 + i] = top[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = threadIdx.x + i * 256;
+    const int64_t col = (int64_t)blockIdx.x * 512 + c;
+    if (col < a.cols)
+      atomicMax(a.tops + a.rows + col, max(max(cols_top[0][c], cols_top[1][c]), max(cols_top[2][c], cols_top[3][c])));
+  }
+}
+
+// By columns, or both ways (ROWS), from the largest magnitudes.  A block takes 128 rows x 128 columns;
+// a lane has eight columns of a row, whose codes by rows leave as they are and whose codes by columns
+// cross LDS.  The draw of an element is shared by its two codes.
+template <int DT, bool STOCH, bool ROWS>
+__global__ __launch_bounds__(256) void k_i8_both(const I8QuantArgs a, int pitch, int pitch_t) {
+  constexpr int kPad = 136;
+  __shared__ __align__(16) uint8_t tile[128 * kPad];
+  __shared__ float inv_rows[128];
+  const int tid = threadIdx.x;
+  const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
+  if (tid < 128) {
+    if (ROWS) {
+      const RowScale s = r0 + tid < a.rows ? row_scale(a.tops[r0 + tid]) : RowScale{0.0f, 0.0f};
+      inv_rows[tid] = s.inv;
+      if (blockIdx.x == 0 && r0 + tid < a.rows) a.scales[r0 + tid] = s.scale;
+    }
+  } else if (blockIdx.y == 0 && c0 + tid - 128 < a.cols) {
+    a.scales_t[c0 + tid - 128] = row_scale(a.tops[a.rows + c0 + tid - 128]).scale;
+  }
+  const int64_t col = c0 + (tid & 15) * 8;
+  float inv_cols[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) inv_cols[i] = col + i < a.cols ? row_scale(a.tops[a.rows + col + i]).inv : 0.0f;
+  float x[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int64_t row = r0 + p * 16 + (tid >> 4);
+    if (row < a.rows && col < a.cols) {
+      load_word<DT>(a.x, row * a.ld, col, a.cols, x[p]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[p][i] = 0.0f;
+    }
+  }
+  if (ROWS) __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int r = p * 16 + (tid >> 4);
+    const int64_t row = r0 + r;
+    uint32_t h[8] = {};
+    if constexpr (STOCH) {
+      const uint32_t first = a.index_base + (uint32_t)(row * a.cols) + (uint32_t)col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = draw(first + i, a.key_mix);
+    }
+    if constexpr (ROWS) {
+      const float inv = inv_rows[r];
+      const u32x2 w = eight_codes<STOCH>(x[p], inv, h);
+      if (row < a.rows)
+        *reinterpret_cast<u32x2 *>(a.codes + row * pitch + col) = inv == 0.0f ? u32x2{0u, 0u} : w;
+    }
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = STOCH ? drawn_byte(x[p][i], inv_cols[i], h[i]) : nearest_byte(x[p][i], inv_cols[i]);
+      if (inv_cols[i] == 0.0f) c[i] = 0;
+    }
+    *reinterpret_cast<u32x2 *>(tile + r * kPad + (tid & 15) * 8) =
+        u32x2{four_bytes(c[0], c[1], c[2], c[3]), four_bytes(c[4], c[5], c[6], c[7])};
+  }
+  __syncthreads();
+  // four columns x sixteen rows a thread
+  const int g = tid & 31, rows16 = (tid >> 5) * 16;
+  u32x4 out[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = *reinterpret_cast<const uint32_t *>(tile + (rows16 + q * 4 + i) * kPad + g * 4);
+    const uint32_t a01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b01 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+    const uint32_t a23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), b23 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+    out[0][q] = __builtin_amdgcn_perm(a23, a01, 0x05040100u);
+    out[1][q] = __builtin_amdgcn_perm(a23, a01, 0x07060302u);
+    out[2][q] = __builtin_amdgcn_perm(b23, b01, 0x05040100u);
+    out[3][q] = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c0 + g * 4 + i < a.cols)
+      *reinterpret_cast<u32x4 *>(a.codes_t + (c0 + g * 4 + i) * (int64_t)pitch_t + r0 + rows16) = out[i];
+}
+
+// ---------------------------------------------------------------- products
+// out = (sum a b) sa sb (+ bias) (+ out): the sum is exact, the rest in fp32, rounded once more to
+// bf16.
+__device__ __forceinline__ float scaled(int sum, float sa, float sb) { return ((float)sum * sa) * sb; }
+
+__device__ __forceinline__ void put_one(const I8MatmulArgs &a, int64_t m, int64_t n, int sum) {
+  float v = scaled(sum, a.a_scales[m], a.b_scales[n]);
+  if (a.bias) v += a.bias[n];
+  const int64_t at = m * a.ldo + n;
+  if (a.out_dtype == 0) {
+    float *o = static_cast<float *>(a.out) + at;
+    *o = a.accumulate ? *o + v : v;
+  } else {
+    uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+    if (a.accumulate) v += __uint_as_float((uint32_t)*o << 16);
+    *o = to_bf16(v);
+  }
+}
+
+typedef i32x4 i32x4_e4 __attribute__((aligned(4)));
+
+template <int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM *WN * 64) void k_i8_matmul(const I8MatmulArgs a, int pitch,
+                                                           int tiles_m, int tiles_n,
+                                                           int steps_each) {
+  using S = TileShape<WM, WN, FM, FN>;
+  __shared__ __align__(1024) uint8_t lds0[S::kStage];
+  __shared__ __align__(1024) uint8_t lds1[S::kStage];
+  __shared__ __align__(1024) uint8_t lds2[S::kStage];
+  __shared__ __align__(1024) uint8_t lds3[S::kStage];
+  int bm, bn;
+  tile_at(near_tiles(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, bm, bn);
+  const int64_t m0 = (int64_t)bm * S::BM, n0 = (int64_t)bn * S::BN;
+  const TileRows ra = {static_cast<const uint8_t *>(a.a) + m0 * pitch, (int)min((int64_t)S::BM, a.M - m0)};
+  const TileRows rb = {reinterpret_cast<const uint8_t *>(a.b) + n0 * pitch, (int)min((int64_t)S::BN, a.N - n0)};
+  const int step0 = blockIdx.y * steps_each;
+  i32x16 acc[FM][FN] = {};
+  tile_product<I8Product, WM, WN, FM, FN>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
+                                          min(steps_each, pitch / kStepBytes - step0), acc);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  constexpr int kOwn = 32 * FN * 128, kPer = S::kStage / kOwn;  // a wave's part of LDS
+  static_assert(kPer * 4 >= WM * WN && kPer > 0, "the waves' rows fit the buffers");
+  uint8_t *const own = (wave / kPer == 0 ? lds0 : wave / kPer == 1 ? lds1 : wave / kPer == 2 ? lds2 : lds3) + wave % kPer * kOwn;
+  const int64_t wm0 = m0 + wave / WN * FM * 32, wn0 = n0 + wave % WN * FN * 32;
+  const int64_t n = wn0 + lane % (FN * 4) * 8;  // a lane's columns
+  auto nothing = [](int) {};
+  if (gridDim.y > 1) {
+    int32_t *part = a.partial + (int64_t)blockIdx.y * a.M * a.N;
+    by_rows<I8Product, FM, FN>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
+      const int64_t m = wm0 + i * 32 + row;
+      if (m >= a.M || n >= a.N) return;
+      int32_t *o = part + m * a.N + n;
+      if (n + 8 <= a.N) {
+        reinterpret_cast<i32x4_e4 *>(o)[0] = lo;
+        reinterpret_cast<i32x4_e4 *>(o)[1] = hi;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.N) o[e] = e < 4 ? lo[e & 3] : hi[e & 3];
+      }
+    }, nothing);
+    return;
+  }
+  float sb[8], bias[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t c = min(n + e, a.N - 1);
+    sb[e] = a.b_scales[c];
+    bias[e] = a.bias ? a.bias[c] : 0.0f;
+  }
+  const bool add = a.bias != nullptr;  // without a bias -0 stays -0
+  const bool lines = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.ldo * 2) & 127) == 0;
+  by_rows<I8Product, FM, FN>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
+    const int64_t m = wm0 + i * 32 + row;
+    if (m >= a.M || n >= a.N) return;
+    const float sa = a.a_scales[m];
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = scaled(e < 4 ? lo[e & 3] : hi[e & 3], sa, sb[e]);
+      if (add) v[e] += bias[e];
+    }
+    const int64_t at = m * a.ldo + n;
+    const bool whole = n + 8 <= a.N;
+    if (a.out_dtype == 0) {
+      float *o = static_cast<float *>(a.out) + at;
+      if (whole) {
+        f32x4 p = {v[0], v[1], v[2], v[3]}, q = {v[4], v[5], v[6], v[7]};
+        f32x4_e4 *to = reinterpret_cast<f32x4_e4 *>(o);
+        if (a.accumulate) {
+          p += to[0];
+          q += to[1];
+        }
+        to[0] = p;
+        to[1] = q;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.N) o[e] = a.accumulate ? o[e] + v[e] : v[e];
+      }
+    } else {
+      uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+      if (whole) {
+        if (a.accumulate) {
+          float x[8];
+          load_eight<1>(o, 0, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += x[e];
+        }
+        const u32x4 w = {to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3]), to_bf16_pair(v[4], v[5]), to_bf16_pair(v[6], v[7])};
+        if (lines)
+          __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(o));
+        else
+          *reinterpret_cast<u32x4_e2 *>(o) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.N) o[e] = to_bf16(a.accumulate ? __uint_as_float((uint32_t)o[e] << 16) + v[e] : v[e]);
+      }
+    }
+  }, nothing);
+}
+
+// The partial sums of the K splits; their order does not matter.
+__global__ __launch_bounds__(256) void k_i8_join(const I8MatmulArgs a, int splits) {
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.M * a.N) return;
+  int v = 0;
+  for (int i = 0; i < splits; ++i) v += a.partial[(int64_t)i * a.M * a.N + t];
+  put_one(a, t / a.N, t % a.N, v);
+}
+
+// Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it, so each
+// block streams 16 rows of B straight to registers, its waves on interleaved steps of 128, four steps
+// of a wave on their way together.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l mod 16 at
+// l / 16.  fp32 / bf16 rows are quantised by the block into LDS while its first weights are on their
+// way.  The waves' sums meet in LDS.
+constexpr int kFewWaves = 8;
+constexpr int kFewAhead = 4;
+constexpr int64_t kFewRows = 16;
+// LDS of M packed rows: a row is padded by a chunk, so that 16 rows lie on different banks.
+inline size_t few_lds(int64_t M, int64_t pitch) { return (size_t)M * (size_t)(pitch + 16); }
+
+template <int AT>
+__global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8MatmulArgs a, int pitch) {
+  __shared__ i32x4 sums[kFewWaves][64];
+  __shared__ uint32_t tops[kFewRows];
+  extern __shared__ __align__(16) uint8_t packed[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, quarter = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int8_t *b = a.b + min(n0 + r16, a.N - 1) * pitch + quarter * 16;
+  const int steps = pitch / 128;
+  i32x4 w[kFewAhead][2];
+  auto load = [&](int k, i32x4 (&to)[2]) {
+    const i32x4 *p = reinterpret_cast<const i32x4 *>(b + (int64_t)k * 128);
+    to[0] = __builtin_nontemporal_load(p);
+    to[1] = __builtin_nontemporal_load(p + 4);
+  };
+#pragma unroll
+  for (int i = 0; i < kFewAhead; ++i)
+    if (wave + i * kFewWaves < steps) load(wave + i * kFewWaves, w[i]);
+  const uint8_t *rows = static_cast<const uint8_t *>(a.a);
+  int row_bytes = pitch;
+  const int M = (int)a.M;
+  if constexpr (AT != 3) {
+    row_bytes = pitch + 16;
+    int shift = 0;  // a row's share of the threads: 512 >> shift, the rows rounded up to a power of two
+    while ((1 << shift) < M) ++shift;
+    const int threads = (kFewWaves * 64) >> shift, row = threadIdx.x / threads, t = threadIdx.x % threads;
+    if (threadIdx.x < kFewRows) tops[threadIdx.x] = 0;
+    __syncthreads();
+    float x[8];
+    uint32_t top = 0;
+    if (row < M)
+      for (int g = t; g * 8 < a.K; g += threads) {
+        load_word<AT>(a.a, row * a.lda, (int64_t)g * 8, a.K, x);
+        top = max(top, top_of(x));
+      }
+    for (int m = 1; m < threads && m < 64; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    if (row < M && (t & 63) == 0) atomicMax(&tops[row], top);
+    __syncthreads();
+    if (row < M) {
+      const RowScale s = row_scale(tops[row]);
+      const uint32_t h[8] = {};
+      for (int g = t; g < pitch / 8; g += threads) {
+        load_word<AT>(a.a, row * a.lda, (int64_t)g * 8, a.K, x);
+        const u32x2 c = eight_codes<false>(x, s.inv, h);
+        *reinterpret_cast<u32x2 *>(packed + row * row_bytes + g * 8) = s.inv == 0.0f ? u32x2{0u, 0u} : c;
+      }
+    }
+    rows = packed;
+    __syncthreads();
+  }
+  i32x4 acc = {0, 0, 0, 0};
+  for (int first = wave; first < steps; first += kFewAhead * kFewWaves) {
+#pragma unroll
+    for (int i = 0; i < kFewAhead; ++i) {
+      const int k = first + i * kFewWaves;
+      if (k < steps) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          i32x4 v = {0, 0, 0, 0};
+          if (r16 < M) v = *reinterpret_cast<const i32x4 *>(rows + (int64_t)r16 * row_bytes + k * 128 + p * 64 + quarter * 16);
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i][p], v, acc, 0, 0, 0);
+        }
+        if (k + kFewAhead * kFewWaves < steps) load(k + kFewAhead * kFewWaves, w[i]);
+      }
+    }
+  }
+  sums[wave][lane] = acc;
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    const int from = threadIdx.x >> 2, e = threadIdx.x & 3;
+    int v = 0;
+#pragma unroll
+    for (int i = 0; i < kFewWaves; ++i) v += sums[i][from][e];
+    const int64_t m = from & 15, col = n0 + 4 * (from >> 4) + e;
+    if (m < a.M && col < a.N) {
+      if constexpr (AT != 3) {
+        float o = scaled(v, row_scale(tops[m]).scale, a.b_scales[col]);
+        if (a.bias) o += a.bias[col];
+        const int64_t at = m * a.ldo + col;
+        if (a.out_dtype == 0) {
+          float *to = static_cast<float *>(a.out) + at;
+          *to = a.accumulate ? *to + o : o;
+        } else {
+          uint16_t *to = static_cast<uint16_t *>(a.out) + at;
+          *to = to_bf16(a.accumulate ? __uint_as_float((uint32_t)*to << 16) + o : o);
+        }
+      } else {
+        put_one(a, m, col, v);
+      }
+    }
+  }
+}
+
+constexpr int kCus = 256;
+
+struct Plan {
+  int bm, bn;        // tile
+  int splits, each;  // K splits and steps of each
+};
+
+Plan plan(int64_t M, int64_t N, int64_t K) {
+  struct Tile {
+    int bm, bn;
+    float step, rest, wait;  // us of a step of 128 bytes, of the rest of a tile, and once a step
+  };
+  constexpr Tile kTiles[3] = {{256, 256, 1.4f, 3.5f, 0.0f}, {128, 128, 0.45f, 1.7f, 0.4f}, {64, 128, 0.4f, 2.2f, 0.4f}};
+  Plan p = {};
+  const int64_t steps = i8_pitch(K) / 128;
+  auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  float least = INFINITY;
+  for (const Tile &t : kTiles) {
+    const float each = (float)((tiles(t.bm, t.bn) + kCus - 1) / kCus);
+    const float us = each * ((float)steps * t.step + t.rest) + (float)steps * t.wait;
+    if (us < least) {
+      least = us;
+      p.bm = t.bm;
+      p.bn = t.bn;
+    }
+  }
+  int64_t splits = 1;
+  if (steps >= 24) {
+    splits = kCus / tiles(p.bm, p.bn);
+    if (splits > steps / 8) splits = steps / 8;
+    if (splits > 16) splits = 16;
+    if (splits < 1) splits = 1;
+  }
+  p.each = (int)((steps + splits - 1) / splits) * 2;  // steps of the loop: 64 bytes
+  p.splits = (int)((steps * 2 + p.each - 1) / p.each);
+  return p;
+}
+
+template <int WM, int WN, int FM, int FN>
+void tiles_of(const I8MatmulArgs &a, const Plan &p, hipStream_t s) {
+  const int tm = (int)((a.M + p.bm - 1) / p.bm), tn = (int)((a.N + p.bn - 1) / p.bn);
+  k_i8_matmul<WM, WN, FM, FN><<<dim3((unsigned)(tm * tn), p.splits), WM * WN * 64, 0, s>>>(
+      a, (int)i8_pitch(a.K), tm, tn, p.each);
+}
+
+template <int DT, bool STOCH>
+void quantize_of(const I8QuantArgs &a, hipStream_t s) {
+  const int pitch = (int)i8_pitch(a.cols);
+  if (!a.codes_t) {
+    // a row in a wave's registers where it fits, else in a block's, else read twice
+    if (a.cols <= 2048)
+      k_i8_rows<DT, STOCH, 1, 4><<<(unsigned)((a.rows + 3) / 4), 256, 0, s>>>(a, pitch);
+    else if (a.cols <= 12288)
+      k_i8_rows<DT, STOCH, 4, 6><<<(unsigned)a.rows, 256, 0, s>>>(a, pitch);
+    else
+      k_i8_rows<DT, STOCH, 4, 0><<<(unsigned)a.rows, 256, 0, s>>>(a, pitch);
+    return;
+  }
+  const int pitch_t = (int)i8_pitch(a.rows);
+  k_i8_clear<<<(unsigned)((a.rows + a.cols + 255) / 256), 256, 0, s>>>(a.tops, a.rows + a.cols);
+  const dim3 parts((unsigned)((a.cols + 511) / 512), (unsigned)((a.rows + 63) / 64));
+  const dim3 tiles((unsigned)(pitch / 128), (unsigned)(pitch_t / 128));
+  if (a.codes) {
+    k_i8_tops<DT, true><<<parts, 256, 0, s>>>(a);
+    k_i8_both<DT, STOCH, true><<<tiles, 256, 0, s>>>(a, pitch, pitch_t);
+  } else {
+    k_i8_tops<DT, false><<<parts, 256, 0, s>>>(a);
+    k_i8_both<DT, STOCH, false><<<tiles, 256, 0, s>>>(a, pitch, pitch_t);
+  }
+}
+
+}  // namespace
+
+size_t i8_quantize_scratch(int64_t rows, int64_t cols, bool by_cols) {
+  return by_cols ? (size_t)(rows + cols) * sizeof(uint32_t) : 0;
+}
+
+hipError_t launch_i8_quantize(const I8QuantArgs &a, int dtype, hipStream_t s) {
+  if (dtype == 0)
+    a.stochastic ? quantize_of<0, true>(a, s) : quantize_of<0, false>(a, s);
+  else
+    a.stochastic ? quantize_of<1, true>(a, s) : quantize_of<1, false>(a, s);
+  return hipGetLastError();
+}
+
+bool i8_matmul_packs_rows(int64_t M, int64_t K) { return M <= kFewRows && M * i8_pitch(K) <= 32768; }
+
+size_t i8_matmul_scratch(int64_t M, int64_t N, int64_t K) {
+  if (M <= kFewRows) return 0;
+  const Plan p = plan(M, N, K);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(int32_t) : 0;
+}
+
+hipError_t launch_i8_matmul(const I8MatmulArgs &a, hipStream_t s) {
+  const int pitch = (int)i8_pitch(a.K);
+  if (a.M <= kFewRows) {
+    const unsigned blocks = (unsigned)((a.N + 15) / 16);
+    const size_t lds = few_lds(a.M, pitch);
+    if (a.a_dtype == 0)
+      k_i8_matmul_few<0><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
+    else if (a.a_dtype == 1)
+      k_i8_matmul_few<1><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
+    else
+      k_i8_matmul_few<3><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+    return hipGetLastError();
+  }
+  const Plan p = plan(a.M, a.N, a.K);
+  if (p.bm == 256)
+    tiles_of<2, 4, 4, 2>(a, p, s);
+  else if (p.bm == 128)
+    tiles_of<2, 2, 2, 2>(a, p, s);
+  else
+    tiles_of<1, 4, 2, 1>(a, p, s);
+  if (p.splits > 1) k_i8_join<<<(unsigned)((a.M * a.N + 255) / 256), 256, 0, s>>>(a, p.splits);
+  return hipGetLastError();
+}
+
+}  // namespace gq

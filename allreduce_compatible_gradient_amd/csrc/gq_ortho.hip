@@ -1,0 +1,549 @@
+// gq_ortho.hip -- gfx950 kernels that bring a matrix's singular values towards 1 by steps of
+//   X <- a X + (b A + c A^2) X,   A = X X^T,   from X = G / |G|_F,
+// with products alone (Newton-Schulz).  Everything is done on the shorter side: n <= m, X n x m, the
+// transpose of a tall G.
+//
+// Numbers.  Operands of the products are halves, sums fp32, and X itself stays fp32.  Three choices
+// make that enough for a result in bf16.  Halves and not bf16: 3 bits more, and all operands have
+// known ranges, which powers of two bring into the halves' (X to at most 2^8 |x|, the others to
+// 2^10).  The diagonals of A and of B = b A + c A^2, large where the rest is small, stay apart in fp32:
+// with A = D + F,  A^2 = D^2 + D F + F D + F^2, and only F^2 is a product of rounded numbers; likewise
+// X <- (a + diag B) X + (B - diag B) X.  And a X, which carries a small singular value through the
+// steps that raise it up to a^steps-fold, is taken from the fp32 X.  The relative error (Frobenius)
+// before the last rounding is 1e-4 to 8e-4 for random, heavy-tailed and nearly low-rank matrices of
+// sides 64 to 1024, where halves alone have 2e-3 to 7e-3 and bf16 1e-2 to 1e-1; rounding to bf16
+// adds 1.7e-3.
+//
+// Work.  A and A^2 are symmetric: tiles on and above the diagonal are computed and stored both ways.
+// A step is three launches: the Gram matrix (of X's halves), its square, and the update, which
+// writes X in fp32, its halves by rows for the next Gram matrix, and by columns for the next update.
+#include <math.h>
+
+#include "gq_layers.h"
+#include "gq_tiles.h"
+
+namespace gq {
+namespace {
+
+constexpr float kScaleX = 256.0f, kScaleB = 1024.0f;
+constexpr int kNormBlocks = 256;
+
+// One group of matrices; every array holds `batch` of them, one after another.
+struct Work {
+  float *x;             // n x mp
+  _Float16 *xh;         // n x mp
+  _Float16 *xt[2];      // m x np, of this step and the next
+  _Float16 *f;          // n x np: A off its diagonal
+  _Float16 *b;          // n x np: B off its diagonal
+  float *diag_a, *diag_b;  // np
+  double *norms;        // kNormBlocks
+  float *partial;       // splits of the Gram matrix
+  int n, m, np, mp;     // np, mp: rounded up to 64
+};
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
+}
+
+__device__ __forceinline__ u32x4 eight_halves(const float (&v)[8]) {
+  return u32x4{pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7])};
+}
+
+// ---------------------------------------------------------------- G to X
+// Sums of squares in 64 bits, one a block.
+template <int DT>
+__global__ __launch_bounds__(256) void k_ortho_norm(const OrthoArgs a, double *norms) {
+  __shared__ double part[4];
+  const int64_t base = (int64_t)blockIdx.y * a.stride_g;
+  const int64_t groups = (a.cols + 7) / 8, all = a.rows * groups;
+  double sum = 0.0;
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < all; t += (int64_t)gridDim.x * 256) {
+    const int64_t r = t / groups, c = (t - r * groups) * 8;
+    float x[8];
+    load_word<DT>(a.g, base + r * a.ldg, c, a.cols, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += (double)x[i] * (double)x[i];
+  }
+  for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) norms[(int64_t)blockIdx.y * kNormBlocks + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// X in fp32 and in halves both ways, padding zero, 64 x 64 elements a block.  A matrix of zeros stays
+// one; one with an infinity or NaN becomes NaN everywhere.
+template <int DT, bool FLIP>
+__global__ __launch_bounds__(256) void k_ortho_start(const OrthoArgs a, const Work w, int parts) {
+  __shared__ float tile[64][65];
+  __shared__ double sums[4];
+  const int tid = threadIdx.x;
+  const int64_t k = blockIdx.z;
+  double sum = tid < parts ? w.norms[k * kNormBlocks + tid] : 0.0;
+  for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+  if ((tid & 63) == 0) sums[tid >> 6] = sum;
+  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+  const int64_t r0 = FLIP ? j0 : i0, c0 = FLIP ? i0 : j0;  // the tile's place in G
+  const int64_t base = k * a.stride_g;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int r = p * 32 + (tid >> 3), c = (tid & 7) * 8;
+    float x[8] = {};
+    if (r0 + r < a.rows && c0 + c < a.cols) load_word<DT>(a.g, base + (r0 + r) * a.ldg, c0 + c, a.cols, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (FLIP)
+        tile[c + i][r] = x[i];
+      else
+        tile[r][c + i] = x[i];
+    }
+  }
+  __syncthreads();
+  const double total = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  const double inv = total > 0.0 ? 1.0 / sqrt(total) : total == 0.0 ? 0.0 : total;
+  const bool bad = !(total < INFINITY);
+  auto value = [&](float g) { return bad ? NAN : (float)((double)g * inv); };
+  float *x = w.x + k * w.n * w.mp;
+  _Float16 *xh = w.xh + k * w.n * w.mp, *xt = w.xt[0] + k * w.m * w.np;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int r = p * 32 + (tid >> 3), c = (tid & 7) * 8;
+    float v[8], h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = j0 + c + i < w.m ? value(tile[r][c + i]) : 0.0f;
+      h[i] = v[i] * kScaleX;
+    }
+    if (i0 + r < w.n) {
+      const int64_t at = (int64_t)(i0 + r) * w.mp + j0 + c;
+      *reinterpret_cast<f32x4 *>(x + at) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4 *>(x + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      *reinterpret_cast<u32x4 *>(xh + at) = eight_halves(h);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = i0 + c + i < w.n ? value(tile[c + i][r]) * kScaleX : 0.0f;
+    if (j0 + r < w.m) *reinterpret_cast<u32x4 *>(xt + (int64_t)(j0 + r) * w.np + i0 + c) = eight_halves(h);
+  }
+}
+
+// ---------------------------------------------------------------- products
+// A wave's 32 x (FN * 32) halves by columns, from what by_rows' lanes hold, through the wave's part of
+// LDS (columns of 72 bytes: the rows' writes fall on different banks): f(column, first row, eight rows).
+template <int FN, class F>
+__device__ __forceinline__ void by_columns(const u32x4 (&keep)[FN * 2], uint8_t *own, F &&f) {
+  const int lane = threadIdx.x & 63;
+  const int col = lane % (FN * 4) * 8;
+#pragma unroll
+  for (int p = 0; p < FN * 2; ++p) {
+    const int row = p * (16 / FN) + lane / (FN * 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      *reinterpret_cast<uint16_t *>(own + (col + e) * 72 + row * 2) = (uint16_t)(keep[p][e >> 1] >> (16 * (e & 1)));
+  }
+  wave_exchange();
+#pragma unroll
+  for (int p = 0; p < FN * 2; ++p) {
+    const int c = p * 16 + (lane >> 2), piece = lane & 3;
+    const u32x2 lo = *reinterpret_cast<const u32x2 *>(own + c * 72 + piece * 16);
+    const u32x2 hi = *reinterpret_cast<const u32x2 *>(own + c * 72 + piece * 16 + 8);
+    f(c, piece * 8, u32x4{lo.x, lo.y, hi.x, hi.y});
+  }
+  wave_exchange();
+}
+
+// Tile t of the triangle of tiles on and above the diagonal, row after row.
+__device__ __forceinline__ void triangle_at(int t, int tiles, int &i, int &j) {
+  // row i begins at i tiles - i (i - 1) / 2
+  const float b = 2.0f * tiles + 1.0f;
+  i = (int)((b - sqrtf(b * b - 8.0f * t)) * 0.5f);
+  while (i > 0 && i * tiles - i * (i - 1) / 2 > t) --i;
+  while ((i + 1) * tiles - (i + 1) * i / 2 <= t) ++i;
+  j = t - (i * tiles - i * (i - 1) / 2) + i;
+}
+
+#define GQ_ORTHO_LDS                                                                              \
+  using S = TileShape<WM, WN, FM, FN>;                                                            \
+  __shared__ __align__(1024) uint8_t lds0[S::kStage];                                             \
+  __shared__ __align__(1024) uint8_t lds1[S::kStage];                                             \
+  __shared__ __align__(1024) uint8_t lds2[S::kStage];                                             \
+  __shared__ __align__(1024) uint8_t lds3[S::kStage];                                             \
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;     \
+  constexpr int kOwn = 32 * FN * 128, kPer = S::kStage / kOwn;                                    \
+  static_assert(kPer > 0 && kPer * 4 >= WM * WN && kOwn >= FN * 32 * 72, "the waves' parts");     \
+  uint8_t *const own = (wave / kPer == 0   ? lds0                                                 \
+                        : wave / kPer == 1 ? lds1                                                 \
+                        : wave / kPer == 2 ? lds2                                                 \
+                                           : lds3) +                                              \
+                       wave % kPer * kOwn
+
+// A symmetric product of the rows of `of` (n of them, pitch bytes each).  SQUARE false: the Gram
+// matrix of X, to F and diag_a (or partial sums, where gridDim.y > 1); true: F^2, to B and diag_b.
+template <bool SQUARE, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM *WN * 64) void k_ortho_symmetric(const Work w, float cb, float cc,
+                                                                 int tiles, int steps_each) {
+  GQ_ORTHO_LDS;
+  static_assert(S::BM == S::BN, "mirrored tiles");
+  int ti, tj;
+  triangle_at(near_tiles(blockIdx.x, tiles * (tiles + 1) / 2), tiles, ti, tj);
+  const int64_t k = blockIdx.z;
+  const int pitch = (SQUARE ? w.np : w.mp) * 2, i0 = ti * S::BM, j0 = tj * S::BN;
+  const uint8_t *of = reinterpret_cast<const uint8_t *>(SQUARE ? w.f : w.xh) + k * w.n * pitch;
+  const TileRows ra = {of + (int64_t)i0 * pitch, min(S::BM, w.n - i0)};
+  const TileRows rb = {of + (int64_t)j0 * pitch, min(S::BN, w.n - j0)};
+  const int step0 = blockIdx.y * steps_each;
+  f32x16 acc[FM][FN] = {};
+  tile_product<F16Product, WM, WN, FM, FN>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
+                                           min(steps_each, pitch / kStepBytes - step0), acc);
+  const int wi = wave / WN * FM * 32, wj = wave % WN * FN * 32;
+  if (!SQUARE && gridDim.y > 1) {
+    float *part = w.partial + (((int64_t)k * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * (S::BM * S::BN);
+    by_rows<F16Product, FM, FN>(acc, own, [&](int i, int, int row, int col, f32x4 lo, f32x4 hi) {
+      f32x4 *o = reinterpret_cast<f32x4 *>(part + (wi + i * 32 + row) * S::BN + wj + col);
+      o[0] = lo;
+      o[1] = hi;
+    }, [](int) {});
+    return;
+  }
+  _Float16 *const to = (SQUARE ? w.b : w.f) + k * w.n * w.np;
+  const _Float16 *const f = w.f + k * w.n * w.np;
+  const float *const da = w.diag_a + k * w.np;
+  float *const diag = (SQUARE ? w.diag_b : w.diag_a) + k * w.np;
+  const int j = j0 + wj + lane % (FN * 4) * 8;  // a lane's columns
+  float dj[8];
+  if (SQUARE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dj[e] = j + e < w.n ? da[j + e] : 0.0f;
+  }
+  u32x4 keep[FN * 2];
+  by_rows<F16Product, FM, FN>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
+    const int i = i0 + wi + i32 * 32 + row;
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    const bool there = i < w.n && j < w.np;
+    float di = 0.0f;
+    f16x8 old = {};
+    if (SQUARE && there) {
+      di = da[i];
+      old = *reinterpret_cast<const f16x8 *>(f + (int64_t)i * w.np + j);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool on = i == j + e, in = i < w.n && j + e < w.n;
+      float r;
+      if (SQUARE) {
+        const float sq = v[e] * (1.0f / (kScaleB * kScaleB)), fe = (float)old[e] * (1.0f / kScaleB);
+        if (on && in) diag[i] = cb * di + cc * (di * di + sq);
+        r = cb * fe + cc * ((di + dj[e]) * fe + sq);
+      } else {
+        r = v[e] * (1.0f / (kScaleX * kScaleX));
+        if (on && in) diag[i] = r;
+      }
+      v[e] = on || !in ? 0.0f : r * kScaleB;
+    }
+    keep[p] = eight_halves(v);
+    if (there) *reinterpret_cast<u32x4 *>(to + (int64_t)i * w.np + j) = keep[p];
+  }, [&](int i32) {
+    if (ti == tj) return;
+    by_columns<FN>(keep, own, [&](int c, int r, u32x4 h) {
+      const int col = j0 + wj + c, row = i0 + wi + i32 * 32 + r;
+      if (col < w.n && row < w.np) *reinterpret_cast<u32x4 *>(to + (int64_t)col * w.np + row) = h;
+    });
+  });
+}
+
+// The Gram matrix from the partial sums of its splits: a block 64 x 64 elements of a tile.
+__global__ __launch_bounds__(256) void k_ortho_join(const Work w, int tiles, int side, int splits) {
+  __shared__ float tile[64][65];
+  const int subs = side / 64, tid = threadIdx.x;
+  const int t = blockIdx.x / (subs * subs), sub = blockIdx.x % (subs * subs);
+  const int count = tiles * (tiles + 1) / 2;
+  int ti, tj;
+  triangle_at(near_tiles(t, count), tiles, ti, tj);
+  const int64_t k = blockIdx.z;
+  const int si = sub / subs * 64, sj = sub % subs * 64;
+  const int i0 = ti * side + si, j0 = tj * side + sj;
+  if (i0 >= w.np || j0 >= w.np) return;
+  _Float16 *f = w.f + k * w.n * w.np;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int r = p * 32 + (tid >> 3), c = (tid & 7) * 8;
+    float v[8] = {};
+    for (int s = 0; s < splits; ++s) {
+      const float *part = w.partial + ((k * splits + s) * count + t) * ((int64_t)side * side) + (si + r) * side + sj + c;
+      const f32x4 lo = *reinterpret_cast<const f32x4 *>(part), hi = *reinterpret_cast<const f32x4 *>(part + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += lo[e];
+        v[4 + e] += hi[e];
+      }
+    }
+    const int i = i0 + r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = j0 + c + e;
+      const bool in = i < w.n && j < w.n;
+      const float x = v[e] * (1.0f / (kScaleX * kScaleX));
+      if (i == j && in) w.diag_a[k * w.np + i] = x;
+      v[e] = i == j || !in ? 0.0f : x * kScaleB;
+      tile[r][c + e] = v[e];
+    }
+    if (i < w.n) *reinterpret_cast<u32x4 *>(f + (int64_t)i * w.np + j0 + c) = eight_halves(v);
+  }
+  if (ti == tj) return;  // (a tile on the diagonal is computed whole)
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int r = p * 32 + (tid >> 3), c = (tid & 7) * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = tile[c + e][r];
+    if (j0 + r < w.n) *reinterpret_cast<u32x4 *>(f + (int64_t)(j0 + r) * w.np + i0 + c) = eight_halves(v);
+  }
+}
+
+// X <- (a + diag B) X + (B - diag B) X; the last step's goes to `out` in bf16, by columns for a tall G.
+template <int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM *WN * 64) void k_ortho_update(const Work w, const OrthoArgs o, float ca,
+                                                              int tiles_i, int tiles_j, int last) {
+  GQ_ORTHO_LDS;
+  int ti, tj;
+  tile_at(near_tiles(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, ti, tj);
+  const int64_t k = blockIdx.z;
+  const int pitch = w.np * 2, i0 = ti * S::BM, j0 = tj * S::BN;
+  const uint8_t *b = reinterpret_cast<const uint8_t *>(w.b + k * w.n * w.np);
+  const uint8_t *xt = reinterpret_cast<const uint8_t *>(w.xt[0] + k * w.m * w.np);
+  const TileRows ra = {b + (int64_t)i0 * pitch, min(S::BM, w.n - i0)};
+  const TileRows rb = {xt + (int64_t)j0 * pitch, min(S::BN, w.m - j0)};
+  f32x16 acc[FM][FN] = {};
+  tile_product<F16Product, WM, WN, FM, FN>(lds0, lds1, lds2, lds3, ra, rb, pitch, 0, pitch / kStepBytes, acc);
+  const int wi = wave / WN * FM * 32, wj = wave % WN * FN * 32;
+  float *const x = w.x + k * w.n * w.mp;
+  _Float16 *const xh = w.xh + k * w.n * w.mp, *const next = w.xt[1] + k * w.m * w.np;
+  const float *const diag = w.diag_b + k * w.np;
+  uint16_t *const out = static_cast<uint16_t *>(o.out) + k * o.stride_o;
+  const bool flip = o.rows > o.cols;
+  const int j = j0 + wj + lane % (FN * 4) * 8;
+  u32x4 keep[FN * 2];
+  by_rows<F16Product, FM, FN>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
+    const int i = i0 + wi + i32 * 32 + row;
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, h[8] = {};
+    const bool there = i < w.n && j < w.mp;
+    if (there) {
+      float *at = x + (int64_t)i * w.mp + j;
+      const f32x4 x0 = *reinterpret_cast<const f32x4 *>(at), x1 = *reinterpret_cast<const f32x4 *>(at + 4);
+      const float s = ca + diag[i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = s * (e < 4 ? x0[e & 3] : x1[e & 3]) + v[e] * (1.0f / (kScaleX * kScaleB));
+        if (j + e >= w.m) v[e] = 0.0f;
+        h[e] = v[e] * kScaleX;
+      }
+      if (!last) {
+        *reinterpret_cast<f32x4 *>(at) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4 *>(at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        *reinterpret_cast<u32x4 *>(xh + (int64_t)i * w.mp + j) = eight_halves(h);
+      }
+    }
+    if (!last) {
+      keep[p] = eight_halves(h);
+    } else {
+      keep[p] = u32x4{to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3]), to_bf16_pair(v[4], v[5]), to_bf16_pair(v[6], v[7])};
+      if (!flip && there && j < w.m) {
+        uint16_t *at = out + (int64_t)i * o.ldo + j;
+        if (j + 8 <= w.m) {
+          *reinterpret_cast<u32x4_e2 *>(at) = keep[p];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (j + e < w.m) at[e] = (uint16_t)(keep[p][e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  }, [&](int i32) {
+    if (last && !flip) return;
+    by_columns<FN>(keep, own, [&](int c, int r, u32x4 h) {
+      const int col = j0 + wj + c, row = i0 + wi + i32 * 32 + r;
+      if (col >= w.m) return;
+      if (!last) {
+        if (row < w.np) *reinterpret_cast<u32x4 *>(next + (int64_t)col * w.np + row) = h;
+      } else if (row < w.n) {
+        uint16_t *at = out + (int64_t)col * o.ldo + row;
+        if (row + 8 <= w.n) {
+          *reinterpret_cast<u32x4_e2 *>(at) = h;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (row + e < w.n) at[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    });
+  });
+}
+
+// ---------------------------------------------------------------- host
+constexpr int kCus = 256;
+constexpr size_t kGroupBytes = (size_t)2 << 30;
+
+int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct Side {
+  int side, splits, each;
+};
+
+// Side of the symmetric products' tiles: the largest of which there is one a CU, else the smallest; the
+// Gram matrix, whose sums are long, in splits where its tiles leave CUs idle.
+Side gram_plan(int64_t batch, int64_t n, int64_t m) {
+  Side s = {64, 1, 0};
+  for (int side : {256, 128}) {
+    const int64_t t = (n + side - 1) / side;
+    if (batch * t * (t + 1) / 2 >= kCus / 2) {
+      s.side = side;
+      break;
+    }
+  }
+  const int64_t t = (n + s.side - 1) / s.side, count = batch * t * (t + 1) / 2;
+  const int64_t steps = up64(m) / 64;  // of 128 bytes
+  int64_t splits = kCus / count;
+  if (splits > steps / 4) splits = steps / 4;
+  if (splits > 16) splits = 16;
+  if (splits < 1) splits = 1;
+  s.each = (int)((steps + splits - 1) / splits) * 2;
+  s.splits = (int)((steps * 2 + s.each - 1) / s.each);
+  return s;
+}
+
+int update_side(int64_t batch, int64_t n, int64_t m) {
+  for (int side : {256, 128})
+    if (batch * ((n + side - 1) / side) * ((m + side - 1) / side) >= kCus / 2) return side;
+  return 64;
+}
+
+struct Sizes {
+  size_t x, xh, xt, f, diag, norms, partial;
+  size_t all() const { return x + xh + 2 * xt + 2 * f + 2 * diag + norms + partial; }
+};
+
+Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t n = rows < cols ? rows : cols, m = rows < cols ? cols : rows, np = up64(n), mp = up64(m);
+  const Side g = gram_plan(batch, n, m);
+  const int64_t t = (n + g.side - 1) / g.side;
+  Sizes z;
+  z.x = up256((size_t)(batch * n * mp) * 4);
+  z.xh = up256((size_t)(batch * n * mp) * 2);
+  z.xt = up256((size_t)(batch * m * np) * 2);
+  z.f = up256((size_t)(batch * n * np) * 2);
+  z.diag = up256((size_t)(batch * np) * 4);
+  z.norms = up256((size_t)batch * kNormBlocks * 8);
+  z.partial = g.splits > 1 ? up256((size_t)(batch * g.splits * (t * (t + 1) / 2)) * g.side * g.side * 4) : 0;
+  return z;
+}
+
+template <bool SQUARE, int WM, int WN, int FM, int FN>
+void symmetric(const Work &w, const OrthoArgs &a, int64_t batch, int splits, int each, hipStream_t s) {
+  using S = TileShape<WM, WN, FM, FN>;
+  const int t = (w.n + S::BM - 1) / S::BM;
+  k_ortho_symmetric<SQUARE, WM, WN, FM, FN>
+      <<<dim3((unsigned)(t * (t + 1) / 2), (unsigned)splits, (unsigned)batch), S::T, 0, s>>>(w, a.b, a.c, t, each);
+}
+
+template <bool SQUARE>
+void symmetric_of(int side, const Work &w, const OrthoArgs &a, int64_t batch, int splits, int each, hipStream_t s) {
+  if (side == 256)
+    symmetric<SQUARE, 2, 4, 4, 2>(w, a, batch, splits, each, s);
+  else if (side == 128)
+    symmetric<SQUARE, 2, 2, 2, 2>(w, a, batch, splits, each, s);
+  else
+    symmetric<SQUARE, 2, 2, 1, 1>(w, a, batch, splits, each, s);
+}
+
+template <int WM, int WN, int FM, int FN>
+void update(const Work &w, const OrthoArgs &a, int64_t batch, int last, hipStream_t s) {
+  using S = TileShape<WM, WN, FM, FN>;
+  const int ti = (w.n + S::BM - 1) / S::BM, tj = (w.m + S::BN - 1) / S::BN;
+  k_ortho_update<WM, WN, FM, FN><<<dim3((unsigned)(ti * tj), 1, (unsigned)batch), S::T, 0, s>>>(w, a, a.a, ti, tj, last);
+}
+
+template <int DT>
+void group(const OrthoArgs &a, hipStream_t s) {
+  const int64_t n = a.rows < a.cols ? a.rows : a.cols, m = a.rows < a.cols ? a.cols : a.rows;
+  const Sizes z = sizes_of(a.batch, a.rows, a.cols);
+  char *p = static_cast<char *>(a.scratch);
+  auto take = [&](size_t bytes) {
+    char *q = p;
+    p += bytes;
+    return q;
+  };
+  Work w;
+  w.n = (int)n;
+  w.m = (int)m;
+  w.np = (int)up64(n);
+  w.mp = (int)up64(m);
+  w.x = reinterpret_cast<float *>(take(z.x));
+  w.xh = reinterpret_cast<_Float16 *>(take(z.xh));
+  w.xt[0] = reinterpret_cast<_Float16 *>(take(z.xt));
+  w.xt[1] = reinterpret_cast<_Float16 *>(take(z.xt));
+  w.f = reinterpret_cast<_Float16 *>(take(z.f));
+  w.b = reinterpret_cast<_Float16 *>(take(z.f));
+  w.diag_a = reinterpret_cast<float *>(take(z.diag));
+  w.diag_b = reinterpret_cast<float *>(take(z.diag));
+  w.norms = reinterpret_cast<double *>(take(z.norms));
+  w.partial = reinterpret_cast<float *>(p);
+  // a block of the norm takes at least 2048 elements
+  int64_t parts = (a.rows * ((a.cols + 7) / 8) + 255) / 256;
+  if (parts > kNormBlocks) parts = kNormBlocks;
+  k_ortho_norm<DT><<<dim3((unsigned)parts, (unsigned)a.batch), 256, 0, s>>>(a, w.norms);
+  const dim3 tiles((unsigned)(w.mp / 64), (unsigned)(w.np / 64), (unsigned)a.batch);
+  if (a.rows > a.cols)
+    k_ortho_start<DT, true><<<tiles, 256, 0, s>>>(a, w, (int)parts);
+  else
+    k_ortho_start<DT, false><<<tiles, 256, 0, s>>>(a, w, (int)parts);
+  const Side g = gram_plan(a.batch, n, m);
+  const int t = (int)((n + g.side - 1) / g.side), side = update_side(a.batch, n, m);
+  for (int step = 0; step < a.steps; ++step) {
+    symmetric_of<false>(g.side, w, a, a.batch, g.splits, g.each, s);
+    if (g.splits > 1)
+      k_ortho_join<<<dim3((unsigned)(t * (t + 1) / 2 * (g.side / 64) * (g.side / 64)), 1, (unsigned)a.batch), 256, 0, s>>>(
+          w, t, g.side, g.splits);
+    symmetric_of<true>(g.side, w, a, a.batch, 1, w.np / 32, s);
+    const int last = step == a.steps - 1;
+    if (side == 256)
+      update<2, 4, 4, 2>(w, a, a.batch, last, s);
+    else if (side == 128)
+      update<2, 2, 2, 2>(w, a, a.batch, last, s);
+    else
+      update<2, 2, 1, 1>(w, a, a.batch, last, s);
+    _Float16 *was = w.xt[0];
+    w.xt[0] = w.xt[1];
+    w.xt[1] = was;
+  }
+}
+
+}  // namespace
+
+// Groups of at most kGroupBytes of scratch: a large batch gains nothing from more.
+int64_t ortho_group(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t fit = (int64_t)(kGroupBytes / sizes_of(1, rows, cols).all());
+  const int64_t most = fit < 1 ? 1 : fit > 4096 ? 4096 : fit;
+  return batch < most ? batch : most;
+}
+
+size_t ortho_scratch(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t group = ortho_group(batch, rows, cols);
+  const size_t whole = sizes_of(group, rows, cols).all();
+  const size_t rest = batch % group ? sizes_of(batch % group, rows, cols).all() : 0;
+  return whole > rest ? whole : rest;
+}
+
+hipError_t launch_orthogonalise(const OrthoArgs &a, int dtype, hipStream_t s) {
+  const int64_t most = ortho_group(a.batch, a.rows, a.cols);
+  for (int64_t first = 0; first < a.batch; first += most) {
+    OrthoArgs part = a;
+    part.g = static_cast<const char *>(a.g) + first * a.stride_g * (dtype == 0 ? 4 : 2);
+    part.out = static_cast<char *>(a.out) + first * a.stride_o * 2;
+    part.batch = a.batch - first < most ? a.batch - first : most;
+    dtype == 0 ? group<0>(part, s) : group<1>(part, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace gq

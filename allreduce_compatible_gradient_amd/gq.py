@@ -23,6 +23,8 @@ UNIFORM, EXP = 0, 1
 NORM_L2, NORM_MAX = 0, 1
 MX = 2                                   # element type of packed microscaled matrices
 MX_NEAREST, MX_STOCHASTIC = 0, 1
+INT8 = 3                                   # element type of packed 8-bit matrices
+INT_NEAREST, INT_STOCHASTIC = 0, 1
 
 if not os.path.exists(LIB_PATH):
     raise ImportError("libgq.so is not built (%s); run `python -m "
@@ -71,6 +73,16 @@ _SIGS = {
                                _p, _i64, _p]),
     "gq_distill_grad": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _p, _p, _i32, _f, _i32, _p, _p, _p,
                                _i64, _p]),
+    "gq_int_pitch": (_i64, [_i64]),
+    "gq_int_quantize": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i32, _u64, _u32, _u32, _p, _p, _p,
+                              _p, _p]),
+    "gq_int_matmul": (_i32, [_p, _p, _i32, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _i32, _i32, _p,
+                            _i64, _p]),
+    "gq_embedding": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _p, _i64, _f, _i32, _p, _i64, _p]),
+    "gq_embedding_grad": (_i32, [_p, _p, _i32, _p, _i64, _i64, _i64, _i64, _f, _i32, _i32, _p,
+                                 _i64, _p]),
+    "gq_orthogonalise": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _d, _d, _d, _p,
+                                _i64, _i64, _p]),
     "gq_global_norm_noalloc": (_i32, [_p, _p, _i32, _i32, _i64, _p, _i32, _p, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -663,6 +675,178 @@ def distill_grad(logits, top_ids, top_logprobs, temperature, tail, stats, row_we
         1 if tail else 0, _dev(stats, "stats", torch.float32), _row_weight(row_weight, rows), pd,
         ldd, _stream()))
     return dlogits
+
+
+# ----------------------------------------------------------------------------- 8-bit matrices
+class IntTensor:
+    """A packed 8-bit matrix of rows x cols: ``codes`` rows x int_pitch(cols) int8, padded with zeros,
+    and ``scales`` rows fp32; an element stands for code * scale."""
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        if (codes.dim() != 2 or cols < 1 or codes.shape[1] != int_pitch(cols)
+                or tuple(scales.shape) != (codes.shape[0],)):
+            raise ValueError("a packed matrix of %d columns has rows of %d codes and a scale each"
+                             % (cols, int_pitch(cols)))
+        self.codes, self.scales, self.rows, self.cols = codes, scales, codes.shape[0], cols
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "IntTensor":
+        t = IntTensor.__new__(IntTensor)
+        t.codes = torch.empty(rows, int_pitch(cols), dtype=torch.int8, device=device)
+        t.scales = torch.empty(rows, dtype=torch.float32, device=device)
+        t.rows, t.cols = rows, cols
+        return t
+
+
+def int_pitch(cols: int) -> int:
+    """Codes of a packed row of ``cols`` elements, padding included."""
+    return (cols + 127) // 128 * 128
+
+
+def _here(*tensors):
+    """The tensors lie on the current device, whose stream and context the call uses."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError("a tensor is on %s, the current device is cuda:%d" % (t.device, dev))
+
+
+def int_quantize(x, rounding=INT_NEAREST, seed=0, worker=0, index_base=0, by_rows=True,
+                by_cols=False, out: Optional[IntTensor] = None, out_t: Optional[IntTensor] = None,
+                ctx: Optional[Context] = None):
+    """Quantise a matrix to 8 bits with a scale for each row.  Returns (packed rows, packed columns),
+    an IntTensor of x and one of its transpose; None for one that is not asked for."""
+    ctx = ctx or context()
+    p, ld = _rows(x, "x")
+    rows, cols = x.shape
+    q = (out or IntTensor.empty(rows, cols, x.device)) if by_rows else None
+    qt = (out_t or IntTensor.empty(cols, rows, x.device)) if by_cols else None
+    if q is not None and (q.rows != rows or q.cols != cols):
+        raise ValueError("out must be a packed %d x %d matrix" % (rows, cols))
+    if qt is not None and (qt.rows != cols or qt.cols != rows):
+        raise ValueError("out_t must be a packed %d x %d matrix" % (cols, rows))
+    _here(x, q and q.codes, q and q.scales, qt and qt.codes, qt and qt.scales)
+    ctx.check(_lib.gq_int_quantize(
+        ctx.handle, p, _elt(x), rows, cols, ld, rounding, seed, worker, index_base,
+        None if q is None else _dev(q.codes, "out.codes", torch.int8),
+        None if q is None else _dev(q.scales, "out.scales", torch.float32),
+        None if qt is None else _dev(qt.codes, "out_t.codes", torch.int8),
+        None if qt is None else _dev(qt.scales, "out_t.scales", torch.float32), _stream()))
+    return q, qt
+
+
+def int_matmul(a, b: IntTensor, bias=None, out_dtype=BF16, out=None, accumulate=False,
+              ctx: Optional[Context] = None):
+    """a @ b.T (+ bias) (+ out): ``b`` packed N x K; ``a`` packed M x K, or an fp32 / bf16 matrix
+    that the call quantises to nearest.  Returns M x N of out_dtype."""
+    ctx = ctx or context()
+    if isinstance(a, IntTensor):
+        m, k = a.rows, a.cols
+        pa, ta, sa, lda = (_dev(a.codes, "a.codes", torch.int8), INT8,
+                           _dev(a.scales, "a.scales", torch.float32), 0)
+    else:
+        pa, lda = _rows(a, "a")
+        (m, k), ta, sa = a.shape, _elt(a), None
+    if k != b.cols:
+        raise ValueError("a has %d columns, b has %d" % (k, b.cols))
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(m, b.rows, dtype=_torch_dtype(out_dtype), device=b.codes.device)
+    po, ldo = _rows(out, "out", _torch_dtype(out_dtype))
+    if tuple(out.shape) != (m, b.rows):
+        raise ValueError("out must be %d x %d" % (m, b.rows))
+    if bias is not None and bias.numel() != b.rows:
+        raise ValueError("bias must hold %d values" % b.rows)
+    _here(a.codes if ta == INT8 else a, a.scales if ta == INT8 else None, b.codes, b.scales, bias, out)
+    ctx.check(_lib.gq_int_matmul(ctx.handle, pa, ta, sa, lda, _dev(b.codes, "b.codes", torch.int8),
+                                _dev(b.scales, "b.scales", torch.float32), m, b.rows, k,
+                                None if bias is None else _dev(bias, "bias", torch.float32),
+                                1 if accumulate else 0, out_dtype, po, ldo, _stream()))
+    return out
+
+
+# ----------------------------------------------------------------------------- embeddings
+def embedding(table, ids, scale=1.0, out_dtype=None, out=None, ctx: Optional[Context] = None):
+    """scale * table[ids] (tokens x dim; the table's type unless out_dtype says otherwise); an id
+    outside the table stands for no token and has a row of zeros."""
+    ctx = ctx or context()
+    p, ldt = _rows(table, "table")
+    vocab, dim = table.shape
+    code = _elt(table)
+    if out_dtype is None:
+        out_dtype = code
+    if ids.dim() != 1:
+        raise ValueError("ids must be a vector")
+    if out is None:
+        out = torch.empty(ids.numel(), dim, dtype=_torch_dtype(out_dtype), device=table.device)
+    po, ldo = _rows(out, "out", _torch_dtype(out_dtype))
+    if tuple(out.shape) != (ids.numel(), dim):
+        raise ValueError("out must be %d x %d" % (ids.numel(), dim))
+    _here(table, ids, out)
+    ctx.check(_lib.gq_embedding(ctx.handle, p, code, vocab, dim, ldt,
+                                _dev(ids, "ids", torch.int64), ids.numel(), scale, out_dtype, po,
+                                ldo, _stream()))
+    return out
+
+
+def embedding_grad(dout, ids, vocab, scale=1.0, out_dtype=F32, out=None, accumulate=False,
+                   ctx: Optional[Context] = None):
+    """The gradient of embedding's table (vocab x dim): scale times the sum of dout's rows of each
+    id.  ``accumulate`` adds it to ``out``, whose rows of no token are not touched."""
+    ctx = ctx or context()
+    p, ldd = _rows(dout, "dout")
+    tokens, dim = dout.shape
+    if ids.dim() != 1 or ids.numel() != tokens:
+        raise ValueError("ids must hold one entry a row")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(vocab, dim, dtype=_torch_dtype(out_dtype), device=dout.device)
+    po, ldt = _rows(out, "out", _torch_dtype(out_dtype))
+    if tuple(out.shape) != (vocab, dim):
+        raise ValueError("out must be %d x %d" % (vocab, dim))
+    _here(dout, ids, out)
+    ctx.check(_lib.gq_embedding_grad(ctx.handle, p, _elt(dout), _dev(ids, "ids", torch.int64),
+                                     tokens, dim, ldd, vocab, scale, 1 if accumulate else 0,
+                                     out_dtype, po, ldt, _stream()))
+    return out
+
+
+# ----------------------------------------------------------------------------- updates
+def _matrices(t: torch.Tensor, name: str, dtype=None):
+    """(address, row stride, stride between matrices) of a matrix or a batch of them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.dim() not in (2, 3):
+        raise ValueError("%s must be a matrix or a batch of matrices" % name)
+    rows, cols = t.shape[-2:]
+    if t.stride(-1) != 1 and cols > 1 and rows > 0:
+        raise ValueError("%s must have contiguous rows" % name)
+    ld = t.stride(-2) if rows > 1 else max(t.stride(-2), cols)
+    return t.data_ptr(), ld, t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else rows * ld
+
+
+def orthogonalise(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), out=None,
+                  ctx: Optional[Context] = None):
+    """The orthogonalised matrix (or batch of equal matrices) of g in bf16: from g / |g|_F, ``steps``
+    times every singular value s becomes a s + b s^3 + c s^5."""
+    ctx = ctx or context()
+    p, ldg, stride_g = _matrices(g, "g")
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    po, ldo, stride_o = _matrices(out, "out", torch.bfloat16)
+    if out.shape != g.shape:
+        raise ValueError("out must have g's shape, %s" % (tuple(g.shape),))
+    _here(g, out)
+    rows, cols = g.shape[-2:]
+    ctx.check(_lib.gq_orthogonalise(ctx.handle, p, _elt(g), g.shape[0] if g.dim() == 3 else 1, rows,
+                                    cols, ldg, stride_g, steps, *coefficients, po, ldo, stride_o,
+                                    _stream()))
+    return out
 
 
 def trim(ctx: Optional[Context] = None) -> None:

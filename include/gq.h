@@ -402,6 +402,90 @@ gq_status gq_distill_grad(gq_ctx *ctx, const void *logits, int32_t dtype, int64_
                           int32_t tail, const float *stats, const float *row_weight_or_null,
                           void *dlogits, int64_t ldd, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around a language model's layers: products of 8-bit integers, token embeddings with
+ * their gradient, and the orthogonalised update.  Row strides are in elements and at least the
+ * row's length; rows may start at any element of a 16-byte aligned buffer.  Buffers that a call
+ * writes do not overlap what it reads, unless it says so. */
+
+/* Packed 8-bit matrices (GQ_INT8).  A row of `cols` elements is cols codes of 8 bits in [-127, 127]
+ * and a scale: an element stands for code * scale.  With t the row's largest magnitude,
+ *   scale = fp32(t / 127),  inv = fp32(127 / t),
+ * the uniform grid of gq_quantize_pack with 127 levels and t in the place of S_g.  A row whose inv
+ * is not finite (t = 0, or t below 2^-121) has scale 0 and zero codes; one that holds an infinity
+ * or NaN has scale NaN and zero codes.  Rows are padded with zero codes to gq_int_pitch(cols), the
+ * next multiple of 128:  codes  rows x gq_int_pitch(cols) bytes,  scales  rows fp32.
+ * A matrix has at most 2^23 rows and 2^17 columns. */
+#define GQ_INT8 3
+/* rounding of gq_int_quantize */
+#define GQ_INT_NEAREST 0     /* x * inv rounded to the nearest integer, ties to even */
+#define GQ_INT_STOCHASTIC 1  /* u = min(fp32(|x| inv), 127): up from floor(u) with probability
+                               u - floor(u) */
+/* Bytes of a packed row of `cols` elements (0 for cols < 1). */
+int64_t gq_int_pitch(int64_t cols);
+
+/* Quantise a matrix by rows (codes, scales: rows x cols), by columns (codes_t, scales_t: the packed
+ * transpose, cols x rows, a scale for each column), or both; a pair that is not wanted is NULL.
+ * Stochastic: element (i, j) draws from (seed, worker, index_base + i * cols + j) as
+ * gq_quantize_pack does, by rows and by columns alike, and goes up when the draw r < p;
+ * rows * cols + index_base must not exceed 2^32 (seed, worker and index_base are not used to
+ * nearest).
+ *   x  rows x cols of `dtype` (GQ_F32 / GQ_BF16), row stride ld; at most 2^17 columns where it is
+ *      packed by rows, at most 2^17 rows where by columns, 2^23 otherwise */
+gq_status gq_int_quantize(gq_ctx *ctx, const void *x, int32_t dtype, int64_t rows, int64_t cols,
+                         int64_t ld, int32_t rounding, uint64_t seed, uint32_t worker,
+                         uint32_t index_base, int8_t *codes, float *scales, int8_t *codes_t,
+                         float *scales_t, void *stream);
+
+/* out = A B^T (+ bias) (+ out), A M x K with a scale for each row (token), B N x K with a scale for
+ * each row (output channel): out_ij = (sum_k a_ik b_jk) sa_i sb_j, the sum exact in 32-bit integers
+ * (K <= 2^17), the rest in fp32.
+ *   a       packed codes (a_dtype GQ_INT8, with a_scales; lda unused), or fp32 / bf16 rows of stride
+ *           lda (a_scales NULL) that are quantised to nearest as gq_int_quantize would
+ *   b       packed codes and scales
+ *   bias    N fp32, or NULL;  accumulate: 1 adds to what `out` holds
+ *   out     M x N of out_dtype, row stride ldo */
+gq_status gq_int_matmul(gq_ctx *ctx, const void *a, int32_t a_dtype, const float *a_scales,
+                       int64_t lda, const int8_t *b, const float *b_scales, int64_t M, int64_t N,
+                       int64_t K, const float *bias_or_null, int32_t accumulate,
+                       int32_t out_dtype, void *out, int64_t ldo, void *stream);
+
+/* Token embedding: out_t = scale * table[ids_t], rounded once.  An id outside [0, vocab) stands for
+ * no token (padding): its row is zeros.  At most 2^24 tokens, 2^23 rows of the table and 2^20
+ * elements of a row.
+ *   table  vocab x dim of `dtype`, row stride ldt;  ids  tokens int64
+ *   out    tokens x dim of out_dtype, row stride ldo */
+gq_status gq_embedding(gq_ctx *ctx, const void *table, int32_t dtype, int64_t vocab, int64_t dim,
+                       int64_t ldt, const int64_t *ids, int64_t tokens, float scale,
+                       int32_t out_dtype, void *out, int64_t ldo, void *stream);
+
+/* The gradient of the table: dtable_v = scale * sum of dout_t over the tokens t with ids_t = v, in
+ * fp32 and in an order that the ids alone set, so that equal calls have equal bits.  Every row is
+ * written (zeros where an id has no token); with accumulate = 1 the sum is added to what dtable
+ * holds, and rows of no token are not touched.
+ *   dout    tokens x dim of `dtype`, row stride ldd
+ *   dtable  vocab x dim of out_dtype, row stride ldt */
+gq_status gq_embedding_grad(gq_ctx *ctx, const void *dout, int32_t dtype, const int64_t *ids,
+                            int64_t tokens, int64_t dim, int64_t ldd, int64_t vocab, float scale,
+                            int32_t accumulate, int32_t out_dtype, void *dtable, int64_t ldt,
+                            void *stream);
+
+/* Orthogonalised update by Newton-Schulz products: X = G / |G|_F, then `steps` times
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X
+ * (on the transpose where rows > cols), which takes every singular value s to a s + b s^3 + c s^5.
+ * Operands of the products are rounded to 11 bits, their diagonals apart and X itself held in fp32,
+ * and the result is rounded to bf16, the type of the output: it carries no more.  A matrix of
+ * zeros gives zeros, one that holds an infinity or NaN NaN everywhere.  The coefficients have to
+ * keep singular values that begin in [0, 1] below 7.5, and |b s^2 + c s^4| below 60 (GQ_EINVAL
+ * otherwise).
+ *   g    batch matrices of rows x cols of `dtype`, row stride ldg, stride_g elements apart
+ *   out  the same in bf16, row stride ldo, stride_o elements apart;  1 <= steps <= 32
+ * rows and cols at most 2^16, batch at most 2^16. */
+gq_status gq_orthogonalise(gq_ctx *ctx, const void *g, int32_t dtype, int64_t batch, int64_t rows,
+                           int64_t cols, int64_t ldg, int64_t stride_g, int32_t steps, double a,
+                           double b, double c, void *out, int64_t ldo, int64_t stride_o,
+                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif
