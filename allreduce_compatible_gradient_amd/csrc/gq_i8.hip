@@ -277,34 +277,27 @@ __device__ __forceinline__ void put_one(const I8MatmulArgs &a, int64_t m, int64_
 
 typedef i32x4 i32x4_e4 __attribute__((aligned(4)));
 
-template <int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(WM *WN * 64) void k_i8_matmul(const I8MatmulArgs a, int pitch,
-                                                           int tiles_m, int tiles_n,
-                                                           int steps_each) {
-  using S = TileShape<WM, WN, FM, FN>;
-  __shared__ __align__(1024) uint8_t lds0[S::kStage];
-  __shared__ __align__(1024) uint8_t lds1[S::kStage];
-  __shared__ __align__(1024) uint8_t lds2[S::kStage];
-  __shared__ __align__(1024) uint8_t lds3[S::kStage];
+template <class S>
+__global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pitch, int tiles_m,
+                                                    int tiles_n, int steps_each) {
+  constexpr int WN = S::WN, FM = S::FM, FN = S::FN;
+  GQ_TILE_LDS(S);
   int bm, bn;
   tile_at(near_tiles(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, bm, bn);
   const int64_t m0 = (int64_t)bm * S::BM, n0 = (int64_t)bn * S::BN;
   const TileRows ra = {static_cast<const uint8_t *>(a.a) + m0 * pitch, (int)min((int64_t)S::BM, a.M - m0)};
   const TileRows rb = {reinterpret_cast<const uint8_t *>(a.b) + n0 * pitch, (int)min((int64_t)S::BN, a.N - n0)};
   const int step0 = blockIdx.y * steps_each;
-  i32x16 acc[FM][FN] = {};
-  tile_product<I8Product, WM, WN, FM, FN>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
-                                          min(steps_each, pitch / kStepBytes - step0), acc);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  constexpr int kOwn = 32 * FN * 128, kPer = S::kStage / kOwn;  // a wave's part of LDS
-  static_assert(kPer * 4 >= WM * WN && kPer > 0, "the waves' rows fit the buffers");
-  uint8_t *const own = (wave / kPer == 0 ? lds0 : wave / kPer == 1 ? lds1 : wave / kPer == 2 ? lds2 : lds3) + wave % kPer * kOwn;
+  i32x4 acc[FM * 2][FN * 2] = {};
+  tile_product<I8Product, S>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
+                             min(steps_each, pitch / kStepBytes - step0), acc);
+  const int lane = threadIdx.x & 63;
   const int64_t wm0 = m0 + wave / WN * FM * 32, wn0 = n0 + wave % WN * FN * 32;
   const int64_t n = wn0 + lane % (FN * 4) * 8;  // a lane's columns
   auto nothing = [](int) {};
   if (gridDim.y > 1) {
     int32_t *part = a.partial + (int64_t)blockIdx.y * a.M * a.N;
-    by_rows<I8Product, FM, FN>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
+    by_rows<I8Product, S>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
       const int64_t m = wm0 + i * 32 + row;
       if (m >= a.M || n >= a.N) return;
       int32_t *o = part + m * a.N + n;
@@ -328,7 +321,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_i8_matmul(const I8MatmulArgs a,
   }
   const bool add = a.bias != nullptr;  // without a bias -0 stays -0
   const bool lines = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.ldo * 2) & 127) == 0;
-  by_rows<I8Product, FM, FN>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
+  by_rows<I8Product, S>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
     const int64_t m = wm0 + i * 32 + row;
     if (m >= a.M || n >= a.N) return;
     const float sa = a.a_scales[m];
@@ -526,15 +519,15 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
     if (splits > 16) splits = 16;
     if (splits < 1) splits = 1;
   }
-  p.each = (int)((steps + splits - 1) / splits) * 2;  // steps of the loop: 64 bytes
-  p.splits = (int)((steps * 2 + p.each - 1) / p.each);
+  p.each = (int)((steps + splits - 1) / splits);
+  p.splits = (int)((steps + p.each - 1) / p.each);
   return p;
 }
 
-template <int WM, int WN, int FM, int FN>
+template <class S>
 void tiles_of(const I8MatmulArgs &a, const Plan &p, hipStream_t s) {
-  const int tm = (int)((a.M + p.bm - 1) / p.bm), tn = (int)((a.N + p.bn - 1) / p.bn);
-  k_i8_matmul<WM, WN, FM, FN><<<dim3((unsigned)(tm * tn), p.splits), WM * WN * 64, 0, s>>>(
+  const int tm = (int)((a.M + S::BM - 1) / S::BM), tn = (int)((a.N + S::BN - 1) / S::BN);
+  k_i8_matmul<S><<<dim3((unsigned)(tm * tn), p.splits), S::T, 0, s>>>(
       a, (int)i8_pitch(a.K), tm, tn, p.each);
 }
 
@@ -601,11 +594,11 @@ hipError_t launch_i8_matmul(const I8MatmulArgs &a, hipStream_t s) {
   }
   const Plan p = plan(a.M, a.N, a.K);
   if (p.bm == 256)
-    tiles_of<2, 4, 4, 2>(a, p, s);
+    tiles_of<TileShape<2, 4, 4, 2, 2>>(a, p, s);
   else if (p.bm == 128)
-    tiles_of<2, 2, 2, 2>(a, p, s);
+    tiles_of<TileShape<2, 2, 2, 2, 2>>(a, p, s);
   else
-    tiles_of<1, 4, 2, 1>(a, p, s);
+    tiles_of<TileShape<1, 4, 2, 1, 2>>(a, p, s);
   if (p.splits > 1) k_i8_join<<<(unsigned)((a.M * a.N + 255) / 256), 256, 0, s>>>(a, p.splits);
   return hipGetLastError();
 }

@@ -161,27 +161,14 @@ __device__ __forceinline__ void triangle_at(int t, int tiles, int &i, int &j) {
   j = t - (i * tiles - i * (i - 1) / 2) + i;
 }
 
-#define GQ_ORTHO_LDS                                                                              \
-  using S = TileShape<WM, WN, FM, FN>;                                                            \
-  __shared__ __align__(1024) uint8_t lds0[S::kStage];                                             \
-  __shared__ __align__(1024) uint8_t lds1[S::kStage];                                             \
-  __shared__ __align__(1024) uint8_t lds2[S::kStage];                                             \
-  __shared__ __align__(1024) uint8_t lds3[S::kStage];                                             \
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;     \
-  constexpr int kOwn = 32 * FN * 128, kPer = S::kStage / kOwn;                                    \
-  static_assert(kPer > 0 && kPer * 4 >= WM * WN && kOwn >= FN * 32 * 72, "the waves' parts");     \
-  uint8_t *const own = (wave / kPer == 0   ? lds0                                                 \
-                        : wave / kPer == 1 ? lds1                                                 \
-                        : wave / kPer == 2 ? lds2                                                 \
-                                           : lds3) +                                              \
-                       wave % kPer * kOwn
-
 // A symmetric product of the rows of `of` (n of them, pitch bytes each).  SQUARE false: the Gram
 // matrix of X, to F and diag_a (or partial sums, where gridDim.y > 1); true: F^2, to B and diag_b.
-template <bool SQUARE, int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(WM *WN * 64) void k_ortho_symmetric(const Work w, float cb, float cc,
-                                                                 int tiles, int steps_each) {
-  GQ_ORTHO_LDS;
+template <bool SQUARE, class S>
+__global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb, float cc, int tiles,
+                                                          int steps_each) {
+  constexpr int WN = S::WN, FM = S::FM, FN = S::FN;
+  GQ_TILE_LDS(S);
+  const int lane = threadIdx.x & 63;
   static_assert(S::BM == S::BN, "mirrored tiles");
   int ti, tj;
   triangle_at(near_tiles(blockIdx.x, tiles * (tiles + 1) / 2), tiles, ti, tj);
@@ -191,13 +178,13 @@ __global__ __launch_bounds__(WM *WN * 64) void k_ortho_symmetric(const Work w, f
   const TileRows ra = {of + (int64_t)i0 * pitch, min(S::BM, w.n - i0)};
   const TileRows rb = {of + (int64_t)j0 * pitch, min(S::BN, w.n - j0)};
   const int step0 = blockIdx.y * steps_each;
-  f32x16 acc[FM][FN] = {};
-  tile_product<F16Product, WM, WN, FM, FN>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
+  f32x4 acc[FM * 2][FN * 2] = {};
+  tile_product<F16Product, S>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
                                            min(steps_each, pitch / kStepBytes - step0), acc);
   const int wi = wave / WN * FM * 32, wj = wave % WN * FN * 32;
   if (!SQUARE && gridDim.y > 1) {
     float *part = w.partial + (((int64_t)k * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * (S::BM * S::BN);
-    by_rows<F16Product, FM, FN>(acc, own, [&](int i, int, int row, int col, f32x4 lo, f32x4 hi) {
+    by_rows<F16Product, S>(acc, own, [&](int i, int, int row, int col, f32x4 lo, f32x4 hi) {
       f32x4 *o = reinterpret_cast<f32x4 *>(part + (wi + i * 32 + row) * S::BN + wj + col);
       o[0] = lo;
       o[1] = hi;
@@ -215,7 +202,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_ortho_symmetric(const Work w, f
     for (int e = 0; e < 8; ++e) dj[e] = j + e < w.n ? da[j + e] : 0.0f;
   }
   u32x4 keep[FN * 2];
-  by_rows<F16Product, FM, FN>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
+  by_rows<F16Product, S>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
     const int i = i0 + wi + i32 * 32 + row;
     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     const bool there = i < w.n && j < w.np;
@@ -301,10 +288,13 @@ __global__ __launch_bounds__(256) void k_ortho_join(const Work w, int tiles, int
 }
 
 // X <- (a + diag B) X + (B - diag B) X; the last step's goes to `out` in bf16, by columns for a tall G.
-template <int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(WM *WN * 64) void k_ortho_update(const Work w, const OrthoArgs o, float ca,
-                                                              int tiles_i, int tiles_j, int last) {
-  GQ_ORTHO_LDS;
+template <class S>
+__global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const OrthoArgs o, float ca,
+                                                       int tiles_i, int tiles_j, int last) {
+  constexpr int WN = S::WN, FM = S::FM, FN = S::FN;
+  GQ_TILE_LDS(S);
+  static_assert(S::kOwn >= FN * 32 * 72, "a wave's columns fit its part");
+  const int lane = threadIdx.x & 63;
   int ti, tj;
   tile_at(near_tiles(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, ti, tj);
   const int64_t k = blockIdx.z;
@@ -313,8 +303,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_ortho_update(const Work w, cons
   const uint8_t *xt = reinterpret_cast<const uint8_t *>(w.xt[0] + k * w.m * w.np);
   const TileRows ra = {b + (int64_t)i0 * pitch, min(S::BM, w.n - i0)};
   const TileRows rb = {xt + (int64_t)j0 * pitch, min(S::BN, w.m - j0)};
-  f32x16 acc[FM][FN] = {};
-  tile_product<F16Product, WM, WN, FM, FN>(lds0, lds1, lds2, lds3, ra, rb, pitch, 0, pitch / kStepBytes, acc);
+  f32x4 acc[FM * 2][FN * 2] = {};
+  tile_product<F16Product, S>(lds0, lds1, lds2, lds3, ra, rb, pitch, 0, pitch / kStepBytes, acc);
   const int wi = wave / WN * FM * 32, wj = wave % WN * FN * 32;
   float *const x = w.x + k * w.n * w.mp;
   _Float16 *const xh = w.xh + k * w.n * w.mp, *const next = w.xt[1] + k * w.m * w.np;
@@ -323,7 +313,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_ortho_update(const Work w, cons
   const bool flip = o.rows > o.cols;
   const int j = j0 + wj + lane % (FN * 4) * 8;
   u32x4 keep[FN * 2];
-  by_rows<F16Product, FM, FN>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
+  by_rows<F16Product, S>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
     const int i = i0 + wi + i32 * 32 + row;
     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, h[8] = {};
     const bool there = i < w.n && j < w.mp;
@@ -407,8 +397,8 @@ Side gram_plan(int64_t batch, int64_t n, int64_t m) {
   if (splits > steps / 4) splits = steps / 4;
   if (splits > 16) splits = 16;
   if (splits < 1) splits = 1;
-  s.each = (int)((steps + splits - 1) / splits) * 2;
-  s.splits = (int)((steps * 2 + s.each - 1) / s.each);
+  s.each = (int)((steps + splits - 1) / splits);
+  s.splits = (int)((steps + s.each - 1) / s.each);
   return s;
 }
 
@@ -438,29 +428,27 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols) {
   return z;
 }
 
-template <bool SQUARE, int WM, int WN, int FM, int FN>
+template <bool SQUARE, class S>
 void symmetric(const Work &w, const OrthoArgs &a, int64_t batch, int splits, int each, hipStream_t s) {
-  using S = TileShape<WM, WN, FM, FN>;
   const int t = (w.n + S::BM - 1) / S::BM;
-  k_ortho_symmetric<SQUARE, WM, WN, FM, FN>
+  k_ortho_symmetric<SQUARE, S>
       <<<dim3((unsigned)(t * (t + 1) / 2), (unsigned)splits, (unsigned)batch), S::T, 0, s>>>(w, a.b, a.c, t, each);
 }
 
 template <bool SQUARE>
 void symmetric_of(int side, const Work &w, const OrthoArgs &a, int64_t batch, int splits, int each, hipStream_t s) {
   if (side == 256)
-    symmetric<SQUARE, 2, 4, 4, 2>(w, a, batch, splits, each, s);
+    symmetric<SQUARE, TileShape<2, 4, 4, 2, 2>>(w, a, batch, splits, each, s);
   else if (side == 128)
-    symmetric<SQUARE, 2, 2, 2, 2>(w, a, batch, splits, each, s);
+    symmetric<SQUARE, TileShape<2, 2, 2, 2, 2>>(w, a, batch, splits, each, s);
   else
-    symmetric<SQUARE, 2, 2, 1, 1>(w, a, batch, splits, each, s);
+    symmetric<SQUARE, TileShape<2, 2, 1, 1, 4>>(w, a, batch, splits, each, s);
 }
 
-template <int WM, int WN, int FM, int FN>
+template <class S>
 void update(const Work &w, const OrthoArgs &a, int64_t batch, int last, hipStream_t s) {
-  using S = TileShape<WM, WN, FM, FN>;
   const int ti = (w.n + S::BM - 1) / S::BM, tj = (w.m + S::BN - 1) / S::BN;
-  k_ortho_update<WM, WN, FM, FN><<<dim3((unsigned)(ti * tj), 1, (unsigned)batch), S::T, 0, s>>>(w, a, a.a, ti, tj, last);
+  k_ortho_update<S><<<dim3((unsigned)(ti * tj), 1, (unsigned)batch), S::T, 0, s>>>(w, a, a.a, ti, tj, last);
 }
 
 template <int DT>
@@ -504,14 +492,14 @@ void group(const OrthoArgs &a, hipStream_t s) {
     if (g.splits > 1)
       k_ortho_join<<<dim3((unsigned)(t * (t + 1) / 2 * (g.side / 64) * (g.side / 64)), 1, (unsigned)a.batch), 256, 0, s>>>(
           w, t, g.side, g.splits);
-    symmetric_of<true>(g.side, w, a, a.batch, 1, w.np / 32, s);
+    symmetric_of<true>(g.side, w, a, a.batch, 1, w.np / 64, s);
     const int last = step == a.steps - 1;
     if (side == 256)
-      update<2, 4, 4, 2>(w, a, a.batch, last, s);
+      update<TileShape<2, 4, 4, 2, 2>>(w, a, a.batch, last, s);
     else if (side == 128)
-      update<2, 2, 2, 2>(w, a, a.batch, last, s);
+      update<TileShape<2, 2, 2, 2, 2>>(w, a, a.batch, last, s);
     else
-      update<2, 2, 1, 1>(w, a, a.batch, last, s);
+      update<TileShape<2, 2, 1, 1, 4>>(w, a, a.batch, last, s);
     _Float16 *was = w.xt[0];
     w.xt[0] = w.xt[1];
     w.xt[1] = was;

@@ -1,9 +1,11 @@
-// gq_tiles.h -- one block's tile of C = A B^T for operands whose rows are read in pieces of 64
-// bytes: 64 codes of 8 bits (v_mfma_i32_32x32x32_i8) or 32 halves (v_mfma_f32_32x32x16_f16).  Both
-// instructions take 32 bytes of 32 rows, lane l the 16 bytes of row l mod 32 at l / 32, in the same
-// number of cycles, so one loop serves both; the result has column l mod 32 and rows
-// 8 i + 4 (l / 32) + 0..3.  B's rows are the first operand, so a lane ends with four neighbouring
-// columns of one row of C.
+// gq_tiles.h -- one block's tile of C = A B^T for operands whose rows are read in pieces of 128
+// bytes: 128 codes of 8 bits (v_mfma_i32_16x16x64_i8) or 64 halves (v_mfma_f32_16x16x32_f16).  Both
+// instructions take 64 bytes of 16 rows, lane l the 16 bytes of row l mod 16 at l / 16, in the same
+// number of cycles, so one loop serves both; the result has column l mod 16 and rows
+// 4 (l / 16) + 0..3.  B's rows are the first operand, so a lane ends with four neighbouring columns
+// of one row of C.  (Products bound by the card's power gain by these over 32 x 32 ones: a loop of
+// nothing else reaches 1.80 against 1.56 PFLOP/s in halves and 3.9 against 3.4 in 8 bits on random
+// data.)
 #pragma once
 
 #include "gq_device.h"
@@ -12,26 +14,23 @@ namespace gq {
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 struct F16Product {
-  typedef f32x16 Acc;
   typedef f32x4 Four;
-  static __device__ __forceinline__ Acc mul(i32x4 first, i32x4 second, Acc acc) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, first),
+  static __device__ __forceinline__ Four mul(i32x4 first, i32x4 second, Four acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, first),
                                                   __builtin_bit_cast(f16x8, second), acc, 0, 0, 0);
   }
 };
 
 struct I8Product {
-  typedef i32x16 Acc;
   typedef i32x4 Four;
-  static __device__ __forceinline__ Acc mul(i32x4 first, i32x4 second, Acc acc) {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(first, second, acc, 0, 0, 0);
+  static __device__ __forceinline__ Four mul(i32x4 first, i32x4 second, Four acc) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(first, second, acc, 0, 0, 0);
   }
 };
 
-constexpr int kStepBytes = 64;  // of a row, one step of the loop
+constexpr int kStepBytes = 128;  // of a row, one step of the loop: a whole line
 
 // An operand's rows as one tile needs them.
 struct TileRows {
@@ -39,12 +38,30 @@ struct TileRows {
   int rows;              // rows there are, at most the tile's: later ones repeat the last
 };
 
-// Shape of a block's tile: WM x WN waves, a wave FM x FN results of 32 x 32.
-template <int WM, int WN, int FM, int FN>
+// Shape of a block's tile: WM x WN waves, a wave 32 FM x 32 FN results, NB buffers of a step's operands.
+template <int WM_, int WN_, int FM_, int FN_, int NB_>
 struct TileShape {
+  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, NB = NB_;
   static constexpr int BM = WM * FM * 32, BN = WN * FN * 32, T = WM * WN * 64;
-  static constexpr int kStage = (BM + BN) * kStepBytes;  // bytes of a step's operands
+  static constexpr int kStage = (BM + BN) * kStepBytes;
+  static constexpr int kOwn = 32 * FN * 128, kPer = kStage / kOwn;  // a wave's part after the products
+  static_assert(NB == 2 || NB == 4, "buffers");
+  static_assert(kPer > 0 && kPer * NB >= WM * WN, "the waves' parts fit the buffers");
 };
+
+// The buffers of a block's tile (arrays of their own), and the wave's part of them once the products
+// are done.
+#define GQ_TILE_LDS(S)                                                              \
+  __shared__ __align__(1024) uint8_t lds0[S::kStage];                               \
+  __shared__ __align__(1024) uint8_t lds1[S::kStage];                               \
+  __shared__ __align__(1024) uint8_t lds2[S::NB > 2 ? S::kStage : 16];              \
+  __shared__ __align__(1024) uint8_t lds3[S::NB > 2 ? S::kStage : 16];              \
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);                \
+  uint8_t *const own = (wave / S::kPer == 0   ? lds0                                \
+                        : wave / S::kPer == 1 ? lds1                                \
+                        : wave / S::kPer == 2 ? lds2                                \
+                                              : lds3) +                             \
+                       wave % S::kPer * S::kOwn
 
 // Waits until at most N of the wave's loads are on their way and its LDS reads are done, then for the
 // block's other waves: what was loaded before those N is in LDS for all of them, and no wave still
@@ -58,20 +75,29 @@ __device__ __forceinline__ void arrive_but() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Steps step0 .. step0 + count - 1 (count even, at least 2) of the tile's sums.  Operands go from
-// memory to LDS without registers, three steps ahead, in four buffers of their own names: LDS reads
-// wait for their own buffer's loads only.  Row r's 16-byte chunk c is kept at chunk
-// c XOR (r / 4 mod 4): 16 rows' reads of one chunk column fall on 16 different places of 256 bytes.
+// Steps step0 .. step0 + count - 1 (count at least 1) of the tile's sums.  Operands go from memory to
+// LDS without registers, into NB buffers in turn, each a static array of its own: LDS reads wait for
+// their own buffer's loads only.  Row r's 16-byte chunk c is kept at chunk c XOR key(r), key(r) =
+// (r XOR r / 8 mod 4) mod 8: 16 rows' reads of one chunk column fall on 16 different places of 256
+// bytes.
+//
+// A step is four groups of products, and a group's operands are read from LDS while the group before
+// is multiplied, across the barrier too: it stands before a step's last group, when the step's own
+// operands are all in registers, so that its buffer is free for the step NB further on and the next
+// step's has arrived.
 // Returns with every load done and every wave past its reads: the buffers are free.
-template <class P, int WM, int WN, int FM, int FN>
+__device__ __forceinline__ int tile_key(int r) { return (r ^ (r >> 3 & 3)) & 7; }
+
+template <class P, class S>
 __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8_t *lds2,
                                              uint8_t *lds3, TileRows a, TileRows b, int pitch,
                                              int step0, int count,
-                                             typename P::Acc (&acc)[FM][FN]) {
+                                             typename P::Four (&acc)[S::FM * 2][S::FN * 2]) {
 #if defined(__HIP_DEVICE_COMPILE__)  // buffer resources are a type of the device only
-  using S = TileShape<WM, WN, FM, FN>;
-  constexpr int T = S::T, CA = S::BM * 4 / T, CB = S::BN * 4 / T;  // 16-byte chunks a thread and step
-  static_assert(S::BM * 4 % T == 0 && S::BN * 4 % T == 0 && T / 4 % 16 == 0, "whole chunks");
+  constexpr int WN = S::WN, FM = S::FM, FN = S::FN, NB = S::NB;
+  uint8_t *const lds[4] = {lds0, lds1, lds2, lds3};
+  constexpr int T = S::T, CA = S::BM * 8 / T, CB = S::BN * 8 / T;  // 16-byte chunks a thread and step
+  static_assert(S::BM * 8 % T == 0 && S::BN * 8 % T == 0 && T / 8 % 32 == 0, "whole chunks");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -80,63 +106,76 @@ __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8
   const auto rb = __builtin_amdgcn_make_buffer_rsrc((void *)b.first, 0, b.rows * pitch, 0x00027000);
   int off_a[CA], off_b[CB];
   {
-    const int row = tid >> 2, chunk = ((tid & 3) ^ (row >> 2 & 3)) << 4;  // T / 4 rows keep the key
+    const int row = tid >> 3, chunk = ((tid & 7) ^ tile_key(row)) << 4;  // T / 8 rows keep the key
 #pragma unroll
-    for (int i = 0; i < CA; ++i) off_a[i] = min(row + i * (T / 4), a.rows - 1) * pitch + chunk;
+    for (int i = 0; i < CA; ++i) off_a[i] = min(row + i * (T / 8), a.rows - 1) * pitch + chunk;
 #pragma unroll
-    for (int i = 0; i < CB; ++i) off_b[i] = min(row + i * (T / 4), b.rows - 1) * pitch + chunk;
+    for (int i = 0; i < CB; ++i) off_b[i] = min(row + i * (T / 8), b.rows - 1) * pitch + chunk;
   }
-  const int r32 = lane & 31, half = lane >> 5;
-  int frag[2];
+  const int r16 = lane & 15;
+  int frag[2];  // rows 16 further on have another key: (r XOR r / 8 mod 4) mod 8 changes by 2
 #pragma unroll
-  for (int j = 0; j < 2; ++j) frag[j] = r32 * 64 + (((2 * j + half) ^ (r32 >> 2 & 3)) << 4);
+  for (int j = 0; j < 2; ++j) frag[j] = r16 * 128 + (((4 * j + (lane >> 4)) ^ tile_key(r16)) << 4);
   const int last = step0 + count - 1;
-  auto issue = [&](uint8_t *lds, int k) {  // past the end: the last step again, not multiplied
+  auto issue = [&](uint8_t *to, int k) {  // past the end: the last step again, not multiplied
     const int at = min(k, last) * kStepBytes;
 #pragma unroll
     for (int i = 0; i < CA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_PTR void *)(lds + (i * T + wave * 64) * 16),
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_PTR void *)(to + (i * T + wave * 64) * 16),
                                                16, off_a[i], at, 0, 0);
 #pragma unroll
     for (int i = 0; i < CB; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (LDS_PTR void *)(lds + S::BM * 64 + (i * T + wave * 64) * 16), 16, off_b[i], at, 0, 0);
+          rb, (LDS_PTR void *)(to + S::BM * 128 + (i * T + wave * 64) * 16), 16, off_b[i], at, 0, 0);
   };
-  auto step = [&](const uint8_t *now, uint8_t *free, int k) {
-    arrive_but<2 * (CA + CB)>();
-    issue(free, k + 3);
-    const uint8_t *la = now + wm * FM * 2048, *lb = now + (S::BM + wn * FN * 32) * 64;
-    i32x4 fa[2][FM], fb[2][FN];
-    auto fetch = [&](int j) {
+  i32x4 fa[2][FM], fb[2][FN * 2];
+  // Group s: half of the wave's rows of A (s odd: the second) times its rows of B, 64 bytes of each
+  // (s / 2: which).
+  auto fetch = [&](const uint8_t *from, int s) {
+    const int g = s >> 1;
+    if ((s & 1) == 0) {
+      const uint8_t *lb = from + (S::BM + wn * FN * 32) * 128;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) fa[j][i] = *reinterpret_cast<const i32x4 *>(la + frag[j] + i * 2048);
+      for (int i = 0; i < FN * 2; ++i) fb[g][i] = *reinterpret_cast<const i32x4 *>(lb + i * 2048 + (frag[g] ^ (i & 1) << 5));
+    }
+    const uint8_t *la = from + (wm * FM * 32 + (s & 1) * FM * 16) * 128;
 #pragma unroll
-      for (int i = 0; i < FN; ++i) fb[j][i] = *reinterpret_cast<const i32x4 *>(lb + frag[j] + i * 2048);
-    };
-    fetch(0);
-    fetch(1);
+    for (int i = 0; i < FM; ++i)
+      fa[s & 1][i] = *reinterpret_cast<const i32x4 *>(la + i * 2048 + (frag[g] ^ ((s * FM + i) & 1) << 5));
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int m = 0; m < FM; ++m)
-#pragma unroll
-        for (int n = 0; n < FN; ++n) acc[m][n] = P::mul(fb[j][n], fa[j][m], acc[m][n]);
   };
-  issue(lds0, step0);
-  issue(lds1, step0 + 1);
-  issue(lds2, step0 + 2);
+  auto multiply = [&](int s) {
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN * 2; ++n)
+        acc[(s & 1) * FM + m][n] = P::mul(fb[s >> 1][n], fa[s & 1][m], acc[(s & 1) * FM + m][n]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int i = 0; i < NB; ++i) issue(lds[i], step0 + i);
+  arrive_but<(NB - 1) * (CA + CB)>();
+  fetch(lds[0], 0);
+  auto step = [&](int i, int k) {
+    fetch(lds[i], 1);
+    multiply(0);
+    fetch(lds[i], 2);
+    multiply(1);
+    fetch(lds[i], 3);
+    multiply(2);
+    arrive_but<(NB - 2) * (CA + CB)>();
+    issue(lds[i], k + NB);
+    fetch(lds[(i + 1) % NB], 0);  // of a step that is not there, after the last: not multiplied
+    multiply(3);
+  };
   int k = step0;
-  for (; k + 3 <= last; k += 4) {
-    step(lds0, lds3, k);
-    step(lds1, lds0, k + 1);
-    step(lds2, lds1, k + 2);
-    step(lds3, lds2, k + 3);
+  for (; k + NB - 1 <= last; k += NB) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) step(i, k + i);
   }
-  if (k <= last) {
-    step(lds0, lds3, k);
-    step(lds1, lds0, k + 1);
-  }
+#pragma unroll
+  for (int i = 0; i < NB - 1; ++i)
+    if (k + i <= last) step(i, k + i);
   arrive_but<0>();
 #endif
 }
@@ -144,21 +183,20 @@ __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8
 // A wave's results by rows, through its own part of LDS (32 rows of FN * 128 bytes): f(i, pass, row,
 // col, lo, hi) with eight neighbouring columns from `col` of row `row` of the wave's i-th 32 rows; a
 // lane's columns are the same in all passes.  after(i) follows each 32 rows.
-template <class P, int FM, int FN, class F, class G>
-__device__ __forceinline__ void by_rows(const typename P::Acc (&acc)[FM][FN], uint8_t *own, F &&f,
-                                        G &&after) {
+template <class P, class S, class F, class G>
+__device__ __forceinline__ void by_rows(const typename P::Four (&acc)[S::FM * 2][S::FN * 2], uint8_t *own,
+                                        F &&f, G &&after) {
   typedef typename P::Four Four;
-  constexpr int kRow = FN * 128, kChunks = FN * 8;
-  const int lane = threadIdx.x & 63, r32 = lane & 31, half = lane >> 5;
+  constexpr int FM = S::FM, FN = S::FN, kRow = FN * 128, kChunks = FN * 8;
+  const int lane = threadIdx.x & 63, r16 = lane & 15;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int chunk = (j * 8 + 2 * q + half) ^ (r32 & (kChunks - 1));
-        *reinterpret_cast<Four *>(own + r32 * kRow + chunk * 16) =
-            Four{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      for (int n = 0; n < FN * 2; ++n) {
+        const int row = m * 16 + r16, chunk = (n * 4 + (lane >> 4)) ^ (row & (kChunks - 1));
+        *reinterpret_cast<Four *>(own + row * kRow + chunk * 16) = acc[i * 2 + m][n];
       }
     wave_exchange();
 #pragma unroll
