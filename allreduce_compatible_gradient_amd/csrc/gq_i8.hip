@@ -259,7 +259,7 @@ __global__ __launch_bounds__(256) void k_i8_both(const I8QuantArgs a, int pitch,
 // ---------------------------------------------------------------- products
 // out = (sum a b) sa sb (+ bias) (+ out): the sum is exact, the rest in fp32, rounded once more to
 // bf16.
-__device__ __forceinline__ float scaled(int sum, float sa, float sb) { return ((float)sum * sa) * sb; }
+__device__ __forceinline__ float scaled(int sum, float sa, float sb) { return (float)sum * sa * sb; }
 
 __device__ __forceinline__ void put_one(const I8MatmulArgs &a, int64_t m, int64_t n, int sum) {
   float v = scaled(sum, a.a_scales[m], a.b_scales[n]);
@@ -297,76 +297,89 @@ __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pi
   auto nothing = [](int) {};
   if (gridDim.y > 1) {
     int32_t *part = a.partial + (int64_t)blockIdx.y * a.M * a.N;
-    by_rows<I8Product, S>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
+    by_rows<I8Product, S>(acc, own, [](int, i32x4 v) { return __builtin_bit_cast(f32x4, v); }, nothing,
+                          [&](int i, int, int row, int, f32x4 lo, f32x4 hi) {
       const int64_t m = wm0 + i * 32 + row;
       if (m >= a.M || n >= a.N) return;
       int32_t *o = part + m * a.N + n;
+      const i32x4 u = __builtin_bit_cast(i32x4, lo), v = __builtin_bit_cast(i32x4, hi);
       if (n + 8 <= a.N) {
-        reinterpret_cast<i32x4_e4 *>(o)[0] = lo;
-        reinterpret_cast<i32x4_e4 *>(o)[1] = hi;
+        reinterpret_cast<i32x4_e4 *>(o)[0] = u;
+        reinterpret_cast<i32x4_e4 *>(o)[1] = v;
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (n + e < a.N) o[e] = e < 4 ? lo[e & 3] : hi[e & 3];
+          if (n + e < a.N) o[e] = e < 4 ? u[e & 3] : v[e & 3];
       }
     }, nothing);
     return;
   }
-  float sb[8], bias[8];
+  // scales of the rows that a lane has before the exchange, scales and biases of the columns that it
+  // has after it; no bias is -0, which changes nothing that it is added to
+  float sa[FM * 2], sb[8], bias[8];
+#pragma unroll
+  for (int k = 0; k < FM * 2; ++k) sa[k] = a.a_scales[min(wm0 + k * 16 + (lane & 15), a.M - 1)];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int64_t c = min(n + e, a.N - 1);
     sb[e] = a.b_scales[c];
-    bias[e] = a.bias ? a.bias[c] : 0.0f;
+    bias[e] = a.bias ? a.bias[c] : -0.0f;
   }
-  const bool add = a.bias != nullptr;  // without a bias -0 stays -0
-  const bool lines = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.ldo * 2) & 127) == 0;
-  by_rows<I8Product, S>(acc, own, [&](int i, int, int row, int, i32x4 lo, i32x4 hi) {
+  auto by_token = [&](int k, i32x4 v) { return f32x4{(float)v[0] * sa[k], (float)v[1] * sa[k], (float)v[2] * sa[k], (float)v[3] * sa[k]}; };
+  auto finished = [&](f32x4 lo, f32x4 hi, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (e < 4 ? lo[e & 3] : hi[e & 3]) * sb[e] + bias[e];
+  };
+  if (!a.accumulate && n0 + S::BN <= a.N) {
+    // Nothing to add to and no row cut short: no questions at the stores but the last rows'.  Rows on
+    // 128-byte lines are stored non-temporally, as every store covers whole lines.
+    auto leave = [&](auto half_width, auto on_lines) {
+      constexpr int kElem = decltype(half_width)::value ? 2 : 4;
+      char *const out = static_cast<char *>(a.out) + (wm0 * a.ldo + n) * kElem;
+      const int64_t row_bytes = a.ldo * kElem;
+      const int rows = (int)min((int64_t)FM * 32, a.M - wm0);
+      by_rows<I8Product, S>(acc, own, by_token, nothing, [&](int i, int, int row, int, f32x4 lo, f32x4 hi) {
+        float v[8];
+        finished(lo, hi, v);
+        if (i * 32 + row >= rows) return;
+        char *o = out + (i * 32 + row) * row_bytes;
+        if constexpr (kElem == 2) {
+          const u32x4 w = {to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3]), to_bf16_pair(v[4], v[5]), to_bf16_pair(v[6], v[7])};
+          if constexpr (decltype(on_lines)::value)
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(o));
+          else
+            *reinterpret_cast<u32x4_e2 *>(o) = w;
+        } else {
+          f32x4_e4 *to = reinterpret_cast<f32x4_e4 *>(o);
+          to[0] = f32x4{v[0], v[1], v[2], v[3]};
+          to[1] = f32x4{v[4], v[5], v[6], v[7]};
+        }
+      }, nothing);
+    };
+    if (a.out_dtype == 0)
+      leave(std::false_type{}, std::false_type{});
+    else if (((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.ldo * 2) & 127) == 0)
+      leave(std::true_type{}, std::true_type{});
+    else
+      leave(std::true_type{}, std::false_type{});
+    return;
+  }
+  by_rows<I8Product, S>(acc, own, by_token, nothing, [&](int i, int, int row, int, f32x4 lo, f32x4 hi) {
     const int64_t m = wm0 + i * 32 + row;
     if (m >= a.M || n >= a.N) return;
-    const float sa = a.a_scales[m];
     float v[8];
+    finished(lo, hi, v);
+    const int64_t at = m * a.ldo + n;
+    const int there = (int)min((int64_t)8, a.N - n);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v[e] = scaled(e < 4 ? lo[e & 3] : hi[e & 3], sa, sb[e]);
-      if (add) v[e] += bias[e];
-    }
-    const int64_t at = m * a.ldo + n;
-    const bool whole = n + 8 <= a.N;
-    if (a.out_dtype == 0) {
-      float *o = static_cast<float *>(a.out) + at;
-      if (whole) {
-        f32x4 p = {v[0], v[1], v[2], v[3]}, q = {v[4], v[5], v[6], v[7]};
-        f32x4_e4 *to = reinterpret_cast<f32x4_e4 *>(o);
-        if (a.accumulate) {
-          p += to[0];
-          q += to[1];
-        }
-        to[0] = p;
-        to[1] = q;
+      if (e >= there) break;
+      if (a.out_dtype == 0) {
+        float *o = static_cast<float *>(a.out) + at + e;
+        *o = a.accumulate ? *o + v[e] : v[e];
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < a.N) o[e] = a.accumulate ? o[e] + v[e] : v[e];
-      }
-    } else {
-      uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-      if (whole) {
-        if (a.accumulate) {
-          float x[8];
-          load_eight<1>(o, 0, x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += x[e];
-        }
-        const u32x4 w = {to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3]), to_bf16_pair(v[4], v[5]), to_bf16_pair(v[6], v[7])};
-        if (lines)
-          __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(o));
-        else
-          *reinterpret_cast<u32x4_e2 *>(o) = w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < a.N) o[e] = to_bf16(a.accumulate ? __uint_as_float((uint32_t)o[e] << 16) + v[e] : v[e]);
+        uint16_t *o = static_cast<uint16_t *>(a.out) + at + e;
+        *o = to_bf16(a.accumulate ? __uint_as_float((uint32_t)*o << 16) + v[e] : v[e]);
       }
     }
   }, nothing);
@@ -496,16 +509,16 @@ struct Plan {
 Plan plan(int64_t M, int64_t N, int64_t K) {
   struct Tile {
     int bm, bn;
-    float step, rest, wait;  // us of a step of 128 bytes, of the rest of a tile, and once a step
+    float step, rest, wait, once;  // us of a step, of the rest of a tile, and once a step and a call
   };
-  constexpr Tile kTiles[3] = {{256, 256, 1.4f, 3.5f, 0.0f}, {128, 128, 0.45f, 1.7f, 0.4f}, {64, 128, 0.4f, 2.2f, 0.4f}};
+  constexpr Tile kTiles[3] = {{256, 256, 1.28f, 11.2f, 0.0f, 0.0f}, {128, 128, 0.46f, 3.3f, 0.11f, 4.0f}, {64, 128, 0.27f, 1.3f, 0.16f, 4.7f}};
   Plan p = {};
   const int64_t steps = i8_pitch(K) / 128;
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   float least = INFINITY;
   for (const Tile &t : kTiles) {
     const float each = (float)((tiles(t.bm, t.bn) + kCus - 1) / kCus);
-    const float us = each * ((float)steps * t.step + t.rest) + (float)steps * t.wait;
+    const float us = each * ((float)steps * t.step + t.rest) + (float)steps * t.wait + t.once;
     if (us < least) {
       least = us;
       p.bm = t.bm;

@@ -182,9 +182,10 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
   tile_product<F16Product, S>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
                                            min(steps_each, pitch / kStepBytes - step0), acc);
   const int wi = wave / WN * FM * 32, wj = wave % WN * FN * 32;
+  auto as_is = [](int, f32x4 v) { return v; };
   if (!SQUARE && gridDim.y > 1) {
     float *part = w.partial + (((int64_t)k * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * (S::BM * S::BN);
-    by_rows<F16Product, S>(acc, own, [&](int i, int, int row, int col, f32x4 lo, f32x4 hi) {
+    by_rows<F16Product, S>(acc, own, as_is, [](int) {}, [&](int i, int, int row, int col, f32x4 lo, f32x4 hi) {
       f32x4 *o = reinterpret_cast<f32x4 *>(part + (wi + i * 32 + row) * S::BN + wj + col);
       o[0] = lo;
       o[1] = hi;
@@ -202,16 +203,22 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
     for (int e = 0; e < 8; ++e) dj[e] = j + e < w.n ? da[j + e] : 0.0f;
   }
   u32x4 keep[FN * 2];
-  by_rows<F16Product, S>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
+  f16x8 olds[2][FN * 2];
+  float dis[2][FN * 2];
+  by_rows<F16Product, S>(acc, own, as_is, [&](int i32) {
+    if (!SQUARE) return;
+#pragma unroll
+    for (int p = 0; p < FN * 2; ++p) {
+      const int i = min(i0 + wi + i32 * 32 + p * (16 / FN) + lane / (FN * 4), w.n - 1);
+      dis[i32 & 1][p] = da[i];
+      olds[i32 & 1][p] = *reinterpret_cast<const f16x8 *>(f + (int64_t)i * w.np + min(j, w.np - 8));
+    }
+  }, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
     const int i = i0 + wi + i32 * 32 + row;
     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     const bool there = i < w.n && j < w.np;
-    float di = 0.0f;
-    f16x8 old = {};
-    if (SQUARE && there) {
-      di = da[i];
-      old = *reinterpret_cast<const f16x8 *>(f + (int64_t)i * w.np + j);
-    }
+    const float di = SQUARE ? dis[i32 & 1][p] : 0.0f;
+    const f16x8 old = SQUARE ? olds[i32 & 1][p] : f16x8{};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const bool on = i == j + e, in = i < w.n && j + e < w.n;
@@ -313,14 +320,25 @@ __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const Ortho
   const bool flip = o.rows > o.cols;
   const int j = j0 + wj + lane % (FN * 4) * 8;
   u32x4 keep[FN * 2];
-  by_rows<F16Product, S>(acc, own, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
+  f32x4 xs[2][FN * 2][2];
+  float ds[2][FN * 2];
+  by_rows<F16Product, S>(acc, own, [](int, f32x4 v) { return v; }, [&](int i32) {
+#pragma unroll
+    for (int p = 0; p < FN * 2; ++p) {
+      const int i = min(i0 + wi + i32 * 32 + p * (16 / FN) + lane / (FN * 4), w.n - 1);
+      const f32x4 *at = reinterpret_cast<const f32x4 *>(x + (int64_t)i * w.mp + min(j, w.mp - 8));
+      xs[i32 & 1][p][0] = at[0];
+      xs[i32 & 1][p][1] = at[1];
+      ds[i32 & 1][p] = diag[i];
+    }
+  }, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
     const int i = i0 + wi + i32 * 32 + row;
     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, h[8] = {};
     const bool there = i < w.n && j < w.mp;
     if (there) {
       float *at = x + (int64_t)i * w.mp + j;
-      const f32x4 x0 = *reinterpret_cast<const f32x4 *>(at), x1 = *reinterpret_cast<const f32x4 *>(at + 4);
-      const float s = ca + diag[i];
+      const f32x4 x0 = xs[i32 & 1][p][0], x1 = xs[i32 & 1][p][1];
+      const float s = ca + ds[i32 & 1][p];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[e] = s * (e < 4 ? x0[e & 3] : x1[e & 3]) + v[e] * (1.0f / (kScaleX * kScaleB));

@@ -180,15 +180,18 @@ __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8
 #endif
 }
 
-// A wave's results by rows, through its own part of LDS (32 rows of FN * 128 bytes): f(i, pass, row,
-// col, lo, hi) with eight neighbouring columns from `col` of row `row` of the wave's i-th 32 rows; a
-// lane's columns are the same in all passes.  after(i) follows each 32 rows.
-template <class P, class S, class F, class G>
+// A wave's results by rows, 32 of them at a time, through its own part of LDS (rows of FN * 128
+// bytes).  For the wave's i-th 32 rows: pre(k, four) makes four neighbouring results of row
+// 16 k + (lane mod 16) of the wave's what is exchanged, f(i, pass, row, col, lo, hi) has eight
+// neighbouring columns from `col` of row `row`, a lane's columns being the same in all passes, and
+// after(i) follows.  before(i) is called one turn ahead, so that what it loads arrives meanwhile: a
+// load in f itself would cost its latency in every pass.
+template <class P, class S, class H, class B, class F, class G>
 __device__ __forceinline__ void by_rows(const typename P::Four (&acc)[S::FM * 2][S::FN * 2], uint8_t *own,
-                                        F &&f, G &&after) {
-  typedef typename P::Four Four;
+                                        H &&pre, B &&before, F &&f, G &&after) {
   constexpr int FM = S::FM, FN = S::FN, kRow = FN * 128, kChunks = FN * 8;
   const int lane = threadIdx.x & 63, r16 = lane & 15;
+  before(0);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -196,14 +199,15 @@ __device__ __forceinline__ void by_rows(const typename P::Four (&acc)[S::FM * 2]
 #pragma unroll
       for (int n = 0; n < FN * 2; ++n) {
         const int row = m * 16 + r16, chunk = (n * 4 + (lane >> 4)) ^ (row & (kChunks - 1));
-        *reinterpret_cast<Four *>(own + row * kRow + chunk * 16) = acc[i * 2 + m][n];
+        *reinterpret_cast<f32x4 *>(own + row * kRow + chunk * 16) = pre(i * 2 + m, acc[i * 2 + m][n]);
       }
     wave_exchange();
+    if (i + 1 < FM) before(i + 1);
 #pragma unroll
     for (int p = 0; p < FN * 2; ++p) {
       const int row = p * (16 / FN) + lane / (FN * 4), c = lane % (FN * 4) * 2;
-      const Four lo = *reinterpret_cast<const Four *>(own + row * kRow + ((c ^ (row & (kChunks - 1))) * 16));
-      const Four hi = *reinterpret_cast<const Four *>(own + row * kRow + (((c + 1) ^ (row & (kChunks - 1))) * 16));
+      const f32x4 lo = *reinterpret_cast<const f32x4 *>(own + row * kRow + ((c ^ (row & (kChunks - 1))) * 16));
+      const f32x4 hi = *reinterpret_cast<const f32x4 *>(own + row * kRow + (((c + 1) ^ (row & (kChunks - 1))) * 16));
       f(i, p, row, c * 4, lo, hi);
     }
     wave_exchange();
