@@ -18,8 +18,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_e2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_e4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_e4 __attribute__((aligned(4)));
 
 #define LDS_PTR __attribute__((address_space(3)))
+#define GLOBAL_PTR __attribute__((address_space(1)))
 
 // Between writes of a wave's lanes to its own part of LDS and other lanes' reads of them, and back.
 // The hardware executes a wave's LDS accesses in order; the fences keep the compiler from moving
@@ -99,6 +101,54 @@ __device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
   return top;
+}
+
+// E neighbouring elements (4 or 8) as they lie in memory.  Loads that should be on their way together
+// are made by raw_word, which has no branch: a row's end moves the place, within the row as long as it
+// has E elements at all, else to a place of its own (after a load that may or may not have been made,
+// the wait for an earlier one is a wait for all).  open_word reads a row's last few elements one by
+// one.
+template <int DT, int E>
+struct Raw {
+  u32x4 a, b;
+};
+
+[[maybe_unused]] __device__ const uint32_t kElsewhere[8] = {};
+
+template <int DT, int E>
+__device__ __forceinline__ Raw<DT, E> raw_word(const void *p, int64_t row_at, int64_t first, int64_t cols) {
+  Raw<DT, E> r = {};
+  uint64_t at = reinterpret_cast<uint64_t>(p) + (uint64_t)(row_at + min(first, cols - E)) * (DT == 0 ? 4 : 2);
+  at = cols >= E ? at : reinterpret_cast<uint64_t>(kElsewhere);
+  if constexpr (DT == 0) {
+    const GLOBAL_PTR u32x4_e4 *q = reinterpret_cast<const GLOBAL_PTR u32x4_e4 *>(at);
+    r.a = q[0];
+    if constexpr (E == 8) r.b = q[1];
+  } else if constexpr (E == 8) {
+    r.a = *reinterpret_cast<const GLOBAL_PTR u32x4_e2 *>(at);
+  } else {
+    const u32x2 v = *reinterpret_cast<const GLOBAL_PTR u32x2_e2 *>(at);
+    r.a.x = v.x;
+    r.a.y = v.y;
+  }
+  return r;
+}
+
+// The elements of raw_word(p, row_at, first, cols), zeros past the row's end.
+template <int DT, int E>
+__device__ __forceinline__ void open_word(const Raw<DT, E> &r, const void *p, int64_t row_at, int64_t first,
+                                          int64_t cols, float (&x)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if constexpr (DT == 0)
+      x[i] = __uint_as_float(i < 4 ? r.a[i & 3] : r.b[i & 3]);
+    else
+      x[i] = __uint_as_float(i & 1 ? r.a[i >> 1] & 0xFFFF0000u : r.a[i >> 1] << 16);
+  }
+  if (first + E > cols) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = first + i < cols ? load_one<DT>(p, row_at + first + i) : 0.0f;
+  }
 }
 
 }  // namespace

@@ -2,6 +2,8 @@
 // gradient, dtable_v = scale * sum over the tokens t with id_t = v of dout_t.
 //
 // An id outside [0, vocab) stands for no token: its row is zeros, and it adds to no gradient.
+#include <type_traits>
+
 #include "gq_device.h"
 #include "gq_layers.h"
 
@@ -39,29 +41,29 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
   if (col >= a.dim) return;
   const int64_t stride = (int64_t)gridDim.y * blockDim.y * kLookAhead;
   for (int64_t t0 = ((int64_t)blockIdx.y * blockDim.y + threadIdx.y) * kLookAhead; t0 < a.tokens; t0 += stride) {
-    float x[kLookAhead][8];
+    int64_t id[kLookAhead];
+    Raw<DT, 8> raw[kLookAhead];
 #pragma unroll
-    for (int i = 0; i < kLookAhead; ++i) {
-      const int64_t id = t0 + i < a.tokens ? a.ids[t0 + i] : -1;
-      if (id >= 0 && id < a.vocab) {
-        load_word<DT>(a.table, id * a.ld_table, col, a.dim, x[i]);
-      } else {
+    for (int i = 0; i < kLookAhead; ++i) id[i] = a.ids[min(t0 + i, a.tokens - 1)];
+    if (a.vocab > 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
-      }
+      for (int i = 0; i < kLookAhead; ++i)  // no token: row 0, not kept
+        raw[i] = raw_word<DT, 8>(a.table, ((uint64_t)id[i] < (uint64_t)a.vocab ? id[i] : 0) * a.ld_table, col, a.dim);
     }
 #pragma unroll
     for (int i = 0; i < kLookAhead; ++i) {
       if (t0 + i >= a.tokens) break;
+      float x[8] = {};
+      if ((uint64_t)id[i] < (uint64_t)a.vocab) open_word(raw[i], a.table, id[i] * a.ld_table, col, a.dim, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] *= a.scale;
+      for (int e = 0; e < 8; ++e) x[e] *= a.scale;
       const int64_t at = (t0 + i) * a.ld_out + col;
       if (col + 8 <= a.dim) {
-        store_eight<OT>(a.out, at, x[i]);
+        store_eight<OT>(a.out, at, x);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (col + e < a.dim) store_one<OT>(a.out, at + e, x[i][e]);
+          if (col + e < a.dim) store_one<OT>(a.out, at + e, x[e]);
       }
     }
   }
@@ -75,10 +77,9 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
 // counters of its own, so places follow the tokens' order without any atomic's.
 constexpr int kSortWaves = 16;
 constexpr int kMaxRange = 896;  // counters of 56 KB
-constexpr int kHeld = 16;       // tokens a lane
 
-// HELD: at most 16384 tokens, which stay in registers between the two.
-template <bool HELD>
+// HELD > 0: at most 1024 HELD tokens, which stay in registers between the two.
+template <int HELD>
 __global__ __launch_bounds__(kSortWaves * 64) void k_embed_sort(const int64_t *ids, int64_t tokens,
                                                                 int64_t vocab, int range, int bits,
                                                                 int32_t *start, int32_t *order,
@@ -91,13 +92,16 @@ __global__ __launch_bounds__(kSortWaves * 64) void k_embed_sort(const int64_t *i
   const int64_t first = wave * run, end = min(first + run, tokens);
   uint32_t *mine = counts + wave * range;
   // a token's id from the range's first on; what has no id is beyond every range
-  auto load = [&](int64_t t) { return t < end ? ids[t] : -1; };
+  auto load = [&](int64_t t) {
+    const int64_t id = ids[max(min(t, tokens - 1), (int64_t)0)];  // (of no tokens: any place that there is)
+    return t < end ? id : -1;
+  };
   auto place_of = [&](int64_t id) { return (uint64_t)id < (uint64_t)vocab ? (int)id - (int)lo : 1 << 30; };
   const uint32_t here = (uint32_t)(hi - lo);
-  constexpr int U = HELD ? kHeld : 4;
+  constexpr int U = HELD > 0 ? HELD : 4;
   int64_t id[U];
   int held[U];
-  if (HELD) {
+  if (HELD > 0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) id[u] = load(first + lane + u * 64);
   }
@@ -105,7 +109,7 @@ __global__ __launch_bounds__(kSortWaves * 64) void k_embed_sort(const int64_t *i
   __syncthreads();
   uint32_t below = 0;
   for (int64_t t = first + lane; t - lane < end; t += 64 * U) {
-    if (!HELD) {
+    if (HELD == 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) id[u] = load(t + u * 64);
     }
@@ -146,7 +150,7 @@ __global__ __launch_bounds__(kSortWaves * 64) void k_embed_sort(const int64_t *i
   }
   __syncthreads();
   for (int64_t t = first + lane; t - lane < end; t += 64 * U) {
-    if (!HELD) {
+    if (HELD == 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) id[u] = load(t + u * 64);
 #pragma unroll
@@ -179,14 +183,67 @@ __global__ __launch_bounds__(kSortWaves * 64) void k_embed_sort(const int64_t *i
 }
 
 // ---------------------------------------------------------------- gradient
-// Tokens are added in their order; ids of more than kPiece tokens in pieces: those at sorted places
-// [p kPiece, (p + 1) kPiece) are added apart.  An id of more than kPiece tokens that has any of a
-// piece has its first or its last, so a piece has at most two sums: of the id that its first token
-// has, and of the one that its last has.
+// Three sorts of rows.  Of at most kFew tokens, most of all: one after another with the zeros
+// (k_embed_rows).  Of at most kPiece tokens: added in their order by a wave, beside the first sort, as
+// a frequent id's neighbours are often frequent too and would wait for each other there.  Of more: in
+// pieces, the tokens at sorted places [p kPiece, (p + 1) kPiece), which are added apart and then
+// joined.  Such an id, if it has any token of a piece, has its first or its last, so a piece has at most two
+// sums: of the id that its first token has, and of the one that its last has.
 constexpr int kPiece = 64;
+constexpr int kFew = 4;
 
-// One piece and 512 columns a block: its waves a quarter of the tokens each, a lane eight columns.
-template <int DT>
+// E elements of a row of the gradient: what was added up times the scale (plus the old values).
+template <int OT, int E>
+__device__ __forceinline__ void leave(const EmbedGradArgs &a, int64_t v, int64_t col, float (&acc)[E], bool lines) {
+  const int64_t to = v * a.ld_out + col;
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] *= a.scale;
+  if (a.accumulate) {
+    float old[E];
+    open_word(raw_word<OT, E>(a.out, v * a.ld_out, col, a.dim), a.out, v * a.ld_out, col, a.dim, old);
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] += old[i];
+  }
+  if (col + E > a.dim) {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (col + i < a.dim) store_one<OT>(a.out, to + i, acc[i]);
+    return;
+  }
+  if constexpr (E == 8) {
+    store_eight<OT>(a.out, to, acc);
+  } else {
+    const u32x4 w = {__float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]), __float_as_uint(acc[3])};
+    float *o = static_cast<float *>(a.out) + to;
+    if (lines)
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(o));
+    else
+      *reinterpret_cast<u32x4_e4 *>(o) = w;
+  }
+}
+
+// Adds U tokens at most, which `of` names, to E columns a lane.
+template <int DT, int E, int U, class F>
+__device__ __forceinline__ void add_some(const EmbedGradArgs &a, int count, int64_t col, F &&of, float (&acc)[E]) {
+  int64_t row[U];
+  Raw<DT, E> raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) row[u] = (int64_t)of(min(u, count - 1)) * a.ld_dout;
+#pragma unroll
+  for (int u = 0; u < U; ++u) raw[u] = raw_word<DT, E>(a.dout, row[u], col, a.dim);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u >= count) break;
+    float x[E];
+    open_word(raw[u], a.dout, row[u], col, a.dim, x);
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] += x[i];
+  }
+}
+
+// One piece and 512 columns a block, a lane eight: the rows of the second sort whose tokens begin in
+// it, a wave one, then its sums of the third, a wave a quarter of the tokens.
+template <int DT, int OT>
 __device__ __forceinline__ void add_piece(const EmbedGradArgs &a, const int32_t *start, const int32_t *order,
                                           const int32_t *sorted, float *sums, int piece, int64_t c0) {
   __shared__ float part[4][64][9];
@@ -195,25 +252,33 @@ __device__ __forceinline__ void add_piece(const EmbedGradArgs &a, const int32_t 
   const int p0 = piece * kPiece, all = start[a.vocab];
   if (p0 >= all) return;
   const int p1 = min(p0 + kPiece, all);
-  const int ids[2] = {sorted[p0], sorted[p1 - 1]};
-  for (int slot = 0; slot < (ids[0] == ids[1] ? 1 : 2); ++slot) {
-    const int s = start[ids[slot]], e = start[ids[slot] + 1];
-    if (e - s <= kPiece) continue;  // (the same for the whole block)
-    constexpr int kEach = kPiece / 4;
-    const int from = max(s, p0) + wave * kEach, to = min(min(e, p1), from + kEach);
+  // of this piece's tokens, a lane one: the token, its id, where the id's tokens begin and end
+  const int here = min(p0 + lane, all - 1), id = sorted[here];
+  const int tokens[2] = {order[here], order[min(p0 + 64 + lane, all - 1)]};
+  const int s = start[id], e = start[id + 1];
+  auto token = [&](int place) {  // within this piece and the next
+    const int k = place - p0;
+    return k < 64 ? __builtin_amdgcn_readlane(tokens[0], k) : __builtin_amdgcn_readlane(tokens[1], k - 64);
+  };
+  uint64_t some = __ballot(s == p0 + lane && p0 + lane < all && e - s > kFew && e - s <= kPiece);
+  for (int k = 0; some; some &= some - 1, ++k) {
+    if ((k & 3) != wave) continue;
+    const int l = __builtin_ctzll(some);
+    const int from = __builtin_amdgcn_readlane(s, l), to = __builtin_amdgcn_readlane(e, l);
     float acc[8] = {};
-    if (col < a.dim) {
-      for (int k = from; k < to; k += 8) {
-        float x[8][8] = {};
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (k + u < to) load_word<DT>(a.dout, (int64_t)order[k + u] * a.ld_dout, col, a.dim, x[u]);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] += x[u][i];
-      }
-    }
+    for (int at = from; at < to; at += 16)
+      add_some<DT, 8, 16>(a, to - at, col, [&](int u) { return token(at + u); }, acc);
+    if (col < a.dim) leave<OT, 8>(a, __builtin_amdgcn_readlane(id, l), col, acc, false);
+  }
+  for (int slot = 0; slot < 2; ++slot) {
+    const int l = slot == 0 ? 0 : p1 - 1 - p0;
+    const int s1 = __builtin_amdgcn_readlane(s, l), e1 = __builtin_amdgcn_readlane(e, l);
+    // (the same for the whole block)
+    if (e1 - s1 <= kPiece || (slot == 1 && __builtin_amdgcn_readlane(id, 0) == __builtin_amdgcn_readlane(id, l))) continue;
+    constexpr int kEach = kPiece / 4;
+    const int from = max(s1, p0) + wave * kEach, to = min(min(e1, p1), from + kEach);
+    float acc[8] = {};
+    if (from < to) add_some<DT, 8, kEach>(a, to - from, col, [&](int u) { return token(from + u); }, acc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[wave][lane][i] = acc[i];
     __syncthreads();
@@ -227,128 +292,58 @@ __device__ __forceinline__ void add_piece(const EmbedGradArgs &a, const int32_t 
   }
 }
 
-// E neighbouring elements from `col` of a row, zeros past its end.
-template <int DT, int E>
-__device__ __forceinline__ void load_some(const void *p, int64_t row_at, int64_t col, int64_t dim, float (&x)[E]) {
-  if constexpr (E == 8) {
-    load_word<DT>(p, row_at, col, dim, x);
-  } else if (col + 4 <= dim) {
-    if constexpr (DT == 0) {
-      const f32x4 w = *reinterpret_cast<const f32x4_e4 *>(static_cast<const float *>(p) + row_at + col);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = w[i];
-    } else {
-      const u32x2 w = *reinterpret_cast<const u32x2_e2 *>(static_cast<const uint16_t *>(p) + row_at + col);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = col + i < dim ? load_one<DT>(p, row_at + col + i) : 0.0f;
-  }
-}
-
-// E elements of a row of the gradient: what was added up times the scale (plus the old values).
-template <int OT, int E>
-__device__ __forceinline__ void leave(const EmbedGradArgs &a, int64_t v, int64_t col, float (&acc)[E], bool lines) {
-  const int64_t to = v * a.ld_out + col;
-#pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] *= a.scale;
-  if (a.accumulate) {
-    float old[E];
-    load_some<OT, E>(a.out, v * a.ld_out, col, a.dim, old);
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] += old[i];
-  }
-  if (col + E > a.dim) {
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (col + i < a.dim) store_one<OT>(a.out, to + i, acc[i]);
-    return;
-  }
-  u32x4 w;
-  if constexpr (OT == 0)
-    w = u32x4{__float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]), __float_as_uint(acc[3])};
-  else
-    w = u32x4{to_bf16_pair(acc[0], acc[1]), to_bf16_pair(acc[2], acc[3]), to_bf16_pair(acc[4], acc[5]), to_bf16_pair(acc[6], acc[7])};
-  char *o = static_cast<char *>(a.out) + to * (OT == 0 ? 4 : 2);
-  if (lines)
-    __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(o));
-  else
-    *reinterpret_cast<u32x4_e2 *>(o) = w;
-}
-
-// Adds the tokens of sorted places [s, e) to C groups of E columns a lane, U tokens on their way
-// together.
-template <int DT, int E, int C, int U>
-__device__ __forceinline__ void add_tokens(const EmbedGradArgs &a, const int32_t *order, int s, int e, int64_t c0,
-                                           float (&acc)[C][E]) {
-  for (int k = s; k < e; k += U) {
-    float x[U][C][E] = {};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k + u < e) {
-        const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(order[k + u]) * a.ld_dout;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          if (c0 + c * 64 * E < a.dim) load_some<DT, E>(a.dout, row, c0 + c * 64 * E, a.dim, x[u][c]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[c][i] += x[u][c][i];
-  }
-}
-
-// Rows of ids of at most kPiece tokens, and in the grid's first blocks the pieces of the others.  A
-// block has 16 rows and 1024 columns.  First a wave takes four rows, a lane 16 bytes of the output at
-// a time, so that the zeros of ids without tokens, most of the bytes, leave in whole lines and without
-// a question of any lane's own, and adds those of at most kFew tokens; then the block's waves
-// share each row of more, a part of the columns each, so that its tokens are few steps.
-constexpr int kFew = 8;
-
+// The pieces in the grid's first blocks, then the rows of at most kFew tokens, 16 a block.  The zeros of
+// ids without tokens, most of the bytes, leave first, by whole lines and without a question of any
+// lane's own, a wave four rows; then a wave takes a quarter of the columns of all rows of some tokens,
+// the first tokens of four rows on their way together, as one token is the rule.
 template <int DT, int OT>
 __global__ __launch_bounds__(256) void k_embed_rows(const EmbedGradArgs a, const int32_t *start,
                                                     const int32_t *order, const int32_t *sorted, float *sums,
-                                                    int pieces, int parts, bool lines) {
+                                                    int pieces, int parts, int wide, bool lines) {
   if ((int)blockIdx.x < pieces * parts) {
-    add_piece<DT>(a, start, order, sorted, sums, blockIdx.x / parts, (int64_t)(blockIdx.x % parts) * 512);
+    add_piece<DT, OT>(a, start, order, sorted, sums, blockIdx.x / parts, (int64_t)(blockIdx.x % parts) * 512);
     return;
   }
-  constexpr int E = OT == 0 ? 4 : 8, C = 1024 / (64 * E);
+  constexpr int E = OT == 0 ? 4 : 8;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wide = (int)((a.dim + 1023) / 1024), block = (int)blockIdx.x - pieces * parts;
-  const int64_t v0 = (int64_t)(block / wide) * 16, from = (int64_t)(block % wide) * 1024;
-  const int at = start[min(v0 + min(lane, 16), a.vocab)];
+  const int block = (int)blockIdx.x - pieces * parts;
+  const int64_t v0 = (int64_t)(block / wide) * 16, col = ((int64_t)(block % wide) * 256 + wave * 64 + lane) * E;
+  const int at = start[min(v0 + min(lane, 16), a.vocab)], count = __shfl_down(at, 1) - at;
+  const bool row = lane < 16 && v0 + lane < a.vocab;
+  if (!a.accumulate)  // a wave four rows, whole
+    for (uint64_t none = __ballot(row && count == 0) & 15ull << wave * 4; none; none &= none - 1) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int s = __builtin_amdgcn_readlane(at, wave * 4 + r), e = __builtin_amdgcn_readlane(at, wave * 4 + r + 1);
-    const int64_t v = v0 + wave * 4 + r, c0 = from + lane * E;
-    if (v >= a.vocab || e - s > kFew || (a.accumulate && s == e)) continue;
-    float acc[C][E] = {};
-    add_tokens<DT, E, C, 4>(a, order, s, e, c0, acc);
+      for (int c = 0; c < 4; ++c) {
+        float zero[E] = {};
+        const int64_t at_col = col + (c - wave) * 64 * E;
+        if (at_col < a.dim) leave<OT, E>(a, v0 + __builtin_ctzll(none), at_col, zero, lines);
+      }
+    }
+  if (col - lane * E >= a.dim) return;
+  uint64_t some = __ballot(row && count > 0 && count <= kFew);
+  while (some) {
+    int r[4];
+    int64_t from[4];
+    Raw<DT, E> raw[4];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (c0 + c * 64 * E < a.dim) leave<OT, E>(a, v, c0 + c * 64 * E, acc[c], lines);
-  }
-  const int next = __shfl_down(at, 1);
-  uint64_t more = __ballot(lane < 16 && next - at > kFew && next - at <= kPiece);
-  for (; more; more &= more - 1) {
-    const int r = __builtin_ctzll(more);
-    const int s = __builtin_amdgcn_readlane(at, r), e = __builtin_amdgcn_readlane(at, r + 1);
+    for (int q = 0; q < 4; ++q) {
+      r[q] = some ? __builtin_ctzll(some) : -1;
+      some &= some - 1;
+      from[q] = (int64_t)__builtin_amdgcn_readfirstlane(order[__builtin_amdgcn_readlane(at, r[q] < 0 ? r[0] : r[q])]) * a.ld_dout;
+    }
 #pragma unroll
-    for (int c = 0; c < C; c += 4) {
-      const int64_t c0 = from + (wave + c) * 64 * E + lane * E;
-      if (wave + c >= C || c0 >= a.dim) continue;
-      float acc[1][E] = {};
-      add_tokens<DT, E, 1, 16>(a, order, s, e, c0, acc);
-      leave<OT, E>(a, v0 + r, c0, acc[0], lines);
+    for (int q = 0; q < 4; ++q) raw[q] = raw_word<DT, E>(a.dout, from[q], col, a.dim);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (r[q] < 0) break;
+      const int s = __builtin_amdgcn_readlane(at, r[q]) + 1, e = __builtin_amdgcn_readlane(at, r[q] + 1);
+      float acc[E] = {}, x[E];
+      open_word(raw[q], a.dout, from[q], col, a.dim, x);
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] += x[i];
+      if (s < e)
+        add_some<DT, E, kFew - 1>(a, e - s, col, [&](int u) { return __builtin_amdgcn_readfirstlane(order[s + u]); }, acc);
+      if (col < a.dim) leave<OT, E>(a, v0 + r[q], col, acc, lines);
     }
   }
 }
@@ -373,16 +368,22 @@ __global__ __launch_bounds__(256) void k_embed_join(const EmbedGradArgs a, const
   float acc[E] = {};
   if (col < a.dim)
     for (int p = from; p < to; p += U) {
-      float x[U][E] = {};
+      int64_t row[U];
+      Raw<0, E> raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t slot = p + u == (int)blockIdx.x && s != p0;
-        if (p + u < to) load_some<0, E>(sums, ((int64_t)(p + u) * 2 + slot) * a.dim, col, a.dim, x[u]);
+        const int q = min(p + u, to - 1);
+        row[u] = ((int64_t)q * 2 + (q == (int)blockIdx.x && s != p0)) * a.dim;
+        raw[u] = raw_word<0, E>(sums, row[u], col, a.dim);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        if (p + u >= to) break;
+        float x[E];
+        open_word(raw[u], sums, row[u], col, a.dim, x);
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] += x[u][i];
+        for (int i = 0; i < E; ++i) acc[i] += x[i];
+      }
     }
 #pragma unroll
   for (int i = 0; i < E; ++i) part[wave][lane][i] = acc[i];
@@ -419,17 +420,26 @@ void gradient(const EmbedGradArgs &a, hipStream_t s) {
   while ((1 << bits) < range) ++bits;
   const unsigned ranges = (unsigned)((a.vocab + range - 1) / range);
   const size_t lds = (size_t)range * kSortWaves * 4;
-  if (a.tokens <= kSortWaves * 64 * kHeld)
-    k_embed_sort<true><<<ranges, kSortWaves * 64, lds, s>>>(a.ids, a.tokens, a.vocab, (int)range, bits, start, order, sorted);
+  auto sort = [&](auto held) {
+    const int64_t *ids = a.tokens > 0 ? a.ids : static_cast<const int64_t *>(a.scratch);
+    k_embed_sort<decltype(held)::value><<<ranges, kSortWaves * 64, lds, s>>>(ids, a.tokens, a.vocab, (int)range, bits,
+                                                                            start, order, sorted);
+  };
+  if (a.tokens <= kSortWaves * 64 * 2)
+    sort(std::integral_constant<int, 2>{});
+  else if (a.tokens <= kSortWaves * 64 * 8)
+    sort(std::integral_constant<int, 8>{});
+  else if (a.tokens <= kSortWaves * 64 * 16)
+    sort(std::integral_constant<int, 16>{});
   else
-    k_embed_sort<false><<<ranges, kSortWaves * 64, lds, s>>>(a.ids, a.tokens, a.vocab, (int)range, bits, start, order, sorted);
+    sort(std::integral_constant<int, 0>{});
   const bool lines = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.ld_out * (OT == 0 ? 4 : 2)) & 127) == 0;
-  const int pieces = a.tokens > kPiece ? (int)pieces_of(a.tokens) : 0, parts = (int)((a.dim + 511) / 512);
-  const int64_t rows = (a.vocab + 15) / 16 * ((a.dim + 1023) / 1024);
-  k_embed_rows<DT, OT><<<(unsigned)((int64_t)pieces * parts + rows), 256, 0, s>>>(a, start, order, sorted, sums, pieces,
-                                                                                 parts, lines);
+  const int pieces = (int)pieces_of(a.tokens), parts = (int)((a.dim + 511) / 512);
   constexpr int kWide = 64 * (OT == 0 ? 4 : 8);
-  if (pieces)
+  const int wide = (int)((a.dim + 4 * kWide - 1) / (4 * kWide));
+  const int64_t blocks = (int64_t)pieces * parts + (a.vocab + 15) / 16 * wide;
+  k_embed_rows<DT, OT><<<(unsigned)blocks, 256, 0, s>>>(a, start, order, sorted, sums, pieces, parts, wide, lines);
+  if (pieces > 1)
     k_embed_join<OT><<<dim3((unsigned)pieces, (unsigned)((a.dim + kWide - 1) / kWide)), 256, 0, s>>>(a, start, sorted, sums, lines);
 }
 

@@ -17,6 +17,8 @@
 namespace gq {
 namespace {
 
+constexpr int kCus = 256;
+
 // ---------------------------------------------------------------- quantisation
 struct RowScale {
   float scale, inv;  // inv 0: all codes are zero
@@ -77,16 +79,11 @@ __global__ __launch_bounds__(256) void k_i8_rows(const I8QuantArgs a, int pitch)
   float x[C > 0 ? C : 1][8];
   uint32_t top = 0;
   if constexpr (C > 0) {
+    Raw<DT, 8> raw[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int g = lane + c * kThreads;
-      if (g * 8 < a.cols) {
-        load_word<DT>(a.x, at, (int64_t)g * 8, a.cols, x[c]);
-      } else {
+    for (int c = 0; c < C; ++c) raw[c] = raw_word<DT, 8>(a.x, at, (int64_t)(lane + c * kThreads) * 8, a.cols);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[c][i] = 0.0f;
-      }
-    }
+    for (int c = 0; c < C; ++c) open_word(raw[c], a.x, at, (int64_t)(lane + c * kThreads) * 8, a.cols, x[c]);
 #pragma unroll
     for (int c = 0; c < C; ++c) top = max(top, top_of(x[c]));
   } else {
@@ -131,87 +128,114 @@ __global__ __launch_bounds__(256) void k_i8_rows(const I8QuantArgs a, int pitch)
   }
 }
 
-__global__ __launch_bounds__(256) void k_i8_clear(uint32_t *p, int64_t count) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t < count) p[t] = 0;
-}
-
-// Largest magnitudes of rows (ROWS) and columns, as bits: their maximum does not hang on the order in
-// which blocks arrive.  A block takes 64 rows x 512 columns, a wave 16 rows, a lane eight columns.
+// Largest magnitudes of rows (ROWS) and columns, as bits, over a part of the matrix each: a block goes
+// through 64 rows at a time of its share, 512 columns, a wave 16 rows, a lane eight columns.
 template <int DT, bool ROWS>
-__global__ __launch_bounds__(256) void k_i8_tops(const I8QuantArgs a) {
+__global__ __launch_bounds__(256) void k_i8_tops(const I8QuantArgs a, int rows_each) {
   __shared__ uint32_t cols_top[4][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c0 = (int64_t)blockIdx.x * 512 + lane * 8, r0 = (int64_t)blockIdx.y * 64 + wave * 16;
+  const int64_t c0 = (int64_t)blockIdx.x * 512 + lane * 8;
+  const int64_t first = (int64_t)blockIdx.y * rows_each, end = min(first + rows_each, a.rows);
   uint32_t top[8] = {};
-#pragma unroll 4
-  for (int r = 0; r < 16; ++r) {
-    if (r0 + r >= a.rows) break;
-    float x[8];
-    if (c0 < a.cols) {
-      load_word<DT>(a.x, (r0 + r) * a.ld, c0, a.cols, x);
-    } else {
+  for (int64_t r0 = first + wave * 16; r0 < end; r0 += 64) {
+    uint32_t row_top[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    for (int q = 0; q < 16; q += 8) {  // rows past the end: the last one again
+      Raw<DT, 8> raw[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) raw[u] = raw_word<DT, 8>(a.x, min(r0 + q + u, end - 1) * a.ld, c0, a.cols);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        float x[8];
+        open_word(raw[u], a.x, min(r0 + q + u, end - 1) * a.ld, c0, a.cols, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = max(top[i], __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        row_top[q + u] = top_of(x);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top[i] = max(top[i], __float_as_uint(x[i]) & 0x7FFFFFFFu);
     if constexpr (ROWS) {
-      const uint32_t m = wave_max(top_of(x));
-      if (lane == 0) atomicMax(a.tops + r0 + r, m);
+      // sixteen rows' maxima over 64 lanes: at each exchange a lane keeps half of the rows
+#pragma unroll
+      for (int half = 8; half > 0; half >>= 1) {
+        const bool upper = lane & half;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+          const uint32_t give = upper ? row_top[i] : row_top[i + half], keep = upper ? row_top[i + half] : row_top[i];
+          row_top[i] = max(keep, (uint32_t)__shfl_xor((int)give, half));
+        }
+      }
+      row_top[0] = max(row_top[0], (uint32_t)__shfl_xor((int)row_top[0], 16));
+      row_top[0] = max(row_top[0], (uint32_t)__shfl_xor((int)row_top[0], 32));
+      if (lane < 16 && r0 + lane < end) a.tops[(int64_t)blockIdx.x * a.rows + r0 + lane] = row_top[0];
     }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) cols_top[wave][lane * 8 + i] = top[i];
   __syncthreads();
+  uint32_t *out = a.tops + (ROWS ? gridDim.x * a.rows : 0) + (int64_t)blockIdx.y * a.cols;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int c = threadIdx.x + i * 256;
     const int64_t col = (int64_t)blockIdx.x * 512 + c;
-    if (col < a.cols)
-      atomicMax(a.tops + a.rows + col, max(max(cols_top[0][c], cols_top[1][c]), max(cols_top[2][c], cols_top[3][c])));
+    if (col < a.cols) out[col] = max(max(cols_top[0][c], cols_top[1][c]), max(cols_top[2][c], cols_top[3][c]));
   }
 }
 
-// By columns, or both ways (ROWS), from the largest magnitudes.  A block takes 128 rows x 128 columns;
-// a lane has eight columns of a row, whose codes by rows leave as they are and whose codes by columns
-// cross LDS.  The draw of an element is shared by its two codes.
+// By columns, or both ways (ROWS), from the parts' largest magnitudes (row_parts of rows, then
+// col_parts of columns).  A block takes 128 rows x 128 columns; a lane has eight columns of a row,
+// whose codes by rows leave as they are and whose codes by columns cross LDS.  The draw of an element
+// is shared by its two codes.
 template <int DT, bool STOCH, bool ROWS>
-__global__ __launch_bounds__(256) void k_i8_both(const I8QuantArgs a, int pitch, int pitch_t) {
+__global__ __launch_bounds__(256) void k_i8_both(const I8QuantArgs a, int pitch, int pitch_t, int row_parts,
+                                                 int col_parts) {
   constexpr int kPad = 136;
   __shared__ __align__(16) uint8_t tile[128 * kPad];
-  __shared__ float inv_rows[128];
+  __shared__ float invs[2][128];  // of rows, of columns
+  __shared__ uint32_t other[2][128];
   const int tid = threadIdx.x;
   const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
-  if (tid < 128) {
-    if (ROWS) {
-      const RowScale s = r0 + tid < a.rows ? row_scale(a.tops[r0 + tid]) : RowScale{0.0f, 0.0f};
-      inv_rows[tid] = s.inv;
-      if (blockIdx.x == 0 && r0 + tid < a.rows) a.scales[r0 + tid] = s.scale;
-    }
-  } else if (blockIdx.y == 0 && c0 + tid - 128 < a.cols) {
-    a.scales_t[c0 + tid - 128] = row_scale(a.tops[a.rows + c0 + tid - 128]).scale;
-  }
   const int64_t col = c0 + (tid & 15) * 8;
+  Raw<DT, 8> raw[8];  // rows past the end: the last one again, not kept
+#pragma unroll
+  for (int p = 0; p < 8; ++p) raw[p] = raw_word<DT, 8>(a.x, min(r0 + p * 16 + (tid >> 4), a.rows - 1) * a.ld, col, a.cols);
+  {
+    // a thread a row or column and half of its parts
+    const int i = tid & 127, half = tid >> 7;
+    const uint32_t *of_cols = a.tops + (ROWS ? row_parts * a.rows : 0);
+    uint32_t row_top = 0, col_top = 0;
+    if (c0 + i < a.cols)
+#pragma unroll 8
+      for (int p = half; p < col_parts; p += 2) col_top = max(col_top, of_cols[(int64_t)p * a.cols + c0 + i]);
+    if (ROWS && r0 + i < a.rows)
+#pragma unroll 4
+      for (int p = half; p < row_parts; p += 2) row_top = max(row_top, a.tops[(int64_t)p * a.rows + r0 + i]);
+    if (half) {
+      other[0][i] = row_top;
+      other[1][i] = col_top;
+    }
+    __syncthreads();
+    if (!half) {
+      const RowScale r = row_scale(max(row_top, other[0][i])), c = row_scale(max(col_top, other[1][i]));
+      invs[0][i] = r.inv;
+      invs[1][i] = c.inv;
+      if (ROWS && blockIdx.x == 0 && r0 + i < a.rows) a.scales[r0 + i] = r.scale;
+      if (blockIdx.y == 0 && c0 + i < a.cols) a.scales_t[c0 + i] = c.scale;
+    }
+    __syncthreads();
+  }
   float inv_cols[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) inv_cols[i] = col + i < a.cols ? row_scale(a.tops[a.rows + col + i]).inv : 0.0f;
-  float x[8][8];
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int64_t row = r0 + p * 16 + (tid >> 4);
-    if (row < a.rows && col < a.cols) {
-      load_word<DT>(a.x, row * a.ld, col, a.cols, x[p]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[p][i] = 0.0f;
-    }
-  }
-  if (ROWS) __syncthreads();
+  for (int i = 0; i < 8; ++i) inv_cols[i] = invs[1][(tid & 15) * 8 + i];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int r = p * 16 + (tid >> 4);
     const int64_t row = r0 + r;
+    float x[8];
+    open_word(raw[p], a.x, min(row, a.rows - 1) * a.ld, col, a.cols, x);
+    if (row >= a.rows) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    }
     uint32_t h[8] = {};
     if constexpr (STOCH) {
       const uint32_t first = a.index_base + (uint32_t)(row * a.cols) + (uint32_t)col;
@@ -219,15 +243,15 @@ __global__ __launch_bounds__(256) void k_i8_both(const I8QuantArgs a, int pitch,
       for (int i = 0; i < 8; ++i) h[i] = draw(first + i, a.key_mix);
     }
     if constexpr (ROWS) {
-      const float inv = inv_rows[r];
-      const u32x2 w = eight_codes<STOCH>(x[p], inv, h);
+      const float inv = invs[0][r];
+      const u32x2 w = eight_codes<STOCH>(x, inv, h);
       if (row < a.rows)
         *reinterpret_cast<u32x2 *>(a.codes + row * pitch + col) = inv == 0.0f ? u32x2{0u, 0u} : w;
     }
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      c[i] = STOCH ? drawn_byte(x[p][i], inv_cols[i], h[i]) : nearest_byte(x[p][i], inv_cols[i]);
+      c[i] = STOCH ? drawn_byte(x[i], inv_cols[i], h[i]) : nearest_byte(x[i], inv_cols[i]);
       if (inv_cols[i] == 0.0f) c[i] = 0;
     }
     *reinterpret_cast<u32x2 *>(tile + r * kPad + (tid & 15) * 8) =
@@ -405,6 +429,13 @@ constexpr int64_t kFewRows = 16;
 // LDS of M packed rows: a row is padded by a chunk, so that 16 rows lie on different banks.
 inline size_t few_lds(int64_t M, int64_t pitch) { return (size_t)M * (size_t)(pitch + 16); }
 
+// A barrier for what crosses LDS alone: loads stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <int AT>
 __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8MatmulArgs a, int pitch) {
   __shared__ i32x4 sums[kFewWaves][64];
@@ -421,9 +452,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
     to[0] = __builtin_nontemporal_load(p);
     to[1] = __builtin_nontemporal_load(p + 4);
   };
+  auto first_weights = [&]() {  // past the end: the last ones again, not multiplied
 #pragma unroll
-  for (int i = 0; i < kFewAhead; ++i)
-    if (wave + i * kFewWaves < steps) load(wave + i * kFewWaves, w[i]);
+    for (int i = 0; i < kFewAhead; ++i) load(min(wave + i * kFewWaves, steps - 1), w[i]);
+  };
   const uint8_t *rows = static_cast<const uint8_t *>(a.a);
   int row_bytes = pitch;
   const int M = (int)a.M;
@@ -432,46 +464,73 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
     int shift = 0;  // a row's share of the threads: 512 >> shift, the rows rounded up to a power of two
     while ((1 << shift) < M) ++shift;
     const int threads = (kFewWaves * 64) >> shift, row = threadIdx.x / threads, t = threadIdx.x % threads;
+    // A's first elements before the weights, as loads return in their order
+    constexpr int kHeld = 4;
+    Raw<AT, 8> raw[kHeld];
+    float x[kHeld][8];
+    const int64_t row_at = min(row, M - 1) * a.lda;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) raw[i] = raw_word<AT, 8>(a.a, row_at, (int64_t)(t + i * threads) * 8, a.K);
     if (threadIdx.x < kFewRows) tops[threadIdx.x] = 0;
-    __syncthreads();
-    float x[8];
+    lds_barrier();
+    first_weights();
     uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      open_word(raw[i], a.a, row_at, (int64_t)(t + i * threads) * 8, a.K, x[i]);
+      top = max(top, top_of(x[i]));
+    }
     if (row < M)
-      for (int g = t; g * 8 < a.K; g += threads) {
-        load_word<AT>(a.a, row * a.lda, (int64_t)g * 8, a.K, x);
-        top = max(top, top_of(x));
+      for (int g = t + kHeld * threads; g * 8 < a.K; g += threads) {
+        float more[8];
+        load_word<AT>(a.a, row * a.lda, (int64_t)g * 8, a.K, more);
+        top = max(top, top_of(more));
       }
     for (int m = 1; m < threads && m < 64; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-    if (row < M && (t & 63) == 0) atomicMax(&tops[row], top);
-    __syncthreads();
+    if (row < M && (threads < 64 ? t == 0 : (t & 63) == 0)) atomicMax(&tops[row], top);
+    lds_barrier();
     if (row < M) {
       const RowScale s = row_scale(tops[row]);
       const uint32_t h[8] = {};
-      for (int g = t; g < pitch / 8; g += threads) {
-        load_word<AT>(a.a, row * a.lda, (int64_t)g * 8, a.K, x);
-        const u32x2 c = eight_codes<false>(x, s.inv, h);
+      auto pack = [&](int g, const float (&v)[8]) {
+        const u32x2 c = eight_codes<false>(v, s.inv, h);
         *reinterpret_cast<u32x2 *>(packed + row * row_bytes + g * 8) = s.inv == 0.0f ? u32x2{0u, 0u} : c;
+      };
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (t + i * threads < pitch / 8) pack(t + i * threads, x[i]);
+      for (int g = t + kHeld * threads; g < pitch / 8; g += threads) {
+        float more[8];
+        load_word<AT>(a.a, row * a.lda, (int64_t)g * 8, a.K, more);
+        pack(g, more);
       }
     }
     rows = packed;
-    __syncthreads();
+    lds_barrier();
+  } else {
+    first_weights();
   }
   i32x4 acc = {0, 0, 0, 0};
-  for (int first = wave; first < steps; first += kFewAhead * kFewWaves) {
+  auto multiply = [&](int k, const i32x4 (&v)[2]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      i32x4 u = {0, 0, 0, 0};
+      if (r16 < M) u = *reinterpret_cast<const i32x4 *>(rows + (int64_t)r16 * row_bytes + k * 128 + p * 64 + quarter * 16);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[p], u, acc, 0, 0, 0);
+    }
+  };
+  constexpr int kTurn = kFewAhead * kFewWaves;
+  int first = wave;
+  for (; first + kTurn < steps; first += kTurn) {  // a turn, with the next one's weights on their way
 #pragma unroll
     for (int i = 0; i < kFewAhead; ++i) {
-      const int k = first + i * kFewWaves;
-      if (k < steps) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          i32x4 v = {0, 0, 0, 0};
-          if (r16 < M) v = *reinterpret_cast<const i32x4 *>(rows + (int64_t)r16 * row_bytes + k * 128 + p * 64 + quarter * 16);
-          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i][p], v, acc, 0, 0, 0);
-        }
-        if (k + kFewAhead * kFewWaves < steps) load(k + kFewAhead * kFewWaves, w[i]);
-      }
+      multiply(first + i * kFewWaves, w[i]);
+      load(min(first + i * kFewWaves + kTurn, steps - 1), w[i]);
     }
   }
+#pragma unroll
+  for (int i = 0; i < kFewAhead; ++i)
+    if (first + i * kFewWaves < steps) multiply(first + i * kFewWaves, w[i]);
   sums[wave][lane] = acc;
   __syncthreads();
   if (threadIdx.x < 256) {
@@ -498,8 +557,6 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
     }
   }
 }
-
-constexpr int kCus = 256;
 
 struct Plan {
   int bm, bn;        // tile
@@ -544,13 +601,32 @@ void tiles_of(const I8MatmulArgs &a, const Plan &p, hipStream_t s) {
       a, (int)i8_pitch(a.K), tm, tn, p.each);
 }
 
+// Parts of the largest magnitudes: 512 columns each of a row, and of a column as many as give some four
+// blocks a CU, at most 256.
+struct Parts {
+  int rows, cols, rows_each;
+};
+
+Parts tops_parts(int64_t rows, int64_t cols) {
+  Parts p;
+  p.rows = (int)((cols + 511) / 512);
+  int64_t n = (4 * kCus + p.rows - 1) / p.rows, most = (rows + 63) / 64;
+  if (n > 256) n = 256;
+  if (n > most) n = most;
+  p.rows_each = (int)(((rows + n - 1) / n + 63) / 64 * 64);
+  p.cols = (int)((rows + p.rows_each - 1) / p.rows_each);
+  return p;
+}
+
 template <int DT, bool STOCH>
 void quantize_of(const I8QuantArgs &a, hipStream_t s) {
   const int pitch = (int)i8_pitch(a.cols);
   if (!a.codes_t) {
     // a row in a wave's registers where it fits, else in a block's, else read twice
-    if (a.cols <= 2048)
-      k_i8_rows<DT, STOCH, 1, 4><<<(unsigned)((a.rows + 3) / 4), 256, 0, s>>>(a, pitch);
+    if (a.cols <= 1024)
+      k_i8_rows<DT, STOCH, 1, 2><<<(unsigned)((a.rows + 3) / 4), 256, 0, s>>>(a, pitch);
+    else if (a.cols <= 4096)
+      k_i8_rows<DT, STOCH, 4, 2><<<(unsigned)a.rows, 256, 0, s>>>(a, pitch);
     else if (a.cols <= 12288)
       k_i8_rows<DT, STOCH, 4, 6><<<(unsigned)a.rows, 256, 0, s>>>(a, pitch);
     else
@@ -558,22 +634,24 @@ void quantize_of(const I8QuantArgs &a, hipStream_t s) {
     return;
   }
   const int pitch_t = (int)i8_pitch(a.rows);
-  k_i8_clear<<<(unsigned)((a.rows + a.cols + 255) / 256), 256, 0, s>>>(a.tops, a.rows + a.cols);
-  const dim3 parts((unsigned)((a.cols + 511) / 512), (unsigned)((a.rows + 63) / 64));
+  const Parts t = tops_parts(a.rows, a.cols);
+  const dim3 parts((unsigned)t.rows, (unsigned)t.cols);
   const dim3 tiles((unsigned)(pitch / 128), (unsigned)(pitch_t / 128));
   if (a.codes) {
-    k_i8_tops<DT, true><<<parts, 256, 0, s>>>(a);
-    k_i8_both<DT, STOCH, true><<<tiles, 256, 0, s>>>(a, pitch, pitch_t);
+    k_i8_tops<DT, true><<<parts, 256, 0, s>>>(a, t.rows_each);
+    k_i8_both<DT, STOCH, true><<<tiles, 256, 0, s>>>(a, pitch, pitch_t, t.rows, t.cols);
   } else {
-    k_i8_tops<DT, false><<<parts, 256, 0, s>>>(a);
-    k_i8_both<DT, STOCH, false><<<tiles, 256, 0, s>>>(a, pitch, pitch_t);
+    k_i8_tops<DT, false><<<parts, 256, 0, s>>>(a, t.rows_each);
+    k_i8_both<DT, STOCH, false><<<tiles, 256, 0, s>>>(a, pitch, pitch_t, 0, t.cols);
   }
 }
 
 }  // namespace
 
 size_t i8_quantize_scratch(int64_t rows, int64_t cols, bool by_cols) {
-  return by_cols ? (size_t)(rows + cols) * sizeof(uint32_t) : 0;
+  if (!by_cols) return 0;
+  const Parts p = tops_parts(rows, cols);
+  return ((size_t)p.rows * (size_t)rows + (size_t)p.cols * (size_t)cols) * sizeof(uint32_t);
 }
 
 hipError_t launch_i8_quantize(const I8QuantArgs &a, int dtype, hipStream_t s) {

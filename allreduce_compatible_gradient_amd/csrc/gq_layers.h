@@ -25,7 +25,7 @@ struct I8QuantArgs {
   int32_t stochastic;
   uint32_t key_mix;        // key ^ (key >> 16)
   uint32_t index_base;
-  uint32_t *tops;          // scratch: rows + cols largest magnitudes (bits), where codes_t is wanted
+  uint32_t *tops;          // scratch: parts' largest magnitudes (bits), where codes_t is wanted
 };
 
 struct I8MatmulArgs {

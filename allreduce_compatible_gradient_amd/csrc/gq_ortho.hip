@@ -26,7 +26,7 @@ namespace gq {
 namespace {
 
 constexpr float kScaleX = 256.0f, kScaleB = 1024.0f;
-constexpr int kNormBlocks = 256;
+constexpr int kNormBlocks = 1024;
 
 // One group of matrices; every array holds `batch` of them, one after another.
 struct Work {
@@ -51,24 +51,32 @@ __device__ __forceinline__ u32x4 eight_halves(const float (&v)[8]) {
 }
 
 // ---------------------------------------------------------------- G to X
-// Sums of squares in 64 bits, one a block.
+// Sums of squares in 64 bits, one a block: four rows' eight elements a thread on their way together.
 template <int DT>
 __global__ __launch_bounds__(256) void k_ortho_norm(const OrthoArgs a, double *norms) {
   __shared__ double part[4];
   const int64_t base = (int64_t)blockIdx.y * a.stride_g;
-  const int64_t groups = (a.cols + 7) / 8, all = a.rows * groups;
   double sum = 0.0;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < all; t += (int64_t)gridDim.x * 256) {
-    const int64_t r = t / groups, c = (t - r * groups) * 8;
-    float x[8];
-    load_word<DT>(a.g, base + r * a.ldg, c, a.cols, x);
+  const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+  for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += (int64_t)blockDim.x * 8)
+    for (int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; r < a.rows; r += 4 * stride) {
+      Raw<DT, 8> raw[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += (double)x[i] * (double)x[i];
-  }
+      for (int u = 0; u < 4; ++u) raw[u] = raw_word<DT, 8>(a.g, base + min(r + u * stride, a.rows - 1) * a.ldg, c, a.cols);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (r + u * stride >= a.rows) break;
+        float x[8];
+        open_word(raw[u], a.g, base + (r + u * stride) * a.ldg, c, a.cols, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += (double)x[i] * (double)x[i];
+      }
+    }
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
   for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  if ((tid & 63) == 0) part[tid >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) norms[(int64_t)blockIdx.y * kNormBlocks + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
+  if (tid == 0) norms[(int64_t)blockIdx.y * kNormBlocks + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
 // X in fp32 and in halves both ways, padding zero, 64 x 64 elements a block.  A matrix of zeros stays
@@ -79,17 +87,22 @@ __global__ __launch_bounds__(256) void k_ortho_start(const OrthoArgs a, const Wo
   __shared__ double sums[4];
   const int tid = threadIdx.x;
   const int64_t k = blockIdx.z;
-  double sum = tid < parts ? w.norms[k * kNormBlocks + tid] : 0.0;
+  double sum = 0.0;
+  for (int i = tid; i < parts; i += 256) sum += w.norms[k * kNormBlocks + i];
   for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
   if ((tid & 63) == 0) sums[tid >> 6] = sum;
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
   const int64_t r0 = FLIP ? j0 : i0, c0 = FLIP ? i0 : j0;  // the tile's place in G
   const int64_t base = k * a.stride_g;
+  Raw<DT, 8> raw[2];  // rows past the end: the last one again, not kept
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    raw[p] = raw_word<DT, 8>(a.g, base + min(r0 + p * 32 + (tid >> 3), a.rows - 1) * a.ldg, c0 + (tid & 7) * 8, a.cols);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int r = p * 32 + (tid >> 3), c = (tid & 7) * 8;
-    float x[8] = {};
-    if (r0 + r < a.rows && c0 + c < a.cols) load_word<DT>(a.g, base + (r0 + r) * a.ldg, c0 + c, a.cols, x);
+    float x[8];
+    open_word(raw[p], a.g, base + min(r0 + r, a.rows - 1) * a.ldg, c0 + c, a.cols, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (FLIP)
@@ -111,7 +124,7 @@ __global__ __launch_bounds__(256) void k_ortho_start(const OrthoArgs a, const Wo
     float v[8], h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v[i] = j0 + c + i < w.m ? value(tile[r][c + i]) : 0.0f;
+      v[i] = j0 + c + i < w.m ? value(tile[r][c + i]) : 0.0f;  // (rows past n are not stored)
       h[i] = v[i] * kScaleX;
     }
     if (i0 + r < w.n) {
@@ -494,10 +507,12 @@ void group(const OrthoArgs &a, hipStream_t s) {
   w.diag_b = reinterpret_cast<float *>(take(z.diag));
   w.norms = reinterpret_cast<double *>(take(z.norms));
   w.partial = reinterpret_cast<float *>(p);
-  // a block of the norm takes at least 2048 elements
-  int64_t parts = (a.rows * ((a.cols + 7) / 8) + 255) / 256;
-  if (parts > kNormBlocks) parts = kNormBlocks;
-  k_ortho_norm<DT><<<dim3((unsigned)parts, (unsigned)a.batch), 256, 0, s>>>(a, w.norms);
+  const unsigned wide = a.cols > 512 ? 256 : a.cols > 128 ? 64 : 16, high = 256 / wide;
+  int64_t parts = (a.rows + 4 * high - 1) / (4 * high), most = 4096 / a.batch;
+  if (most > kNormBlocks) most = kNormBlocks;
+  if (most < 32) most = 32;
+  if (parts > most) parts = most;
+  k_ortho_norm<DT><<<dim3((unsigned)parts, (unsigned)a.batch), dim3(wide, high), 0, s>>>(a, w.norms);
   const dim3 tiles((unsigned)(w.mp / 64), (unsigned)(w.np / 64), (unsigned)a.batch);
   if (a.rows > a.cols)
     k_ortho_start<DT, true><<<tiles, 256, 0, s>>>(a, w, (int)parts);
