@@ -304,7 +304,7 @@ typedef i32x4 i32x4_e4 __attribute__((aligned(4)));
 template <class S>
 __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pitch, int tiles_m,
                                                     int tiles_n, int steps_each) {
-  constexpr int WN = S::WN, FM = S::FM, FN = S::FN;
+  constexpr int WN = S::WN, R = S::R, C = S::C;
   GQ_TILE_LDS(S);
   int bm, bn;
   tile_at(near_tiles(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, bm, bn);
@@ -312,12 +312,13 @@ __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pi
   const TileRows ra = {static_cast<const uint8_t *>(a.a) + m0 * pitch, (int)min((int64_t)S::BM, a.M - m0)};
   const TileRows rb = {reinterpret_cast<const uint8_t *>(a.b) + n0 * pitch, (int)min((int64_t)S::BN, a.N - n0)};
   const int step0 = blockIdx.y * steps_each;
-  i32x4 acc[FM * 2][FN * 2] = {};
+  i32x4 acc[R][C] = {};
   tile_product<I8Product, S>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
                              min(steps_each, pitch / kStepBytes - step0), acc);
   const int lane = threadIdx.x & 63;
-  const int64_t wm0 = m0 + wave / WN * FM * 32, wn0 = n0 + wave % WN * FN * 32;
-  const int64_t n = wn0 + lane % (FN * 4) * 8;  // a lane's columns
+  const int64_t wm0 = m0 + wave / WN * R * 16, wn0 = n0 + wave % WN * C * 16;
+  static_assert(S::kSameCols, "a lane's columns");
+  const int64_t n = wn0 + S::col_of(0, lane);
   auto nothing = [](int) {};
   if (gridDim.y > 1) {
     int32_t *part = a.partial + (int64_t)blockIdx.y * a.M * a.N;
@@ -340,9 +341,9 @@ __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pi
   }
   // scales of the rows that a lane has before the exchange, scales and biases of the columns that it
   // has after it; no bias is -0, which changes nothing that it is added to
-  float sa[FM * 2], sb[8], bias[8];
+  float sa[R], sb[8], bias[8];
 #pragma unroll
-  for (int k = 0; k < FM * 2; ++k) sa[k] = a.a_scales[min(wm0 + k * 16 + (lane & 15), a.M - 1)];
+  for (int k = 0; k < R; ++k) sa[k] = a.a_scales[min(wm0 + k * 16 + (lane & 15), a.M - 1)];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int64_t c = min(n + e, a.N - 1);
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pi
       constexpr int kElem = decltype(half_width)::value ? 2 : 4;
       char *const out = static_cast<char *>(a.out) + (wm0 * a.ldo + n) * kElem;
       const int64_t row_bytes = a.ldo * kElem;
-      const int rows = (int)min((int64_t)FM * 32, a.M - wm0);
+      const int rows = (int)min((int64_t)R * 16, a.M - wm0);
       by_rows<I8Product, S>(acc, own, by_token, nothing, [&](int i, int, int row, int, f32x4 lo, f32x4 hi) {
         float v[8];
         finished(lo, hi, v);
@@ -685,11 +686,11 @@ hipError_t launch_i8_matmul(const I8MatmulArgs &a, hipStream_t s) {
   }
   const Plan p = plan(a.M, a.N, a.K);
   if (p.bm == 256)
-    tiles_of<TileShape<2, 4, 4, 2, 2>>(a, p, s);
+    tiles_of<TileShape<2, 4, 8, 4, 2>>(a, p, s);
   else if (p.bm == 128)
-    tiles_of<TileShape<2, 2, 2, 2, 2>>(a, p, s);
+    tiles_of<TileShape<2, 2, 4, 4, 2>>(a, p, s);
   else
-    tiles_of<TileShape<1, 4, 2, 1, 2>>(a, p, s);
+    tiles_of<TileShape<1, 4, 4, 2, 2>>(a, p, s);
   if (p.splits > 1) k_i8_join<<<(unsigned)((a.M * a.N + 255) / 256), 256, 0, s>>>(a, p.splits);
   return hipGetLastError();
 }

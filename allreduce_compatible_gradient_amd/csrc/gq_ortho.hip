@@ -140,22 +140,22 @@ __global__ __launch_bounds__(256) void k_ortho_start(const OrthoArgs a, const Wo
 }
 
 // ---------------------------------------------------------------- products
-// A wave's 32 x (FN * 32) halves by columns, from what by_rows' lanes hold, through the wave's part of
-// LDS (columns of 72 bytes: the rows' writes fall on different banks): f(column, first row, eight rows).
-template <int FN, class F>
-__device__ __forceinline__ void by_columns(const u32x4 (&keep)[FN * 2], uint8_t *own, F &&f) {
+// A wave's 32 x 16 C halves by columns, from what by_rows' lanes hold, through the wave's part of LDS
+// (columns of 72 bytes: the rows' writes fall on different banks): f(column, first row, eight rows).
+template <class S, class F>
+__device__ __forceinline__ void by_columns(const u32x4 (&keep)[S::C], uint8_t *own, F &&f) {
+  static_assert(S::kOwn >= S::C * 16 * 72, "a wave's columns fit its part");
   const int lane = threadIdx.x & 63;
-  const int col = lane % (FN * 4) * 8;
 #pragma unroll
-  for (int p = 0; p < FN * 2; ++p) {
-    const int row = p * (16 / FN) + lane / (FN * 4);
+  for (int p = 0; p < S::C; ++p) {
+    const int row = S::row_of(p, lane), col = S::col_of(p, lane);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       *reinterpret_cast<uint16_t *>(own + (col + e) * 72 + row * 2) = (uint16_t)(keep[p][e >> 1] >> (16 * (e & 1)));
   }
   wave_exchange();
 #pragma unroll
-  for (int p = 0; p < FN * 2; ++p) {
+  for (int p = 0; p < S::C; ++p) {
     const int c = p * 16 + (lane >> 2), piece = lane & 3;
     const u32x2 lo = *reinterpret_cast<const u32x2 *>(own + c * 72 + piece * 16);
     const u32x2 hi = *reinterpret_cast<const u32x2 *>(own + c * 72 + piece * 16 + 8);
@@ -179,7 +179,7 @@ __device__ __forceinline__ void triangle_at(int t, int tiles, int &i, int &j) {
 template <bool SQUARE, class S>
 __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb, float cc, int tiles,
                                                           int steps_each) {
-  constexpr int WN = S::WN, FM = S::FM, FN = S::FN;
+  constexpr int WN = S::WN, R = S::R, C = S::C;
   GQ_TILE_LDS(S);
   const int lane = threadIdx.x & 63;
   static_assert(S::BM == S::BN, "mirrored tiles");
@@ -191,10 +191,10 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
   const TileRows ra = {of + (int64_t)i0 * pitch, min(S::BM, w.n - i0)};
   const TileRows rb = {of + (int64_t)j0 * pitch, min(S::BN, w.n - j0)};
   const int step0 = blockIdx.y * steps_each;
-  f32x4 acc[FM * 2][FN * 2] = {};
+  f32x4 acc[R][C] = {};
   tile_product<F16Product, S>(lds0, lds1, lds2, lds3, ra, rb, pitch, step0,
                                            min(steps_each, pitch / kStepBytes - step0), acc);
-  const int wi = wave / WN * FM * 32, wj = wave % WN * FN * 32;
+  const int wi = wave / WN * R * 16, wj = wave % WN * C * 16;
   auto as_is = [](int, f32x4 v) { return v; };
   if (!SQUARE && gridDim.y > 1) {
     float *part = w.partial + (((int64_t)k * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * (S::BM * S::BN);
@@ -209,25 +209,30 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
   const _Float16 *const f = w.f + k * w.n * w.np;
   const float *const da = w.diag_a + k * w.np;
   float *const diag = (SQUARE ? w.diag_b : w.diag_a) + k * w.np;
-  const int j = j0 + wj + lane % (FN * 4) * 8;  // a lane's columns
-  float dj[8];
+  constexpr int kCols = S::kSameCols ? 1 : C;  // different columns that a lane has
+  float dj[kCols][8];
   if (SQUARE) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dj[e] = j + e < w.n ? da[j + e] : 0.0f;
+    for (int p = 0; p < kCols; ++p)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + wj + S::col_of(p, lane) + e;
+        dj[p][e] = j < w.n ? da[j] : 0.0f;
+      }
   }
-  u32x4 keep[FN * 2];
-  f16x8 olds[2][FN * 2];
-  float dis[2][FN * 2];
+  u32x4 keep[C];
+  f16x8 olds[2][C];
+  float dis[2][C];
   by_rows<F16Product, S>(acc, own, as_is, [&](int i32) {
     if (!SQUARE) return;
 #pragma unroll
-    for (int p = 0; p < FN * 2; ++p) {
-      const int i = min(i0 + wi + i32 * 32 + p * (16 / FN) + lane / (FN * 4), w.n - 1);
+    for (int p = 0; p < C; ++p) {
+      const int i = min(i0 + wi + i32 * 32 + S::row_of(p, lane), w.n - 1);
       dis[i32 & 1][p] = da[i];
-      olds[i32 & 1][p] = *reinterpret_cast<const f16x8 *>(f + (int64_t)i * w.np + min(j, w.np - 8));
+      olds[i32 & 1][p] = *reinterpret_cast<const f16x8 *>(f + (int64_t)i * w.np + min(j0 + wj + S::col_of(p, lane), w.np - 8));
     }
-  }, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
-    const int i = i0 + wi + i32 * 32 + row;
+  }, [&](int i32, int p, int row, int col, f32x4 lo, f32x4 hi) {
+    const int i = i0 + wi + i32 * 32 + row, j = j0 + wj + col;
     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     const bool there = i < w.n && j < w.np;
     const float di = SQUARE ? dis[i32 & 1][p] : 0.0f;
@@ -239,7 +244,7 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
       if (SQUARE) {
         const float sq = v[e] * (1.0f / (kScaleB * kScaleB)), fe = (float)old[e] * (1.0f / kScaleB);
         if (on && in) diag[i] = cb * di + cc * (di * di + sq);
-        r = cb * fe + cc * ((di + dj[e]) * fe + sq);
+        r = cb * fe + cc * ((di + dj[S::kSameCols ? 0 : p][e]) * fe + sq);
       } else {
         r = v[e] * (1.0f / (kScaleX * kScaleX));
         if (on && in) diag[i] = r;
@@ -250,7 +255,7 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
     if (there) *reinterpret_cast<u32x4 *>(to + (int64_t)i * w.np + j) = keep[p];
   }, [&](int i32) {
     if (ti == tj) return;
-    by_columns<FN>(keep, own, [&](int c, int r, u32x4 h) {
+    by_columns<S>(keep, own, [&](int c, int r, u32x4 h) {
       const int col = j0 + wj + c, row = i0 + wi + i32 * 32 + r;
       if (col < w.n && row < w.np) *reinterpret_cast<u32x4 *>(to + (int64_t)col * w.np + row) = h;
     });
@@ -311,9 +316,8 @@ __global__ __launch_bounds__(256) void k_ortho_join(const Work w, int tiles, int
 template <class S>
 __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const OrthoArgs o, float ca,
                                                        int tiles_i, int tiles_j, int last) {
-  constexpr int WN = S::WN, FM = S::FM, FN = S::FN;
+  constexpr int WN = S::WN, R = S::R, C = S::C;
   GQ_TILE_LDS(S);
-  static_assert(S::kOwn >= FN * 32 * 72, "a wave's columns fit its part");
   const int lane = threadIdx.x & 63;
   int ti, tj;
   tile_at(near_tiles(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, ti, tj);
@@ -323,29 +327,28 @@ __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const Ortho
   const uint8_t *xt = reinterpret_cast<const uint8_t *>(w.xt[0] + k * w.m * w.np);
   const TileRows ra = {b + (int64_t)i0 * pitch, min(S::BM, w.n - i0)};
   const TileRows rb = {xt + (int64_t)j0 * pitch, min(S::BN, w.m - j0)};
-  f32x4 acc[FM * 2][FN * 2] = {};
+  f32x4 acc[R][C] = {};
   tile_product<F16Product, S>(lds0, lds1, lds2, lds3, ra, rb, pitch, 0, pitch / kStepBytes, acc);
-  const int wi = wave / WN * FM * 32, wj = wave % WN * FN * 32;
+  const int wi = wave / WN * R * 16, wj = wave % WN * C * 16;
   float *const x = w.x + k * w.n * w.mp;
   _Float16 *const xh = w.xh + k * w.n * w.mp, *const next = w.xt[1] + k * w.m * w.np;
   const float *const diag = w.diag_b + k * w.np;
   uint16_t *const out = static_cast<uint16_t *>(o.out) + k * o.stride_o;
   const bool flip = o.rows > o.cols;
-  const int j = j0 + wj + lane % (FN * 4) * 8;
-  u32x4 keep[FN * 2];
-  f32x4 xs[2][FN * 2][2];
-  float ds[2][FN * 2];
+  u32x4 keep[C];
+  f32x4 xs[2][C][2];
+  float ds[2][C];
   by_rows<F16Product, S>(acc, own, [](int, f32x4 v) { return v; }, [&](int i32) {
 #pragma unroll
-    for (int p = 0; p < FN * 2; ++p) {
-      const int i = min(i0 + wi + i32 * 32 + p * (16 / FN) + lane / (FN * 4), w.n - 1);
-      const f32x4 *at = reinterpret_cast<const f32x4 *>(x + (int64_t)i * w.mp + min(j, w.mp - 8));
+    for (int p = 0; p < C; ++p) {
+      const int i = min(i0 + wi + i32 * 32 + S::row_of(p, lane), w.n - 1);
+      const f32x4 *at = reinterpret_cast<const f32x4 *>(x + (int64_t)i * w.mp + min(j0 + wj + S::col_of(p, lane), w.mp - 8));
       xs[i32 & 1][p][0] = at[0];
       xs[i32 & 1][p][1] = at[1];
       ds[i32 & 1][p] = diag[i];
     }
-  }, [&](int i32, int p, int row, int, f32x4 lo, f32x4 hi) {
-    const int i = i0 + wi + i32 * 32 + row;
+  }, [&](int i32, int p, int row, int col, f32x4 lo, f32x4 hi) {
+    const int i = i0 + wi + i32 * 32 + row, j = j0 + wj + col;
     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, h[8] = {};
     const bool there = i < w.n && j < w.mp;
     if (there) {
@@ -381,7 +384,7 @@ __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const Ortho
     }
   }, [&](int i32) {
     if (last && !flip) return;
-    by_columns<FN>(keep, own, [&](int c, int r, u32x4 h) {
+    by_columns<S>(keep, own, [&](int c, int r, u32x4 h) {
       const int col = j0 + wj + c, row = i0 + wi + i32 * 32 + r;
       if (col >= w.m) return;
       if (!last) {
@@ -407,36 +410,65 @@ constexpr size_t kGroupBytes = (size_t)2 << 30;
 int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-struct Side {
-  int side, splits, each;
+// Expected time of a launch in us: a block of a side takes `step` a step of 64 halves and `rest` besides,
+// as many blocks one after another as the fullest CU has; `wait` a step and `once` come on top.  Fitted
+// to eleven sizes (n 256 to 6000, m 768 to 11008, batches to 48), where the sides so chosen are the best
+// ones or lose at most 22 us of 390.  One side instead of the chosen one: 4096 x 4096, Gram matrix and
+// square together 293 us of a step's time less with 192 than with 256 (253 tiles against 136 on 256 CUs).
+struct Cost {
+  int side;
+  float step, rest, wait, once;
 };
+constexpr Cost kSymmetric[] = {{256, 0.93f, 12.8f, 0.09f, 0.8f}, {192, 0.64f, 8.3f, 0.08f, 0.3f},
+                               {128, 0.31f, 4.5f, 0.29f, 3.5f}, {64, 0.28f, 0.0f, 0.0f, 3.4f}};
+constexpr Cost kUpdate[] = {{256, 0.93f, 40.0f, 0.09f, 0.8f}, {128, 0.31f, 9.0f, 0.29f, 3.5f}, {64, 0.13f, 2.4f, 0.0f, 7.8f}};
 
-// Side of the symmetric products' tiles: the largest of which there is one a CU, else the smallest; the
-// Gram matrix, whose sums are long, in splits where its tiles leave CUs idle.
-Side gram_plan(int64_t batch, int64_t n, int64_t m) {
-  Side s = {64, 1, 0};
-  for (int side : {256, 128}) {
-    const int64_t t = (n + side - 1) / side;
-    if (batch * t * (t + 1) / 2 >= kCus / 2) {
-      s.side = side;
-      break;
-    }
-  }
-  const int64_t t = (n + s.side - 1) / s.side, count = batch * t * (t + 1) / 2;
-  const int64_t steps = up64(m) / 64;  // of 128 bytes
-  int64_t splits = kCus / count;
-  if (splits > steps / 4) splits = steps / 4;
-  if (splits > 16) splits = 16;
-  if (splits < 1) splits = 1;
-  s.each = (int)((steps + splits - 1) / splits);
-  s.splits = (int)((steps + s.each - 1) / s.each);
-  return s;
+float cost_of(const Cost &c, int64_t tiles, int64_t steps) {
+  return (float)((tiles + kCus - 1) / kCus) * ((float)steps * c.step + c.rest) + (float)steps * c.wait + c.once;
 }
 
+struct Side {
+  int side, splits, each;
+  bool alone;  // a CU has one block at most
+};
+
+// Tiles of a symmetric product with sums of `steps`; the Gram matrix, whose sums may be long, in splits
+// where its tiles leave CUs idle and a launch that joins them costs less.
+Side symmetric_plan(int64_t batch, int64_t n, int64_t steps, bool may_split) {
+  Side best = {64, 1, (int)steps, false};
+  float least = INFINITY;
+  for (const Cost &c : kSymmetric) {
+    const int64_t t = (n + c.side - 1) / c.side, count = batch * t * (t + 1) / 2;
+    int64_t most = kCus / count;
+    if (most > steps / 4) most = steps / 4;
+    if (most > 16) most = 16;
+    if (most < 1 || !may_split) most = 1;
+    for (int64_t splits : {(int64_t)1, most}) {
+      const int64_t each = (steps + splits - 1) / splits;
+      // partial sums are written and read, at some 4 TB/s
+      const float join = splits > 1 ? 4.0f + (float)(count * splits) * (float)(c.side * c.side) * 2e-6f : 0.0f;
+      const float us = cost_of(c, count * splits, each) + join;
+      if (us >= least) continue;
+      least = us;
+      best = Side{c.side, (int)((steps + each - 1) / each), (int)each, count * splits <= kCus};
+    }
+  }
+  return best;
+}
+
+Side gram_plan(int64_t batch, int64_t n, int64_t m) { return symmetric_plan(batch, n, up64(m) / 64, true); }
+
 int update_side(int64_t batch, int64_t n, int64_t m) {
-  for (int side : {256, 128})
-    if (batch * ((n + side - 1) / side) * ((m + side - 1) / side) >= kCus / 2) return side;
-  return 64;
+  int side = 64;
+  float least = INFINITY;
+  for (const Cost &c : kUpdate) {
+    const float us = cost_of(c, batch * ((n + c.side - 1) / c.side) * ((m + c.side - 1) / c.side), up64(n) / 64);
+    if (us < least) {
+      least = us;
+      side = c.side;
+    }
+  }
+  return side;
 }
 
 struct Sizes {
@@ -467,13 +499,17 @@ void symmetric(const Work &w, const OrthoArgs &a, int64_t batch, int splits, int
 }
 
 template <bool SQUARE>
-void symmetric_of(int side, const Work &w, const OrthoArgs &a, int64_t batch, int splits, int each, hipStream_t s) {
-  if (side == 256)
-    symmetric<SQUARE, TileShape<2, 4, 4, 2, 2>>(w, a, batch, splits, each, s);
-  else if (side == 128)
-    symmetric<SQUARE, TileShape<2, 2, 2, 2, 2>>(w, a, batch, splits, each, s);
+void symmetric_of(const Side &p, const Work &w, const OrthoArgs &a, int64_t batch, hipStream_t s) {
+  if (p.side == 256)
+    symmetric<SQUARE, TileShape<2, 4, 8, 4, 2>>(w, a, batch, p.splits, p.each, s);
+  else if (p.side == 192)
+    symmetric<SQUARE, TileShape<2, 4, 6, 3, 2>>(w, a, batch, p.splits, p.each, s);
+  else if (p.side == 128 && p.alone)
+    symmetric<SQUARE, TileShape<2, 2, 4, 4, 4>>(w, a, batch, p.splits, p.each, s);
+  else if (p.side == 128)
+    symmetric<SQUARE, TileShape<2, 2, 4, 4, 2>>(w, a, batch, p.splits, p.each, s);
   else
-    symmetric<SQUARE, TileShape<2, 2, 1, 1, 4>>(w, a, batch, splits, each, s);
+    symmetric<SQUARE, TileShape<2, 2, 2, 2, 4>>(w, a, batch, p.splits, p.each, s);
 }
 
 template <class S>
@@ -518,21 +554,21 @@ void group(const OrthoArgs &a, hipStream_t s) {
     k_ortho_start<DT, true><<<tiles, 256, 0, s>>>(a, w, (int)parts);
   else
     k_ortho_start<DT, false><<<tiles, 256, 0, s>>>(a, w, (int)parts);
-  const Side g = gram_plan(a.batch, n, m);
+  const Side g = gram_plan(a.batch, n, m), square = symmetric_plan(a.batch, n, w.np / 64, false);
   const int t = (int)((n + g.side - 1) / g.side), side = update_side(a.batch, n, m);
   for (int step = 0; step < a.steps; ++step) {
-    symmetric_of<false>(g.side, w, a, a.batch, g.splits, g.each, s);
+    symmetric_of<false>(g, w, a, a.batch, s);
     if (g.splits > 1)
       k_ortho_join<<<dim3((unsigned)(t * (t + 1) / 2 * (g.side / 64) * (g.side / 64)), 1, (unsigned)a.batch), 256, 0, s>>>(
           w, t, g.side, g.splits);
-    symmetric_of<true>(g.side, w, a, a.batch, 1, w.np / 64, s);
+    symmetric_of<true>(square, w, a, a.batch, s);
     const int last = step == a.steps - 1;
     if (side == 256)
-      update<TileShape<2, 4, 4, 2, 2>>(w, a, a.batch, last, s);
+      update<TileShape<2, 4, 8, 4, 2>>(w, a, a.batch, last, s);
     else if (side == 128)
-      update<TileShape<2, 2, 2, 2, 2>>(w, a, a.batch, last, s);
+      update<TileShape<2, 2, 4, 4, 2>>(w, a, a.batch, last, s);
     else
-      update<TileShape<2, 2, 1, 1, 4>>(w, a, a.batch, last, s);
+      update<TileShape<2, 2, 2, 2, 4>>(w, a, a.batch, last, s);
     _Float16 *was = w.xt[0];
     w.xt[0] = w.xt[1];
     w.xt[1] = was;

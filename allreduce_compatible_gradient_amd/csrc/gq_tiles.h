@@ -38,15 +38,29 @@ struct TileRows {
   int rows;              // rows there are, at most the tile's: later ones repeat the last
 };
 
-// Shape of a block's tile: WM x WN waves, a wave 32 FM x 32 FN results, NB buffers of a step's operands.
-template <int WM_, int WN_, int FM_, int FN_, int NB_>
+// Shape of a block's tile: WM x WN waves, a wave 16 R x 16 C results, NB buffers of a step's operands.
+// After the products a wave's results leave 32 rows at a time in C passes of 64 lanes, eight columns
+// each: where C is a power of two a lane has the same columns in all passes, else a pass has 16
+// columns.
+template <int WM_, int WN_, int R_, int C_, int NB_>
 struct TileShape {
-  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, NB = NB_;
-  static constexpr int BM = WM * FM * 32, BN = WN * FN * 32, T = WM * WN * 64;
+  static constexpr int WM = WM_, WN = WN_, R = R_, C = C_, NB = NB_;
+  static constexpr int BM = WM * R * 16, BN = WN * C * 16, T = WM * WN * 64;
   static constexpr int kStage = (BM + BN) * kStepBytes;
-  static constexpr int kOwn = 32 * FN * 128, kPer = kStage / kOwn;  // a wave's part after the products
-  static_assert(NB == 2 || NB == 4, "buffers");
+  static constexpr int kOwn = 32 * C * 64, kPer = kStage / kOwn;  // a wave's part after the products
+  static constexpr bool kSameCols = (C & (C - 1)) == 0;
+  static_assert(R % 2 == 0 && (NB == 2 || NB == 4), "pairs of rows, buffers");
   static_assert(kPer > 0 && kPer * NB >= WM * WN, "the waves' parts fit the buffers");
+  static __device__ __forceinline__ int row_of(int pass, int lane) {
+    return kSameCols ? pass * (32 / C) + lane / (C * 2) : lane >> 1;
+  }
+  static __device__ __forceinline__ int col_of(int pass, int lane) {
+    return kSameCols ? lane % (C * 2) * 8 : pass * 16 + (lane & 1) * 8;
+  }
+  // where four columns of a row are in a wave's part
+  static __device__ __forceinline__ int place(int row, int chunk) {
+    return row * (C * 64) + ((chunk ^ (kSameCols ? row & (C * 4 - 1) : row >> 2 & 3)) << 4);
+  }
 };
 
 // The buffers of a block's tile (arrays of their own), and the wave's part of them once the products
@@ -92,9 +106,9 @@ template <class P, class S>
 __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8_t *lds2,
                                              uint8_t *lds3, TileRows a, TileRows b, int pitch,
                                              int step0, int count,
-                                             typename P::Four (&acc)[S::FM * 2][S::FN * 2]) {
+                                             typename P::Four (&acc)[S::R][S::C]) {
 #if defined(__HIP_DEVICE_COMPILE__)  // buffer resources are a type of the device only
-  constexpr int WN = S::WN, FM = S::FM, FN = S::FN, NB = S::NB;
+  constexpr int WN = S::WN, R = S::R, C = S::C, H = R / 2, NB = S::NB;
   uint8_t *const lds[4] = {lds0, lds1, lds2, lds3};
   constexpr int T = S::T, CA = S::BM * 8 / T, CB = S::BN * 8 / T;  // 16-byte chunks a thread and step
   static_assert(S::BM * 8 % T == 0 && S::BN * 8 % T == 0 && T / 8 % 32 == 0, "whole chunks");
@@ -128,28 +142,30 @@ __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rb, (LDS_PTR void *)(to + S::BM * 128 + (i * T + wave * 64) * 16), 16, off_b[i], at, 0, 0);
   };
-  i32x4 fa[2][FM], fb[2][FN * 2];
+  const int odd_b = (wn * C & 1) << 5;
+  i32x4 fa[2][H], fb[2][C];
   // Group s: half of the wave's rows of A (s odd: the second) times its rows of B, 64 bytes of each
   // (s / 2: which).
   auto fetch = [&](const uint8_t *from, int s) {
     const int g = s >> 1;
     if ((s & 1) == 0) {
-      const uint8_t *lb = from + (S::BM + wn * FN * 32) * 128;
+      const uint8_t *lb = from + (S::BM + wn * C * 16) * 128;
 #pragma unroll
-      for (int i = 0; i < FN * 2; ++i) fb[g][i] = *reinterpret_cast<const i32x4 *>(lb + i * 2048 + (frag[g] ^ (i & 1) << 5));
+      for (int i = 0; i < C; ++i)
+        fb[g][i] = *reinterpret_cast<const i32x4 *>(lb + i * 2048 + (frag[g] ^ (i & 1) << 5 ^ odd_b));
     }
-    const uint8_t *la = from + (wm * FM * 32 + (s & 1) * FM * 16) * 128;
+    const uint8_t *la = from + (wm * R + (s & 1) * H) * 2048;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      fa[s & 1][i] = *reinterpret_cast<const i32x4 *>(la + i * 2048 + (frag[g] ^ ((s * FM + i) & 1) << 5));
+    for (int i = 0; i < H; ++i)
+      fa[s & 1][i] = *reinterpret_cast<const i32x4 *>(la + i * 2048 + (frag[g] ^ (((s & 1) * H + i) & 1) << 5));
     __builtin_amdgcn_sched_barrier(0);
   };
   auto multiply = [&](int s) {
 #pragma unroll
-    for (int m = 0; m < FM; ++m)
+    for (int m = 0; m < H; ++m)
 #pragma unroll
-      for (int n = 0; n < FN * 2; ++n)
-        acc[(s & 1) * FM + m][n] = P::mul(fb[s >> 1][n], fa[s & 1][m], acc[(s & 1) * FM + m][n]);
+      for (int n = 0; n < C; ++n)
+        acc[(s & 1) * H + m][n] = P::mul(fb[s >> 1][n], fa[s & 1][m], acc[(s & 1) * H + m][n]);
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
@@ -180,35 +196,33 @@ __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8
 #endif
 }
 
-// A wave's results by rows, 32 of them at a time, through its own part of LDS (rows of FN * 128
-// bytes).  For the wave's i-th 32 rows: pre(k, four) makes four neighbouring results of row
-// 16 k + (lane mod 16) of the wave's what is exchanged, f(i, pass, row, col, lo, hi) has eight
-// neighbouring columns from `col` of row `row`, a lane's columns being the same in all passes, and
+// A wave's results by rows, 32 of them at a time, through its own part of LDS.  For the wave's i-th 32
+// rows: pre(k, four) makes four neighbouring results of row 16 k + (lane mod 16) of the wave's what is
+// exchanged, f(i, pass, row, col, lo, hi) has eight neighbouring columns from `col` of row `row`, and
 // after(i) follows.  before(i) is called one turn ahead, so that what it loads arrives meanwhile: a
 // load in f itself would cost its latency in every pass.
 template <class P, class S, class H, class B, class F, class G>
-__device__ __forceinline__ void by_rows(const typename P::Four (&acc)[S::FM * 2][S::FN * 2], uint8_t *own,
-                                        H &&pre, B &&before, F &&f, G &&after) {
-  constexpr int FM = S::FM, FN = S::FN, kRow = FN * 128, kChunks = FN * 8;
-  const int lane = threadIdx.x & 63, r16 = lane & 15;
+__device__ __forceinline__ void by_rows(const typename P::Four (&acc)[S::R][S::C], uint8_t *own, H &&pre,
+                                        B &&before, F &&f, G &&after) {
+  constexpr int R = S::R, C = S::C;
+  const int lane = threadIdx.x & 63;
   before(0);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  for (int i = 0; i < R / 2; ++i) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int n = 0; n < FN * 2; ++n) {
-        const int row = m * 16 + r16, chunk = (n * 4 + (lane >> 4)) ^ (row & (kChunks - 1));
-        *reinterpret_cast<f32x4 *>(own + row * kRow + chunk * 16) = pre(i * 2 + m, acc[i * 2 + m][n]);
-      }
+      for (int n = 0; n < C; ++n)
+        *reinterpret_cast<f32x4 *>(own + S::place(m * 16 + (lane & 15), n * 4 + (lane >> 4))) =
+            pre(i * 2 + m, acc[i * 2 + m][n]);
     wave_exchange();
-    if (i + 1 < FM) before(i + 1);
+    if (i + 1 < R / 2) before(i + 1);
 #pragma unroll
-    for (int p = 0; p < FN * 2; ++p) {
-      const int row = p * (16 / FN) + lane / (FN * 4), c = lane % (FN * 4) * 2;
-      const f32x4 lo = *reinterpret_cast<const f32x4 *>(own + row * kRow + ((c ^ (row & (kChunks - 1))) * 16));
-      const f32x4 hi = *reinterpret_cast<const f32x4 *>(own + row * kRow + (((c + 1) ^ (row & (kChunks - 1))) * 16));
-      f(i, p, row, c * 4, lo, hi);
+    for (int p = 0; p < C; ++p) {
+      const int row = S::row_of(p, lane), col = S::col_of(p, lane);
+      const f32x4 lo = *reinterpret_cast<const f32x4 *>(own + S::place(row, col >> 2));
+      const f32x4 hi = *reinterpret_cast<const f32x4 *>(own + S::place(row, (col >> 2) + 1));
+      f(i, p, row, col, lo, hi);
     }
     wave_exchange();
     after(i);
