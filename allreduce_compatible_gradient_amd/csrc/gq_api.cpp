@@ -1394,7 +1394,8 @@ GQ_EXPORT gq_status gq_orthogonalise(gq_ctx *ctx, const void *g, int32_t dtype, 
   TRY(check_ptr(ctx, out, "out", none));
   if (!none && g == out) return fail(ctx, GQ_EINVAL, "out is g");
   if (none) return GQ_OK;
-  TRY(ensure_scratch(ctx, gq::ortho_scratch(batch, rows, cols), s));
+  const size_t bytes = gq::ortho_scratch(batch, rows, cols);
+  if (bytes) TRY(ensure_scratch(ctx, bytes, s));
   gq::OrthoArgs o;
   std::memset(&o, 0, sizeof o);
   o.g = g;

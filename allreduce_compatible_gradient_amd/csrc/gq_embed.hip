@@ -233,11 +233,12 @@ __device__ __forceinline__ void add_some(const EmbedGradArgs &a, int count, int6
   for (int u = 0; u < U; ++u) raw[u] = raw_word<DT, E>(a.dout, row[u], col, a.dim);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (u >= count) break;
-    float x[E];
-    open_word(raw[u], a.dout, row[u], col, a.dim, x);
+    if (u < count) {
+      float x[E];
+      open_word(raw[u], a.dout, row[u], col, a.dim, x);
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] += x[i];
+      for (int i = 0; i < E; ++i) acc[i] += x[i];
+    }
   }
 }
 
@@ -254,11 +255,11 @@ __device__ __forceinline__ void add_piece(const EmbedGradArgs &a, const int32_t 
   const int p1 = min(p0 + kPiece, all);
   // of this piece's tokens, a lane one: the token, its id, where the id's tokens begin and end
   const int here = min(p0 + lane, all - 1), id = sorted[here];
-  const int tokens[2] = {order[here], order[min(p0 + 64 + lane, all - 1)]};
+  const int token0 = order[here], token1 = order[min(p0 + 64 + lane, all - 1)];
   const int s = start[id], e = start[id + 1];
   auto token = [&](int place) {  // within this piece and the next
     const int k = place - p0;
-    return k < 64 ? __builtin_amdgcn_readlane(tokens[0], k) : __builtin_amdgcn_readlane(tokens[1], k - 64);
+    return k < 64 ? __builtin_amdgcn_readlane(token0, k) : __builtin_amdgcn_readlane(token1, k - 64);
   };
   uint64_t some = __ballot(s == p0 + lane && p0 + lane < all && e - s > kFew && e - s <= kPiece);
   for (int k = 0; some; some &= some - 1, ++k) {

@@ -403,6 +403,144 @@ __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const Ortho
   });
 }
 
+// ---------------------------------------------------------------- small matrices
+// n <= 64, m <= MP: a block a matrix, all steps in one launch, where the tiled way takes seventeen
+// launches of some 3.7 us each whatever the size.  X stays in registers, four neighbouring columns of
+// a row a lane and tile (the products' own layout), its halves by rows and by columns in LDS, and so do
+// F and B; rows are padded by 16 bytes, so that 16 rows' reads fall on different banks.  A wave has
+// MP / 8 columns of X, and two of the sixteen tiles of A and of A^2.
+template <int DT, int MP>
+__global__ __launch_bounds__(512) void k_ortho_small(const OrthoArgs a) {
+  constexpr int kRow = MP * 2 + 16, kSquare = 64 * 2 + 16, kTiles = MP / 128;
+  __shared__ __align__(16) uint8_t xh[64 * kRow];
+  __shared__ __align__(16) uint8_t xt[MP * kSquare];
+  __shared__ __align__(16) uint8_t fs[64 * kSquare];
+  __shared__ __align__(16) uint8_t bs[64 * kSquare];
+  __shared__ float diag_a[64], diag_b[64];
+  __shared__ double sums[8];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, four = (lane >> 4) * 4;
+  const bool flip = a.rows > a.cols;
+  const int n = (int)(flip ? a.cols : a.rows), m = (int)(flip ? a.rows : a.cols);
+  const int64_t base = (int64_t)blockIdx.x * a.stride_g;
+  float x[kTiles][4][4];  // tile of columns, tile of rows, columns
+  double sum = 0.0;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = r * 16 + r16, j = (wave * kTiles + t) * 16 + four + e;
+        x[t][r][e] = i < n && j < m ? load_one<DT>(a.g, base + (flip ? j * a.ldg + i : i * a.ldg + j)) : 0.0f;
+        sum += (double)x[t][r][e] * (double)x[t][r][e];
+      }
+  for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k);
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  double total = 0.0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) total += sums[w];
+  const double inv = total > 0.0 ? 1.0 / sqrt(total) : 0.0;
+  const bool bad = !(total < INFINITY);
+  auto share = [&]() {  // X's halves
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = r * 16 + r16, j = (wave * kTiles + t) * 16 + four;
+        const float *v = x[t][r];
+        const u32x2 h = {pack_half(v[0] * kScaleX, v[1] * kScaleX), pack_half(v[2] * kScaleX, v[3] * kScaleX)};
+        *reinterpret_cast<u32x2 *>(xh + i * kRow + j * 2) = h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint16_t *>(xt + (j + e) * kSquare + i * 2) = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+      }
+  };
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[t][r][e] = bad ? NAN : (float)((double)x[t][r][e] * inv);
+  share();
+  __syncthreads();
+  auto piece = [&](const uint8_t *rows, int pitch, int tile, int k) {  // 32 halves of a tile's rows
+    return *reinterpret_cast<const i32x4 *>(rows + (tile * 16 + r16) * pitch + k * 64 + (lane >> 4) * 16);
+  };
+  const int ti = wave >> 1, tj = (wave & 1) * 2;
+  for (int step = 0; step < a.steps; ++step) {
+    float f[2][4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+      for (int k = 0; k < MP / 32; ++k) acc = F16Product::mul(piece(xh, kRow, tj + q, k), piece(xh, kRow, ti, k), acc);
+      const int i = ti * 16 + r16, j = (tj + q) * 16 + four;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[q][e] = acc[e] * (1.0f / (kScaleX * kScaleX));
+        if (i == j + e) {
+          diag_a[i] = f[q][e];
+          f[q][e] = 0.0f;
+        }
+      }
+      *reinterpret_cast<u32x2 *>(fs + i * kSquare + j * 2) =
+          u32x2{pack_half(f[q][0] * kScaleB, f[q][1] * kScaleB), pack_half(f[q][2] * kScaleB, f[q][3] * kScaleB)};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) acc = F16Product::mul(piece(fs, kSquare, tj + q, k), piece(fs, kSquare, ti, k), acc);
+      const int i = ti * 16 + r16, j = (tj + q) * 16 + four;
+      const float di = diag_a[i];
+      float b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float sq = acc[e] * (1.0f / (kScaleB * kScaleB));
+        b[e] = (a.b * f[q][e] + a.c * ((di + diag_a[j + e]) * f[q][e] + sq)) * kScaleB;
+        if (i == j + e) {
+          diag_b[i] = a.b * di + a.c * (di * di + sq);
+          b[e] = 0.0f;
+        }
+      }
+      *reinterpret_cast<u32x2 *>(bs + i * kSquare + j * 2) = u32x2{pack_half(b[0], b[1]), pack_half(b[2], b[3])};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      i32x4 columns[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) columns[k] = piece(xt, kSquare, wave * kTiles + t, k);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) acc = F16Product::mul(columns[k], piece(bs, kSquare, r, k), acc);
+        const float s = a.a + diag_b[r * 16 + r16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[t][r][e] = s * x[t][r][e] + acc[e] * (1.0f / (kScaleX * kScaleB));
+      }
+    }
+    if (step == a.steps - 1) break;
+    __syncthreads();  // every wave is past its reads of X's halves
+    share();
+    __syncthreads();
+  }
+  uint16_t *const out = static_cast<uint16_t *>(a.out) + (int64_t)blockIdx.x * a.stride_o;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = r * 16 + r16, j = (wave * kTiles + t) * 16 + four + e;
+        if (i < n && j < m) out[flip ? j * a.ldo + i : i * a.ldo + j] = to_bf16(x[t][r][e]);
+      }
+}
+
 // ---------------------------------------------------------------- host
 constexpr int kCus = 256;
 constexpr size_t kGroupBytes = (size_t)2 << 30;
@@ -518,6 +656,22 @@ void update(const Work &w, const OrthoArgs &a, int64_t batch, int last, hipStrea
   k_ortho_update<S><<<dim3((unsigned)(ti * tj), 1, (unsigned)batch), S::T, 0, s>>>(w, a, a.a, ti, tj, last);
 }
 
+// What one block holds: 64 x 512 takes 159 KB of LDS.
+bool ortho_is_small(int64_t rows, int64_t cols) {
+  return (rows < cols ? rows : cols) <= 64 && (rows < cols ? cols : rows) <= 512;
+}
+
+template <int DT>
+void small(const OrthoArgs &a, hipStream_t s) {
+  const int64_t m = a.rows < a.cols ? a.cols : a.rows;
+  if (m <= 128)
+    k_ortho_small<DT, 128><<<(unsigned)a.batch, 512, 0, s>>>(a);
+  else if (m <= 256)
+    k_ortho_small<DT, 256><<<(unsigned)a.batch, 512, 0, s>>>(a);
+  else
+    k_ortho_small<DT, 512><<<(unsigned)a.batch, 512, 0, s>>>(a);
+}
+
 template <int DT>
 void group(const OrthoArgs &a, hipStream_t s) {
   const int64_t n = a.rows < a.cols ? a.rows : a.cols, m = a.rows < a.cols ? a.cols : a.rows;
@@ -579,12 +733,14 @@ void group(const OrthoArgs &a, hipStream_t s) {
 
 // Groups of at most kGroupBytes of scratch: a large batch gains nothing from more.
 int64_t ortho_group(int64_t batch, int64_t rows, int64_t cols) {
+  if (ortho_is_small(rows, cols)) return batch;
   const int64_t fit = (int64_t)(kGroupBytes / sizes_of(1, rows, cols).all());
   const int64_t most = fit < 1 ? 1 : fit > 4096 ? 4096 : fit;
   return batch < most ? batch : most;
 }
 
 size_t ortho_scratch(int64_t batch, int64_t rows, int64_t cols) {
+  if (ortho_is_small(rows, cols)) return 0;
   const int64_t group = ortho_group(batch, rows, cols);
   const size_t whole = sizes_of(group, rows, cols).all();
   const size_t rest = batch % group ? sizes_of(batch % group, rows, cols).all() : 0;
@@ -592,6 +748,10 @@ size_t ortho_scratch(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_orthogonalise(const OrthoArgs &a, int dtype, hipStream_t s) {
+  if (ortho_is_small(a.rows, a.cols)) {
+    dtype == 0 ? small<0>(a, s) : small<1>(a, s);
+    return hipGetLastError();
+  }
   const int64_t most = ortho_group(a.batch, a.rows, a.cols);
   for (int64_t first = 0; first < a.batch; first += most) {
     OrthoArgs part = a;
