@@ -1198,7 +1198,7 @@ GQ_EXPORT gq_status gq_int_quantize(gq_ctx *c, const void *x, int32_t dtype, int
   if (!c) return GQ_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   TRY(check_dtype(c, dtype, "dtype"));
-  if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
+  if (rows > 0 && ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr)))
     return fail(c, GQ_EINVAL, "codes without scales, or scales without codes");
   TRY(check_matrix(c, rows, cols, ld, codes_t ? gq::kI8MaxCols : gq::kI8MaxRows,
                    codes ? gq::kI8MaxCols : gq::kI8MaxRows, "x"));

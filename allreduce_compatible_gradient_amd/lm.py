@@ -1,7 +1,8 @@
-"""Training a language model's layers in 4 bits from a teacher's answers, under torch autograd.
+"""Training a language model's layers in 4 or 8 bits from a teacher's answers, under torch autograd.
 
-Two functions over the library's operators (``gq``): a linear layer whose three products run on
-microscaled 4-bit operands, and the distillation loss from a teacher's top log probabilities.
+Functions over the library's operators (``gq``): linear layers whose three products run on
+microscaled 4-bit operands or on 8-bit integers, the token embedding with its gradient by sorted
+tokens, and the distillation loss from a teacher's top log probabilities.
 The gradients they leave on fp32 master weights are what the gradient quantisers exchange.  They
 are differentiable once: a derivative of their gradients raises.
 
@@ -48,7 +49,8 @@ class _Once(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("mx_linear and distill are differentiable once: their gradients have no derivative")
+        raise RuntimeError("mx_linear, int_linear, embedding and distill are differentiable once: "
+                           "their gradients have no derivative")
 
 
 def _once(ctx, incoming, grad):
@@ -104,6 +106,78 @@ def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
     exchange, which draws by the same hash; workers draw apart by ``worker``.  The backward pass takes
     at most 2^32 entries of the output, the draws' counter."""
     return _Linear.apply(x, weight, bias, seed, worker, ctx)[0]
+
+
+class _IntLinear(torch.autograd.Function):
+    """y = x W^T + b in 8-bit integers.  Activations and weights have a scale for each row of what is
+    multiplied: for each token and output channel in y, for each input channel in dX = dY W, and for each
+    channel over the tokens in dW = dY^T X.  dY is rounded stochastically, both ways, so that the
+    gradients are unbiased in it."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, seed, worker, context):
+        qx, qxt = gq.int_quantize(_laid(x, strided=True), by_cols=ctx.needs_input_grad[1], ctx=context)
+        qw, qwt = gq.int_quantize(_laid(weight, strided=True), by_cols=ctx.needs_input_grad[0], ctx=context)
+        ctx.operands = qxt, qwt
+        ctx.draws, ctx.context = (seed, worker), context
+        ctx.device, ctx.shape = weight.device, weight.shape
+        ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
+        link = torch.empty(0, device=weight.device)
+        ctx.save_for_backward(link)
+        return gq.int_matmul(qx, qw, bias=None if bias is None else _laid(bias.float()),
+                             out_dtype=_code(x.dtype), ctx=context), link
+
+    @staticmethod
+    def backward(ctx, dy, _):
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        qxt, qwt = ctx.operands
+        dtype_x, dtype_w, dtype_b = ctx.dtypes
+        dx = dw = db = None
+        if need_w and len(dy) == 0:  # a product has at least one column
+            dw, need_w = torch.zeros(ctx.shape, dtype=dtype_w, device=ctx.device), False
+        if need_x or need_w:
+            q, qt = gq.int_quantize(_laid(dy), gq.INT_STOCHASTIC, *ctx.draws, by_rows=need_x,
+                                    by_cols=need_w, ctx=ctx.context)
+            if need_x:
+                dx = gq.int_matmul(q, qwt, out_dtype=_code(dtype_x), ctx=ctx.context)
+            if need_w:
+                dw = gq.int_matmul(qt, qxt, out_dtype=_code(dtype_w), ctx=ctx.context)
+        if need_b:
+            db = dy.float().sum(0).to(dtype_b)
+        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None, None
+
+
+def int_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               seed: int = 0, worker: int = 0, ctx: Optional[gq.Context] = None) -> torch.Tensor:
+    """A linear layer (x: tokens x in, weight: out x in) in 8-bit integers.  ``seed`` and ``worker`` as
+    for mx_linear; tokens, inputs and outputs are at most 2^17 where a gradient is wanted."""
+    return _IntLinear.apply(x, weight, bias, seed, worker, ctx)[0]
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, weight, ids, scale, out_dtype, context):
+        ids = _laid(ids.reshape(-1))
+        link = torch.empty(0, device=weight.device)
+        ctx.save_for_backward(link, ids)
+        ctx.table, ctx.scale, ctx.context = (weight.shape, weight.dtype), scale, context
+        out = gq.embedding(_laid(weight, strided=True), ids, scale=scale,
+                           out_dtype=_code(weight.dtype if out_dtype is None else out_dtype), ctx=context)
+        return out, link
+
+    @staticmethod
+    def backward(ctx, dout, _):
+        (vocab, _), dtype = ctx.table
+        d = gq.embedding_grad(_laid(dout, strided=True), ctx.saved_tensors[1], vocab, scale=ctx.scale,
+                              out_dtype=_code(dtype), ctx=ctx.context)
+        return _once(ctx, dout, d), None, None, None, None
+
+
+def embedding(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
+              out_dtype: Optional[torch.dtype] = None, ctx: Optional[gq.Context] = None) -> torch.Tensor:
+    """scale * weight[ids] for ids of any shape, differentiable in ``weight`` (vocab x dim); an id outside
+    the vocabulary (padding) has zeros and leaves no gradient."""
+    return _Embedding.apply(weight, ids, scale, out_dtype, ctx)[0].view(*ids.shape, weight.shape[1])
 
 
 class _Distill(torch.autograd.Function):
