@@ -472,9 +472,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
     const int64_t row_at = min(row, M - 1) * a.lda;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) raw[i] = raw_word<AT, 8>(a.a, row_at, (int64_t)(t + i * threads) * 8, a.K);
+    first_weights();
     if (threadIdx.x < kFewRows) tops[threadIdx.x] = 0;
     lds_barrier();
-    first_weights();
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {

@@ -127,9 +127,13 @@ __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8
     for (int i = 0; i < CB; ++i) off_b[i] = min(row + i * (T / 8), b.rows - 1) * pitch + chunk;
   }
   const int r16 = lane & 15;
+  // Lanes 16..31 take the third 16 bytes and 32..47 the second, for A and B alike: the order of a sum's
+  // terms.  LDS serves lanes of both halves of a wave together: with the bytes in the lanes' order every
+  // read met a conflict.
+  const int quarter = (lane >> 4 & 1) << 1 | lane >> 5;
   int frag[2];  // rows 16 further on have another key: (r XOR r / 8 mod 4) mod 8 changes by 2
 #pragma unroll
-  for (int j = 0; j < 2; ++j) frag[j] = r16 * 128 + (((4 * j + (lane >> 4)) ^ tile_key(r16)) << 4);
+  for (int j = 0; j < 2; ++j) frag[j] = r16 * 128 + (((4 * j + quarter) ^ tile_key(r16)) << 4);
   const int last = step0 + count - 1;
   auto issue = [&](uint8_t *to, int k) {  // past the end: the last step again, not multiplied
     const int at = min(k, last) * kStepBytes;
