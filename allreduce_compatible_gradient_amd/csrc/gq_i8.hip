@@ -308,6 +308,8 @@ __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pi
   GQ_TILE_LDS(S);
   int bm, bn;
   tile_at(near_tiles(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, bm, bn);
+  bm = uniform(bm);
+  bn = uniform(bn);
   const int64_t m0 = (int64_t)bm * S::BM, n0 = (int64_t)bn * S::BN;
   const TileRows ra = {static_cast<const uint8_t *>(a.a) + m0 * pitch, (int)min((int64_t)S::BM, a.M - m0)};
   const TileRows rb = {reinterpret_cast<const uint8_t *>(a.b) + n0 * pitch, (int)min((int64_t)S::BN, a.N - n0)};

@@ -183,9 +183,14 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
   GQ_TILE_LDS(S);
   const int lane = threadIdx.x & 63;
   static_assert(S::BM == S::BN, "mirrored tiles");
+  // a matrix's tiles lie on one XCD or two, which read its operands once
+  const int count = tiles * (tiles + 1) / 2, all = near_tiles(blockIdx.x, gridDim.x);
+  const int matrix = uniform(all / count), tile = uniform(all % count);
+  const int64_t k = matrix;
   int ti, tj;
-  triangle_at(near_tiles(blockIdx.x, tiles * (tiles + 1) / 2), tiles, ti, tj);
-  const int64_t k = blockIdx.z;
+  triangle_at(tile, tiles, ti, tj);
+  ti = uniform(ti);
+  tj = uniform(tj);
   const int pitch = (SQUARE ? w.np : w.mp) * 2, i0 = ti * S::BM, j0 = tj * S::BN;
   const uint8_t *of = reinterpret_cast<const uint8_t *>(SQUARE ? w.f : w.xh) + k * w.n * pitch;
   const TileRows ra = {of + (int64_t)i0 * pitch, min(S::BM, w.n - i0)};
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(S::T) void k_ortho_symmetric(const Work w, float cb
   const int wi = wave / WN * R * 16, wj = wave % WN * C * 16;
   auto as_is = [](int, f32x4 v) { return v; };
   if (!SQUARE && gridDim.y > 1) {
-    float *part = w.partial + (((int64_t)k * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * (S::BM * S::BN);
+    float *part = w.partial + ((k * gridDim.y + blockIdx.y) * count + tile) * (S::BM * S::BN);
     by_rows<F16Product, S>(acc, own, as_is, [](int) {}, [&](int i, int, int row, int col, f32x4 lo, f32x4 hi) {
       f32x4 *o = reinterpret_cast<f32x4 *>(part + (wi + i * 32 + row) * S::BN + wj + col);
       o[0] = lo;
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(256) void k_ortho_join(const Work w, int tiles, int
   const int t = blockIdx.x / (subs * subs), sub = blockIdx.x % (subs * subs);
   const int count = tiles * (tiles + 1) / 2;
   int ti, tj;
-  triangle_at(near_tiles(t, count), tiles, ti, tj);
+  triangle_at(t, tiles, ti, tj);
   const int64_t k = blockIdx.z;
   const int si = sub / subs * 64, sj = sub % subs * 64;
   const int i0 = ti * side + si, j0 = tj * side + sj;
@@ -319,9 +324,12 @@ __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const Ortho
   constexpr int WN = S::WN, R = S::R, C = S::C;
   GQ_TILE_LDS(S);
   const int lane = threadIdx.x & 63;
+  const int all = near_tiles(blockIdx.x, gridDim.x);
+  const int64_t k = uniform(all / (tiles_i * tiles_j));
   int ti, tj;
-  tile_at(near_tiles(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, ti, tj);
-  const int64_t k = blockIdx.z;
+  tile_at(uniform(all % (tiles_i * tiles_j)), tiles_i, tiles_j, ti, tj);
+  ti = uniform(ti);
+  tj = uniform(tj);
   const int pitch = w.np * 2, i0 = ti * S::BM, j0 = tj * S::BN;
   const uint8_t *b = reinterpret_cast<const uint8_t *>(w.b + k * w.n * w.np);
   const uint8_t *xt = reinterpret_cast<const uint8_t *>(w.xt[0] + k * w.m * w.np);
@@ -633,7 +641,7 @@ template <bool SQUARE, class S>
 void symmetric(const Work &w, const OrthoArgs &a, int64_t batch, int splits, int each, hipStream_t s) {
   const int t = (w.n + S::BM - 1) / S::BM;
   k_ortho_symmetric<SQUARE, S>
-      <<<dim3((unsigned)(t * (t + 1) / 2), (unsigned)splits, (unsigned)batch), S::T, 0, s>>>(w, a.b, a.c, t, each);
+      <<<dim3((unsigned)(t * (t + 1) / 2 * batch), (unsigned)splits), S::T, 0, s>>>(w, a.b, a.c, t, each);
 }
 
 template <bool SQUARE>
@@ -653,7 +661,7 @@ void symmetric_of(const Side &p, const Work &w, const OrthoArgs &a, int64_t batc
 template <class S>
 void update(const Work &w, const OrthoArgs &a, int64_t batch, int last, hipStream_t s) {
   const int ti = (w.n + S::BM - 1) / S::BM, tj = (w.m + S::BN - 1) / S::BN;
-  k_ortho_update<S><<<dim3((unsigned)(ti * tj), 1, (unsigned)batch), S::T, 0, s>>>(w, a, a.a, ti, tj, last);
+  k_ortho_update<S><<<(unsigned)(ti * tj * batch), S::T, 0, s>>>(w, a, a.a, ti, tj, last);
 }
 
 // What one block holds: 64 x 512 takes 159 KB of LDS.

@@ -233,6 +233,10 @@ __device__ __forceinline__ void by_rows(const typename P::Four (&acc)[S::R][S::C
   }
 }
 
+// What all lanes have alike, for the scalar registers: a quotient comes out of the vector ones, and a
+// buffer's address from there would be asked for lane by lane at every load.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // Blocks are handed to the XCDs in turn: an XCD's blocks take neighbouring tiles, which share
 // operand rows in its L2.
 __device__ __forceinline__ int near_tiles(int block, int total) {

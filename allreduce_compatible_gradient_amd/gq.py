@@ -708,7 +708,7 @@ def _here(*tensors):
     """The tensors lie on the current device, whose stream and context the call uses."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
+        if t is not None and t.get_device() not in (dev, -1):
             raise ValueError("a tensor is on %s, the current device is cuda:%d" % (t.device, dev))
 
 
