@@ -32,7 +32,9 @@ __device__ __forceinline__ void store_eight(void *p, int64_t i, const float (&v)
 }
 
 // ---------------------------------------------------------------- lookup
-// A thread eight elements of four tokens, whose rows are on their way together.
+// A thread eight elements of four tokens, whose rows are on their way together.  Bound by its bytes: 16383
+// tokens of 4096 bf16 37 us (268 MB by algorithm; rows that come again come from the caches, 213 MB by
+// the counters); eight tokens 2.5 us, a launch.
 constexpr int kLookAhead = 4;
 
 template <int DT, int OT>
@@ -74,7 +76,9 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
 // start[v]: where id v's begin, start[vocab] the number of tokens that count.  A block takes `range` ids and goes through
 // all tokens twice (they come from L2: 64 KB for 8192): it counts its ids and the tokens of smaller
 // ids, then puts its tokens in their places.  A wave takes a run of tokens of its own and has
-// counters of its own, so places follow the tokens' order without any atomic's.
+// counters of its own, so places follow the tokens' order without any atomic's.  One launch whatever the
+// vocabulary: 10 us for 8191 tokens, 18 for 16384, latency (tokens, counters, sums and places wait for
+// each other).
 constexpr int kSortWaves = 16;
 constexpr int kMaxRange = 896;  // counters of 56 KB
 
@@ -297,6 +301,11 @@ __device__ __forceinline__ void add_piece(const EmbedGradArgs &a, const int32_t 
 // ids without tokens, most of the bytes, leave first, by whole lines and without a question of any
 // lane's own, a wave four rows; then a wave takes a quarter of the columns of all rows of some tokens,
 // the first tokens of four rows on their way together, as one token is the rule.
+// 50257 x 768 fp32 from 8191 tokens 29 us (167 MB, 5.8 TB/s), 131071 x 4096 from 16384 395 us (2.28 GB, 5.8
+// TB/s), bound by the stores.  With every row of up to 64 tokens added here, one after another, a call at
+// the first size took 77 us, and 352 where the frequent ids are neighbours: 42 and 46 this way.
+// Non-temporal stores: 65 us a call against 95 with plain ones, 457 against 481 at the larger size (at an
+// earlier step).
 template <int DT, int OT>
 __global__ __launch_bounds__(256) void k_embed_rows(const EmbedGradArgs a, const int32_t *start,
                                                     const int32_t *order, const int32_t *sorted, float *sums,

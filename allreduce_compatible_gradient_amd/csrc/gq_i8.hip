@@ -66,7 +66,8 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 
 // By rows: W waves a row, C groups of eight elements a lane held in registers, so that a row is read
-// once; C = 0: a row too long for that is read twice, the second time mostly from the caches.
+// once; C = 0: a row too long for that is read twice, the second time mostly from the caches.  Bound by
+// its bytes at size (8192 x 4096 bf16 17 us, 101 MB, 6.0 TB/s), by a launch below (333 x 768 5 us).
 template <int DT, bool STOCH, int W, int C>
 __global__ __launch_bounds__(256) void k_i8_rows(const I8QuantArgs a, int pitch) {
   constexpr int kThreads = W * 64, kRows = 256 / kThreads;
@@ -129,7 +130,8 @@ __global__ __launch_bounds__(256) void k_i8_rows(const I8QuantArgs a, int pitch)
 }
 
 // Largest magnitudes of rows (ROWS) and columns, as bits, over a part of the matrix each: a block goes
-// through 64 rows at a time of its share, 512 columns, a wave 16 rows, a lane eight columns.
+// through 64 rows at a time of its share, 512 columns, a wave 16 rows, a lane eight columns.  This read of
+// the matrix is what scales of whole columns cost: 4095 x 4096 bf16 16 us (33 MB), bound by latency.
 template <int DT, bool ROWS>
 __global__ __launch_bounds__(256) void k_i8_tops(const I8QuantArgs a, int rows_each) {
   __shared__ uint32_t cols_top[4][512];
@@ -184,7 +186,9 @@ __global__ __launch_bounds__(256) void k_i8_tops(const I8QuantArgs a, int rows_e
 // By columns, or both ways (ROWS), from the parts' largest magnitudes (row_parts of rows, then
 // col_parts of columns).  A block takes 128 rows x 128 columns; a lane has eight columns of a row,
 // whose codes by rows leave as they are and whose codes by columns cross LDS.  The draw of an element
-// is shared by its two codes.
+// is shared by its two codes.  4095 x 4096 bf16 stochastic both ways 29 us: some 30 vector instructions
+// an element, 7 of them the draw, beside 67 MB.  Parts of twice the length, half the maxima to read again
+// here, changed nothing (29 us, and 20 for the maxima instead of 16).
 template <int DT, bool STOCH, bool ROWS>
 __global__ __launch_bounds__(256) void k_i8_both(const I8QuantArgs a, int pitch, int pitch_t, int row_parts,
                                                  int col_parts) {
@@ -301,6 +305,13 @@ __device__ __forceinline__ void put_one(const I8MatmulArgs &a, int64_t m, int64_
 
 typedef i32x4 i32x4_e4 __attribute__((aligned(4)));
 
+// Tiled product for more than kFewRows rows.  8192 x 11008 x 4096 takes 330-370 us by the card, 2.0-2.2
+// POP/s (a loop of nothing but the instruction reaches 3.9 on random data, a library's product of this
+// size took 409 us): matrix cores busy 49%, at 1.9 GHz; 1376 tiles fill 5.4 of 6 rounds, and a tile's first
+// loads and stores, which nothing covers as one block fills a CU's LDS, took 11 us of its 52 when that
+// was fitted.  333 x 50257 x 768 takes 32-37 us, six steps a tile: first loads and stores are most of it.
+// What the epilogue needs is loaded before it: row scales read at each store cost a latency every pass
+// (8192 x 11008 x 4096 391 us, 371 without).
 template <class S>
 __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pitch, int tiles_m,
                                                     int tiles_n, int steps_each) {
@@ -425,7 +436,8 @@ __global__ __launch_bounds__(256) void k_i8_join(const I8MatmulArgs a, int split
 // block streams 16 rows of B straight to registers, its waves on interleaved steps of 128, four steps
 // of a wave on their way together.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l mod 16 at
 // l / 16.  fp32 / bf16 rows are quantised by the block into LDS while its first weights are on their
-// way.  The waves' sums meet in LDS.
+// way.  The waves' sums meet in LDS.  1 x 4096 by 11008 x 4096, 45 MB, takes 13.6 us, 3.3 TB/s: one
+// wait for all weights, which are on their way at once, after a launch.
 constexpr int kFewWaves = 8;
 constexpr int kFewAhead = 4;
 constexpr int64_t kFewRows = 16;
@@ -566,6 +578,12 @@ struct Plan {
   int splits, each;  // K splits and steps of each
 };
 
+// Tile and K splits of a product of more than kFewRows rows.  The tile is the one of the least expected
+// time, with n blocks on the fullest CU n (step K / 128 + rest) + wait K / 128 + once, fitted to 160 sizes
+// (M 17 to 8192, N 300 to 51200, K 128 to 11008), where the tile so chosen takes 1.03 times the best
+// one's time in the mean: 1000 x 4096 x 4096 23.0 us with 64 x 128, 27.0 with 128 x 128, 49.9 with 256 x
+// 256; 4095 x 11008 x 4096 209, 205 and 178.  Splits where tiles are few and K is long (64 x 4096 x 4096
+// 11.3 us, 13.5 without).
 Plan plan(int64_t M, int64_t N, int64_t K) {
   struct Tile {
     int bm, bn;

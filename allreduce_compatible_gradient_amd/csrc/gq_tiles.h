@@ -99,6 +99,14 @@ __device__ __forceinline__ void arrive_but() {
 // is multiplied, across the barrier too: it stands before a step's last group, when the step's own
 // operands are all in registers, so that its buffer is free for the step NB further on and the next
 // step's has arrived.
+//
+// Measured in 8 bits on 4096 x 4096 (a 256 x 256 tile a CU, two buffers): a step takes 1.43 us on random
+// codes and 1.14 on zeros; the matrix instructions alone 1.10 and 0.89; loading and LDS reads without them
+// 0.86, whatever the data: 64 KB a step and CU, some 19 TB/s from the L2s.  On random data the card's
+// power sets the clock (1.9 GHz).  Tried at 8192 x 11008 x 4096 on random codes: pieces of 64 bytes a row,
+// half a line, in four buffers (422 us against 394), and with them 256 x 128 tiles, two a CU, which load
+// half as much again (476 against 422); operands read after the barrier instead of across it made no
+// difference (390 and 390); conflicts in LDS, see below, cost 0.11 us a step.
 // Returns with every load done and every wave past its reads: the buffers are free.
 __device__ __forceinline__ int tile_key(int r) { return (r ^ (r >> 3 & 3)) & 7; }
 
