@@ -413,7 +413,7 @@ void look_up(const EmbedArgs &a, hipStream_t s) {
   const int64_t groups = (a.dim + 7) / 8;
   const unsigned bx = groups > 64 ? 256 : groups > 16 ? 64 : 16;
   const int64_t by = 256 / bx, gy = (a.tokens + by * kLookAhead - 1) / (by * kLookAhead);
-  const dim3 grid((unsigned)((groups + bx - 1) / bx), (unsigned)(gy < 32768 ? gy : 32768));
+  const dim3 grid((unsigned)((groups + bx - 1) / bx), (unsigned)(gy < 16384 ? gy : 16384));
   k_embed<DT, OT><<<grid, dim3(bx, (unsigned)by), 0, s>>>(a);
 }
 

@@ -408,17 +408,38 @@ __global__ __launch_bounds__(S::T) void k_i8_matmul(const I8MatmulArgs a, int pi
     float v[8];
     finished(lo, hi, v);
     const int64_t at = m * a.ldo + n;
-    const int there = (int)min((int64_t)8, a.N - n);
+    if (n + 8 > a.N) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (e >= there) break;
-      if (a.out_dtype == 0) {
-        float *o = static_cast<float *>(a.out) + at + e;
-        *o = a.accumulate ? *o + v[e] : v[e];
-      } else {
-        uint16_t *o = static_cast<uint16_t *>(a.out) + at + e;
-        *o = to_bf16(a.accumulate ? __uint_as_float((uint32_t)*o << 16) + v[e] : v[e]);
+      for (int e = 0; e < 8; ++e) {
+        if (n + e < a.N) {
+          if (a.out_dtype == 0) {
+            float *o = static_cast<float *>(a.out) + at + e;
+            *o = a.accumulate ? *o + v[e] : v[e];
+          } else {
+            uint16_t *o = static_cast<uint16_t *>(a.out) + at + e;
+            *o = to_bf16(a.accumulate ? __uint_as_float((uint32_t)*o << 16) + v[e] : v[e]);
+          }
+        }
       }
+    } else if (a.out_dtype == 0) {
+      f32x4_e4 *o = reinterpret_cast<f32x4_e4 *>(static_cast<float *>(a.out) + at);
+      f32x4 p = {v[0], v[1], v[2], v[3]}, q = {v[4], v[5], v[6], v[7]};
+      if (a.accumulate) {
+        p += o[0];
+        q += o[1];
+      }
+      o[0] = p;
+      o[1] = q;
+    } else {
+      uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+      if (a.accumulate) {
+        float x[8];
+        load_eight<1>(o, 0, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += x[e];
+      }
+      *reinterpret_cast<u32x4_e2 *>(o) =
+          u32x4{to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3]), to_bf16_pair(v[4], v[5]), to_bf16_pair(v[6], v[7])};
     }
   }, nothing);
 }
