@@ -454,13 +454,12 @@ __global__ __launch_bounds__(256) void k_i8_join(const I8MatmulArgs a, int split
 }
 
 // Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it, so each
-// block streams 16 rows of B straight to registers, its waves on interleaved steps of 128, four steps
-// of a wave on their way together.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l mod 16 at
+// block streams 16 rows of B straight to registers, its waves on interleaved steps of 128, AHEAD steps
+// of a wave on their way together: four, or as many as a short row has for each wave.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l mod 16 at
 // l / 16.  fp32 / bf16 rows are quantised by the block into LDS while its first weights are on their
 // way.  The waves' sums meet in LDS.  1 x 4096 by 11008 x 4096, 45 MB, takes 13.6 us, 3.3 TB/s: one
 // wait for all weights, which are on their way at once, after a launch.
 constexpr int kFewWaves = 8;
-constexpr int kFewAhead = 4;
 constexpr int64_t kFewRows = 16;
 // LDS of M packed rows: a row is padded by a chunk, so that 16 rows lie on different banks.
 inline size_t few_lds(int64_t M, int64_t pitch) { return (size_t)M * (size_t)(pitch + 16); }
@@ -472,7 +471,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int AT>
+template <int AT, int AHEAD>
 __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8MatmulArgs a, int pitch) {
   __shared__ i32x4 sums[kFewWaves][64];
   __shared__ uint32_t tops[kFewRows];
@@ -482,7 +481,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int8_t *b = a.b + min(n0 + r16, a.N - 1) * pitch + quarter * 16;
   const int steps = pitch / 128;
-  i32x4 w[kFewAhead][2];
+  i32x4 w[AHEAD][2];
   auto load = [&](int k, i32x4 (&to)[2]) {
     const i32x4 *p = reinterpret_cast<const i32x4 *>(b + (int64_t)k * 128);
     to[0] = __builtin_nontemporal_load(p);
@@ -490,7 +489,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
   };
   auto first_weights = [&]() {  // past the end: the last ones again, not multiplied
 #pragma unroll
-    for (int i = 0; i < kFewAhead; ++i) load(min(wave + i * kFewWaves, steps - 1), w[i]);
+    for (int i = 0; i < AHEAD; ++i) load(min(wave + i * kFewWaves, steps - 1), w[i]);
   };
   const uint8_t *rows = static_cast<const uint8_t *>(a.a);
   int row_bytes = pitch;
@@ -555,17 +554,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
       acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[p], u, acc, 0, 0, 0);
     }
   };
-  constexpr int kTurn = kFewAhead * kFewWaves;
+  constexpr int kTurn = AHEAD * kFewWaves;
   int first = wave;
   for (; first + kTurn < steps; first += kTurn) {  // a turn, with the next one's weights on their way
 #pragma unroll
-    for (int i = 0; i < kFewAhead; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       multiply(first + i * kFewWaves, w[i]);
       load(min(first + i * kFewWaves + kTurn, steps - 1), w[i]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < kFewAhead; ++i)
+  for (int i = 0; i < AHEAD; ++i)
     if (first + i * kFewWaves < steps) multiply(first + i * kFewWaves, w[i]);
   sums[wave][lane] = acc;
   __syncthreads();
@@ -717,12 +716,22 @@ hipError_t launch_i8_matmul(const I8MatmulArgs &a, hipStream_t s) {
   if (a.M <= kFewRows) {
     const unsigned blocks = (unsigned)((a.N + 15) / 16);
     const size_t lds = few_lds(a.M, pitch);
-    if (a.a_dtype == 0)
-      k_i8_matmul_few<0><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
-    else if (a.a_dtype == 1)
-      k_i8_matmul_few<1><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
+    const int64_t steps = (pitch / 128 + kFewWaves - 1) / kFewWaves;  // of a wave
+    auto few = [&](auto ahead) {
+      constexpr int kAhead = decltype(ahead)::value;
+      if (a.a_dtype == 0)
+        k_i8_matmul_few<0, kAhead><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
+      else if (a.a_dtype == 1)
+        k_i8_matmul_few<1, kAhead><<<blocks, kFewWaves * 64, lds, s>>>(a, pitch);
+      else
+        k_i8_matmul_few<3, kAhead><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+    };
+    if (steps == 1)
+      few(std::integral_constant<int, 1>{});
+    else if (steps == 2)
+      few(std::integral_constant<int, 2>{});
     else
-      k_i8_matmul_few<3><<<blocks, kFewWaves * 64, 0, s>>>(a, pitch);
+      few(std::integral_constant<int, 4>{});
     return hipGetLastError();
   }
   const Plan p = plan(a.M, a.N, a.K);
