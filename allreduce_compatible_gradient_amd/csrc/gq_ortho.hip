@@ -564,10 +564,12 @@ int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Expected time of a launch in us: a block of a side takes `step` a step of 64 halves and `rest` besides,
-// as many blocks one after another as the fullest CU has; `wait` a step and `once` come on top.  Fitted
-// to eleven sizes (n 256 to 6000, m 768 to 11008, batches to 48), where the sides so chosen are the best
-// ones or lose at most 22 us of 390.  One side instead of the chosen one: 4096 x 4096, Gram matrix and
-// square together 293 us of a step's time less with 192 than with 256 (253 tiles against 136 on 256 CUs).
+// as many blocks one after another as the fullest CU has; `wait` a step and `once` come on top.  The
+// symmetric products' are fitted to eleven sizes (n 256 to 6000, m 768 to 11008, batches to 48), where
+// the sides so chosen are the best ones but for four launches of 22, which lose 4 to 22 us; the update's
+// have the same loop and an epilogue of 12 bytes an element.  4096 x 4096, five Gram matrices and squares:
+// 293 us less with 192 than with 256 (253 tiles against 136 on 256 CUs), 12 x 768 x 2304, five updates:
+// 39 us less with 128 than with 256.
 struct Cost {
   int side;
   float step, rest, wait, once;
