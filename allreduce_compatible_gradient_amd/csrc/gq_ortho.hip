@@ -3,16 +3,23 @@
 // with products alone (Newton-Schulz).  Everything is done on the shorter side: n <= m, X n x m, the
 // transpose of a tall G.
 //
-// Numbers.  Operands of the products are halves, sums fp32, and X itself stays fp32.  Three choices
+// Numbers.  Operands of the products are halves, sums fp32, and X itself stays fp32.  Four choices
 // make that enough for a result in bf16.  Halves and not bf16: 3 bits more, and all operands have
 // known ranges, which powers of two bring into the halves' (X to at most 2^8 |x|, the others to
 // 2^10).  The diagonals of A and of B = b A + c A^2, large where the rest is small, stay apart in fp32:
 // with A = D + F,  A^2 = D^2 + D F + F D + F^2, and only F^2 is a product of rounded numbers; likewise
 // X <- (a + diag B) X + (B - diag B) X.  And a X, which carries a small singular value through the
-// steps that raise it up to a^steps-fold, is taken from the fp32 X.  The relative error (Frobenius)
-// before the last rounding is 1e-4 to 8e-4 for random, heavy-tailed and nearly low-rank matrices of
-// sides 64 to 1024, where halves alone have 2e-3 to 7e-3 and bf16 1e-2 to 1e-1; rounding to bf16
-// adds 1.7e-3.
+// steps that raise it up to a^steps-fold, is taken from the fp32 X.  Last, what X's halves h differ
+// from X by is noise in every direction, also in those that X does not have, where it grows a-fold a
+// step: (B - diag B) h + diag B X leaves -diag B (h - X) there, which for one direction in few rows came to
+// 4e-2 of the result.  Before the last two steps therefore either h carries all of X (two halves an
+// element: small matrices), or diag B multiplies h as well, so that the noise is multiplied by the whole
+// of B and stays in X's directions; in the last two the noise of a large diag B would count for more than
+// what still grows.
+// The relative error (Frobenius) before the last rounding, by a model of these roundings: 1e-4 to 1.3e-3 for random,
+// heavy-tailed and nearly low-rank matrices, where halves alone have 2e-3 to 7e-3 and bf16 1e-2 to
+// 1e-1; up to 3e-3 for one to eight directions, in few rows and columns too; 2e-3, at worst 1.2e-2, where
+// all elements are alike, as all roundings then have one sign.  Rounding to bf16 adds 1.7e-3.
 //
 // Work.  A and A^2 are symmetric: tiles on and above the diagonal are computed and stored both ways.
 // A step is three launches: the Gram matrix (of X's halves), its square, and the update, which
@@ -324,9 +331,10 @@ __global__ __launch_bounds__(256) void k_ortho_join(const Work w, int tiles, int
 }
 
 // X <- (a + diag B) X + (B - diag B) X; the last step's goes to `out` in bf16, by columns for a tall G.
+// `early`: diag B multiplies X's halves, as the product does, and a alone X itself.
 template <class S>
 __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const OrthoArgs o, float ca,
-                                                       int tiles_i, int tiles_j, int last) {
+                                                       int tiles_i, int tiles_j, int early, int last) {
   constexpr int WN = S::WN, R = S::R, C = S::C;
   GQ_TILE_LDS(S);
   const int lane = threadIdx.x & 63;
@@ -368,10 +376,11 @@ __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const Ortho
     if (there) {
       float *at = x + (int64_t)i * w.mp + j;
       const f32x4 x0 = xs[i32 & 1][p][0], x1 = xs[i32 & 1][p][1];
-      const float s = ca + ds[i32 & 1][p];
+      const float d = ds[i32 & 1][p], whole = early ? ca : ca + d, rounded = early ? d * (1.0f / kScaleX) : 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = s * (e < 4 ? x0[e & 3] : x1[e & 3]) + v[e] * (1.0f / (kScaleX * kScaleB));
+        const float was = e < 4 ? x0[e & 3] : x1[e & 3];
+        v[e] = whole * was + (v[e] * (1.0f / (kScaleX * kScaleB)) + rounded * (float)(_Float16)(was * kScaleX));
         if (j + e >= w.m) v[e] = 0.0f;
         h[e] = v[e] * kScaleX;
       }
@@ -422,8 +431,8 @@ __global__ __launch_bounds__(S::T) void k_ortho_update(const Work w, const Ortho
 // launches of some 3.7 us each whatever the size.  X stays in registers, four neighbouring columns of
 // a row a lane and tile (the products' own layout), its halves by rows and by columns in LDS, and so do
 // F and B; rows are padded by 16 bytes, so that 16 rows' reads fall on different banks.  A wave has
-// MP / 8 columns of X, and two of the sixteen tiles of A and of A^2.  64 x 147 takes 25 us, 67 the tiled
-// way.
+// MP / 8 columns of X, and two of the sixteen tiles of A and of A^2.  64 x 147 takes 28 us, 25 of them
+// without the second halves of three steps, and 67 the tiled way.
 template <int DT, int MP>
 __global__ __launch_bounds__(512) void k_ortho_small(const OrthoArgs a) {
   constexpr int kRow = MP * 2 + 16, kSquare = 64 * 2 + 16, kTiles = MP / 128;
@@ -485,6 +494,31 @@ __global__ __launch_bounds__(512) void k_ortho_small(const OrthoArgs a) {
   };
   const int ti = wave >> 1, tj = (wave & 1) * 2;
   for (int step = 0; step < a.steps; ++step) {
+    // X's columns; where they are two halves an element, the second ones in their place (a wave reads no
+    // other wave's)
+    const bool early = step < a.steps - 2;
+    i32x4 columns[kTiles][2];
+    auto take = [&]() {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) columns[t][k] = piece(xt, kSquare, wave * kTiles + t, k);
+    };
+    take();
+    if (early) {
+      wave_exchange();
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = x[t][r][e] * kScaleX;
+            *reinterpret_cast<_Float16 *>(xt + ((wave * kTiles + t) * 16 + four + e) * kSquare + (r * 16 + r16) * 2) =
+                (_Float16)(v - (float)(_Float16)v);
+          }
+      wave_exchange();
+    }
     float f[2][4];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -524,21 +558,28 @@ __global__ __launch_bounds__(512) void k_ortho_small(const OrthoArgs a) {
       *reinterpret_cast<u32x2 *>(bs + i * kSquare + j * 2) = u32x2{pack_half(b[0], b[1]), pack_half(b[2], b[3])};
     }
     __syncthreads();
+    auto multiply = [&](const i32x4 (&columns)[kTiles][2], f32x4 (&acc)[kTiles][4]) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      i32x4 columns[2];
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) columns[k] = piece(xt, kSquare, wave * kTiles + t, k);
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) acc[t][r] = F16Product::mul(columns[t][k], piece(bs, kSquare, r, k), acc[t][r]);
+    };
+    f32x4 acc[kTiles][4] = {};
+    multiply(columns, acc);
+    if (early) {
+      take();
+      multiply(columns, acc);
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) acc = F16Product::mul(columns[k], piece(bs, kSquare, r, k), acc);
         const float s = a.a + diag_b[r * 16 + r16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][r][e] = s * x[t][r][e] + acc[e] * (1.0f / (kScaleX * kScaleB));
+        for (int e = 0; e < 4; ++e) x[t][r][e] = s * x[t][r][e] + acc[t][r][e] * (1.0f / (kScaleX * kScaleB));
       }
-    }
     if (step == a.steps - 1) break;
     __syncthreads();  // every wave is past its reads of X's halves
     share();
@@ -668,9 +709,9 @@ void symmetric_of(const Side &p, const Work &w, const OrthoArgs &a, int64_t batc
 }
 
 template <class S>
-void update(const Work &w, const OrthoArgs &a, int64_t batch, int last, hipStream_t s) {
+void update(const Work &w, const OrthoArgs &a, int64_t batch, int early, int last, hipStream_t s) {
   const int ti = (w.n + S::BM - 1) / S::BM, tj = (w.m + S::BN - 1) / S::BN;
-  k_ortho_update<S><<<(unsigned)(ti * tj * batch), S::T, 0, s>>>(w, a, a.a, ti, tj, last);
+  k_ortho_update<S><<<(unsigned)(ti * tj * batch), S::T, 0, s>>>(w, a, a.a, ti, tj, early, last);
 }
 
 // What one block holds: 64 x 512 takes 159 KB of LDS.
@@ -733,13 +774,13 @@ void group(const OrthoArgs &a, hipStream_t s) {
       k_ortho_join<<<dim3((unsigned)(t * (t + 1) / 2 * (g.side / 64) * (g.side / 64)), 1, (unsigned)a.batch), 256, 0, s>>>(
           w, t, g.side, g.splits);
     symmetric_of<true>(square, w, a, a.batch, s);
-    const int last = step == a.steps - 1;
+    const int early = step < a.steps - 2, last = step == a.steps - 1;
     if (side == 256)
-      update<TileShape<2, 4, 8, 4, 2>>(w, a, a.batch, last, s);
+      update<TileShape<2, 4, 8, 4, 2>>(w, a, a.batch, early, last, s);
     else if (side == 128)
-      update<TileShape<2, 2, 4, 4, 2>>(w, a, a.batch, last, s);
+      update<TileShape<2, 2, 4, 4, 2>>(w, a, a.batch, early, last, s);
     else
-      update<TileShape<2, 2, 2, 2, 4>>(w, a, a.batch, last, s);
+      update<TileShape<2, 2, 2, 2, 4>>(w, a, a.batch, early, last, s);
     _Float16 *was = w.xt[0];
     w.xt[0] = w.xt[1];
     w.xt[1] = was;

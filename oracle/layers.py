@@ -113,3 +113,59 @@ def orthogonalise_rounded(g, steps=5, coefficients=QUINTIC):
         x = ((a + diag)[:, None] * x + half(q, 1024.0) @ h).astype(np.float32).astype(np.float64)
     x = bf16(x)
     return x.T if flip else x
+
+
+def orthogonalise_in_halves(g, steps=5, coefficients=QUINTIC):
+    """The same, with what keeps roundings out of directions that X does not have.  X's halves h differ
+    from X by noise in every direction, and the diagonal's part, which acts on rows apart, would leave
+    it there, to grow a-fold a step.  Before the last two steps therefore: sides to 64 x 512 multiply X as
+    two halves an element; else the diagonal multiplies h too, so that b A + c A^2 acts as a whole."""
+    a, b, c = coefficients
+    x = np.asarray(g, np.float64)
+    flip = x.shape[0] > x.shape[1]
+    x = x.T if flip else x
+    small = x.shape[0] <= 64 and x.shape[1] <= 512
+    norm = np.sqrt((x * x).sum())
+    x = (x / norm if norm > 0 else x).astype(np.float32).astype(np.float64)
+    for step in range(steps):
+        h = half(x, 256.0)
+        p = (h @ h.T).astype(np.float32).astype(np.float64)
+        d = np.diag(p).copy()
+        f = half(p - np.diag(d), 1024.0)
+        sq = f @ f
+        q = b * f + c * ((d[:, None] + d) * f + sq)
+        diag = b * d + c * (d * d + np.diag(sq))
+        np.fill_diagonal(q, 0.0)
+        taken = h + half(x - h, 256.0) if small and step < steps - 2 else h
+        own = h if not small and step < steps - 2 else x
+        x = (a * x + diag[:, None] * own + half(q, 1024.0) @ taken).astype(np.float32).astype(np.float64)
+    x = bf16(x)
+    return x.T if flip else x
+
+
+def low_rank(rows, cols, kind, seed):
+    """Matrices of few directions, as the gradients of few tokens or of few live channels are."""
+    rng = np.random.default_rng(seed)
+
+    def few(n, k):
+        v = np.zeros(n)
+        v[rng.choice(n, min(n, k), replace=False)] = rng.standard_normal(min(n, k))
+        return v
+
+    if kind.startswith("rank"):
+        r = int(kind[4:])
+        x = rng.standard_normal((rows, r)) @ rng.standard_normal((r, cols))
+    elif kind == "rows":        # one direction in two to four rows
+        x = np.outer(few(rows, rng.integers(2, 5)), rng.standard_normal(cols))
+    elif kind == "columns":
+        x = np.outer(rng.standard_normal(rows), few(cols, rng.integers(2, 5)))
+    elif kind == "both":
+        x = np.outer(few(rows, 4), few(cols, 4))
+    elif kind == "live":        # eight tokens, half of the channels of each alive
+        x = np.maximum(rng.standard_normal((rows, 8)), 0) @ np.maximum(rng.standard_normal((8, cols)), 0)
+    else:
+        raise ValueError(kind)
+    return (x * 1e-3).astype(np.float32)
+
+
+LOW_RANK = ("rank1", "rank2", "rank8", "rows", "columns", "both", "live")
