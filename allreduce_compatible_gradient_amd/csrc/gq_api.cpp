@@ -23,6 +23,7 @@
 #include "gq_layers.h"
 #include "gq_lm.h"
 #include "gq_lq.h"
+#include "gq_range.h"
 
 #define GQ_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -1340,36 +1341,6 @@ GQ_EXPORT gq_status gq_embedding_grad(gq_ctx *c, const void *dout, int32_t dtype
   return e == hipSuccess ? GQ_OK : hip_fail(c, e, "embedding_grad launch");
 }
 
-namespace {
-
-// Whether singular values that begin in [0, 1] stay in the range of the products' operands: the
-// largest |p(x)| = |a x + b x^3 + c x^5| on [0, top] lies at top or where a + 3 b x^2 + 5 c x^4 = 0,
-// the largest |b x + c x^2| on [0, top^2] at top^2 or at -b / 2c.
-bool ortho_stays(int32_t steps, double a, double b, double c) {
-  auto p = [&](double x) { return std::fabs(x * (a + x * x * (b + x * x * c))); };
-  auto q = [&](double x) { return std::fabs(x * (b + x * c)); };
-  double top = 1.0;
-  for (int32_t i = 0; i < steps; ++i) {
-    const double square = top * top;
-    double most = p(top), off = q(square);
-    if (c != 0.0) {
-      if (-b / (2.0 * c) > 0.0 && -b / (2.0 * c) < square) off = std::fmax(off, q(-b / (2.0 * c)));
-      const double d = 9.0 * b * b - 20.0 * a * c;
-      if (d >= 0.0)
-        for (double root : {(-3.0 * b + std::sqrt(d)) / (10.0 * c), (-3.0 * b - std::sqrt(d)) / (10.0 * c)})
-          if (root > 0.0 && root < square) most = std::fmax(most, p(std::sqrt(root)));
-    } else if (b != 0.0) {
-      const double root = -a / (3.0 * b);
-      if (root > 0.0 && root < square) most = std::fmax(most, p(std::sqrt(root)));
-    }
-    if (!(most <= 7.5) || !(off <= 60.0)) return false;
-    top = most;
-  }
-  return true;
-}
-
-}  // namespace
-
 GQ_EXPORT gq_status gq_orthogonalise(gq_ctx *ctx, const void *g, int32_t dtype, int64_t batch,
                                      int64_t rows, int64_t cols, int64_t ldg, int64_t stride_g,
                                      int32_t steps, double a, double b, double c, void *out,
@@ -1387,7 +1358,7 @@ GQ_EXPORT gq_status gq_orthogonalise(gq_ctx *ctx, const void *g, int32_t dtype, 
   if (batch > 1 && (stride_g > (int64_t)1 << 40 || stride_o > (int64_t)1 << 40))
     return fail(ctx, GQ_EINVAL, "a stride between matrices is above 2^40");
   if (steps < 1 || steps > 32) return fail(ctx, GQ_EINVAL, "steps = %d outside [1, 32]", steps);
-  if (!ortho_stays(steps, a, b, c))
+  if (!gq::ortho_stays(steps, a, b, c))
     return fail(ctx, GQ_EINVAL, "coefficients (%g, %g, %g) take singular values out of range in %d steps", a, b, c, steps);
   const bool none = rows == 0 || batch == 0;
   TRY(check_ptr(ctx, g, "g", none));
