@@ -477,8 +477,8 @@ gq_status gq_embedding_grad(gq_ctx *ctx, const void *dout, int32_t dtype, const 
  * and the result is rounded to bf16, the type of the output.  With the default coefficients the
  * products' roundings are some 1e-3 of the result's norm, up to 3e-3 where G has few directions, and at
  * worst 1.2e-2 where all its elements are alike; a bf16's are 1.7e-3.  A matrix of zeros gives zeros, one that holds an infinity or NaN NaN everywhere.  The coefficients have to
- * keep singular values that begin in [0, 1] below 7.5, and |b s^2 + c s^4| below 60 (GQ_EINVAL
- * otherwise).
+ * keep singular values that begin in [0, 1] below 7.5, and |b s^2 + c s^4| below 60, also where each
+ * step's roundings carry a value past its bounds (GQ_EINVAL otherwise).
  *   g    batch matrices of rows x cols of `dtype`, row stride ldg, stride_g elements apart
  *   out  the same in bf16, row stride ldo, stride_o elements apart;  1 <= steps <= 32
  * rows and cols at most 2^16, batch at most 2^16. */

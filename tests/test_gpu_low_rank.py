@@ -50,3 +50,14 @@ def test_one_direction_in_few_rows_of_a_large_matrix(side):
     got = gq().orthogonalise(torch.from_numpy(g).cuda())
     assert off(got[[5, side // 2, side - 1]], want) <= 2.0 ** -7
     assert got.double().norm().item() <= np.linalg.norm(want) * (1 + 2.0 ** -7)
+
+
+def test_coefficients_that_roundings_escape():
+    """Refused, where finite numbers would come out as NaN after some steps."""
+    say("coefficients refused")
+    g = gq()
+    x = torch.ones(64, 147, device="cuda")
+    for coefficients, steps in (((5.0, -20.0, 16.0), 5), ((3.0, -4.0, 0.0), 32), ((50.0, -49.0, 1e-18), 1)):
+        with pytest.raises(g.GQError):
+            g.orthogonalise(x, steps=steps, coefficients=coefficients)
+    assert torch.isfinite(g.orthogonalise(x, steps=32)).all()

@@ -68,3 +68,36 @@ def test_not_numbers(stays, bad):
         k = [1.0, 0.0, 0.0]
         k[i] = bad
         assert not stays(1, *k)
+
+
+# on [0, 1] these stay within [-1, 1], but a rounding past 1 is taken out of it, 9 or 25 times as far a step
+ESCAPE = [((5.0, -20.0, 16.0), 5), ((5.0, -20.0, 16.0), 10), ((3.0, -4.0, 0.0), 32), ((-3.0, 4.0, 0.0), 32),
+          ((-5.0, 20.0, -16.0), 32)]
+
+
+@pytest.mark.parametrize("coefficients,steps", ESCAPE)
+def test_roundings_that_escape(stays, coefficients, steps):
+    assert not stays(steps, *coefficients)
+
+
+def test_what_is_taken_stays_finite(stays):
+    """Coefficients near the rule's border, on matrices of one direction, of equal elements and of a broad
+    spectrum, with the products' roundings: the values that halves hold are never left."""
+    rng = np.random.default_rng(3)
+    matrices = [layers.low_rank(64, 147, "rank1", 1), layers.low_rank(70, 90, "rows", 2), np.full((40, 60), 0.37),
+                rng.standard_normal((30, 40)), np.eye(7, 9)]
+    taken = escaped = 0
+    while taken < 150:
+        # maps of [0, 1] to about itself: any a and c, b so that p(1) lies within [-1.2, 1.2]
+        a, c = rng.uniform(-6, 6), rng.uniform(-16, 16)
+        b, steps = rng.uniform(-1.2, 1.2) - a - c, int(rng.integers(4, 33))
+        if not stays(steps, a, b, c):
+            escaped += 1
+            continue
+        taken += 1
+        for g in matrices:
+            with np.errstate(all="ignore"):
+                got = layers.orthogonalise_in_halves(g, steps, (a, b, c))
+            assert np.all(np.isfinite(got)), (a, b, c, steps)
+            assert np.linalg.norm(got, 2) <= 7.5 * (1 + 2.0 ** -7), (a, b, c, steps)
+    assert escaped > 50
