@@ -61,15 +61,22 @@ def _once(ctx, incoming, grad):
     return _Once.apply(grad, incoming, *ctx.saved_tensors[:1])
 
 
+def _needed(ctx, recorded):
+    """Whether gradients of a layer's input and weight are to come: a parameter asks for one under
+    torch.no_grad too, where nothing is recorded (in forward itself gradients are always off)."""
+    return [recorded and n for n in ctx.needs_input_grad[:2]]
+
+
 class _Linear(torch.autograd.Function):
     """y = x W^T + b.  Activations and weights are rounded to nearest, along the products' inner
     axis: by rows for y, by columns for dX = dY W and dW = dY^T X.  dY is rounded stochastically,
     both ways in one read, so that the gradients are unbiased in it."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, seed, worker, context):
-        qx, qxt = gq.mx_quantize(_laid(x, strided=True), by_cols=ctx.needs_input_grad[1], ctx=context)
-        qw, qwt = gq.mx_quantize(_laid(weight, strided=True), by_cols=ctx.needs_input_grad[0], ctx=context)
+    def forward(ctx, x, weight, bias, seed, worker, context, recorded):
+        need_x, need_w = _needed(ctx, recorded)
+        qx, qxt = gq.mx_quantize(_laid(x, strided=True), by_cols=need_w, ctx=context)
+        qw, qwt = gq.mx_quantize(_laid(weight, strided=True), by_cols=need_x, ctx=context)
         ctx.operands = qxt, qwt
         ctx.draws, ctx.context = (seed, worker), context
         ctx.device, ctx.shape = weight.device, weight.shape
@@ -96,7 +103,7 @@ class _Linear(torch.autograd.Function):
                 dw = gq.mx_matmul(qt, qxt, out_dtype=_code(dtype_w), ctx=ctx.context)
         if need_b:
             db = dy.float().sum(0).to(dtype_b)
-        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None, None
+        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None, None, None
 
 
 def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -105,7 +112,7 @@ def mx_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
     ``seed`` has to differ from one step and layer to the next, and from the seeds of the gradients'
     exchange, which draws by the same hash; workers draw apart by ``worker``.  The backward pass takes
     at most 2^32 entries of the output, the draws' counter."""
-    return _Linear.apply(x, weight, bias, seed, worker, ctx)[0]
+    return _Linear.apply(x, weight, bias, seed, worker, ctx, torch.is_grad_enabled())[0]
 
 
 class _IntLinear(torch.autograd.Function):
@@ -115,9 +122,10 @@ class _IntLinear(torch.autograd.Function):
     gradients are unbiased in it."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, seed, worker, context):
-        qx, qxt = gq.int_quantize(_laid(x, strided=True), by_cols=ctx.needs_input_grad[1], ctx=context)
-        qw, qwt = gq.int_quantize(_laid(weight, strided=True), by_cols=ctx.needs_input_grad[0], ctx=context)
+    def forward(ctx, x, weight, bias, seed, worker, context, recorded):
+        need_x, need_w = _needed(ctx, recorded)
+        qx, qxt = gq.int_quantize(_laid(x, strided=True), by_cols=need_w, ctx=context)
+        qw, qwt = gq.int_quantize(_laid(weight, strided=True), by_cols=need_x, ctx=context)
         ctx.operands = qxt, qwt
         ctx.draws, ctx.context = (seed, worker), context
         ctx.device, ctx.shape = weight.device, weight.shape
@@ -144,14 +152,14 @@ class _IntLinear(torch.autograd.Function):
                 dw = gq.int_matmul(qt, qxt, out_dtype=_code(dtype_w), ctx=ctx.context)
         if need_b:
             db = dy.float().sum(0).to(dtype_b)
-        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None, None
+        return _once(ctx, dy, dx), _once(ctx, dy, dw), db, None, None, None, None
 
 
 def int_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                seed: int = 0, worker: int = 0, ctx: Optional[gq.Context] = None) -> torch.Tensor:
     """A linear layer (x: tokens x in, weight: out x in) in 8-bit integers.  ``seed`` and ``worker`` as
     for mx_linear; tokens, inputs and outputs are at most 2^17 where a gradient is wanted."""
-    return _IntLinear.apply(x, weight, bias, seed, worker, ctx)[0]
+    return _IntLinear.apply(x, weight, bias, seed, worker, ctx, torch.is_grad_enabled())[0]
 
 
 class _Embedding(torch.autograd.Function):
