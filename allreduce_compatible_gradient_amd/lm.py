@@ -124,6 +124,8 @@ class _IntLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, seed, worker, context, recorded):
         need_x, need_w = _needed(ctx, recorded)
+        if (need_x or need_w) and len(x) * len(weight) > 1 << 32:
+            raise ValueError("%d x %d outputs are more than the 2^32 draws of a backward pass" % (len(x), len(weight)))
         qx, qxt = gq.int_quantize(_laid(x, strided=True), by_cols=need_w, ctx=context)
         qw, qwt = gq.int_quantize(_laid(weight, strided=True), by_cols=need_x, ctx=context)
         ctx.operands = qxt, qwt
@@ -158,7 +160,8 @@ class _IntLinear(torch.autograd.Function):
 def int_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                seed: int = 0, worker: int = 0, ctx: Optional[gq.Context] = None) -> torch.Tensor:
     """A linear layer (x: tokens x in, weight: out x in) in 8-bit integers.  ``seed`` and ``worker`` as
-    for mx_linear; tokens, inputs and outputs are at most 2^17 where a gradient is wanted."""
+    for mx_linear; inputs are at most 2^17, and where a gradient is wanted tokens and outputs too, and
+    tokens times outputs at most 2^32, the draws' counter."""
     return _IntLinear.apply(x, weight, bias, seed, worker, ctx, torch.is_grad_enabled())[0]
 
 

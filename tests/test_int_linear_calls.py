@@ -45,3 +45,19 @@ def test_without_gradients_nothing_is_packed_by_columns(made, kind, off):
     made.clear()
     linear(leaf(6, 3, grad=True), w.detach())
     assert made == [((6, 3), True, False), ((5, 3), True, True)]
+
+
+def test_more_outputs_than_the_draws_of_a_backward_pass(made):
+    """The gradient's rounding has 2^32 draws: a layer of more outputs is refused before its forward
+    work, unless no gradient is wanted."""
+    x, w = leaf(98304, 1), leaf(50257, 1)
+    for a, c in ((leaf(98304, 1, grad=True), w), (x, leaf(50257, 1, grad=True))):
+        with pytest.raises(ValueError, match="2\\^32"):
+            lm.int_linear(a, c)
+    assert made == []
+    assert lm.int_linear(x, w).shape == (98304, 50257)
+    with torch.no_grad():
+        assert lm.int_linear(x, leaf(50257, 1, grad=True)).shape == (98304, 50257)
+    # a bias alone has a gradient without draws; 2^32 entries are within the limit
+    assert lm.int_linear(x, w, torch.zeros(50257, requires_grad=True)).requires_grad
+    assert lm.int_linear(leaf(65536, 1), leaf(65536, 1, grad=True)).shape == (65536, 65536)
