@@ -1212,7 +1212,7 @@ GQ_EXPORT gq_status gq_int_quantize(gq_ctx *c, const void *x, int32_t dtype, int
   TRY(check_ptr(c, scales, "scales", true));
   TRY(check_ptr(c, codes_t, "codes_t", true));
   TRY(check_ptr(c, scales_t, "scales_t", true));
-  if (rows == 0) return GQ_OK;
+  if (rows == 0 && !scales_t) return GQ_OK;
   gq::I8QuantArgs a;
   std::memset(&a, 0, sizeof a);
   a.x = x;
@@ -1226,7 +1226,7 @@ GQ_EXPORT gq_status gq_int_quantize(gq_ctx *c, const void *x, int32_t dtype, int
   a.stochastic = rounding == GQ_INT_STOCHASTIC;
   if (a.stochastic) a.key_mix = key_mix(worker_key(seed, worker));
   a.index_base = index_base;
-  const size_t bytes = gq::i8_quantize_scratch(rows, cols, codes_t != nullptr);
+  const size_t bytes = rows > 0 ? gq::i8_quantize_scratch(rows, cols, codes_t != nullptr) : 0;
   if (bytes) TRY(ensure_scratch(c, bytes, s));
   a.tops = static_cast<uint32_t *>(c->scratch);
   const hipError_t e = gq::launch_i8_quantize(a, dtype, s);

@@ -129,6 +129,12 @@ __global__ __launch_bounds__(256) void k_i8_rows(const I8QuantArgs a, int pitch)
   }
 }
 
+// The columns of a matrix without rows: scales of zero, and no codes.
+__global__ __launch_bounds__(256) void k_i8_no_rows(float *scales_t, int64_t cols) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < cols) scales_t[i] = 0.0f;
+}
+
 // Largest magnitudes of rows (ROWS) and columns, as bits, over a part of the matrix each: a block goes
 // through 64 rows at a time of its share, 512 columns, a wave 16 rows, a lane eight columns.  This read of
 // the matrix is what scales of whole columns cost: 4095 x 4096 bf16 16 us (33 MB), bound by latency.
@@ -696,7 +702,9 @@ size_t i8_quantize_scratch(int64_t rows, int64_t cols, bool by_cols) {
 }
 
 hipError_t launch_i8_quantize(const I8QuantArgs &a, int dtype, hipStream_t s) {
-  if (dtype == 0)
+  if (a.rows == 0)
+    k_i8_no_rows<<<(unsigned)((a.cols + 255) / 256), 256, 0, s>>>(a.scales_t, a.cols);
+  else if (dtype == 0)
     a.stochastic ? quantize_of<0, true>(a, s) : quantize_of<0, false>(a, s);
   else
     a.stochastic ? quantize_of<1, true>(a, s) : quantize_of<1, false>(a, s);
