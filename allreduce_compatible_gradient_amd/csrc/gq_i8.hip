@@ -17,8 +17,6 @@
 namespace gq {
 namespace {
 
-constexpr int kCus = 256;
-
 // ---------------------------------------------------------------- quantisation
 struct RowScale {
   float scale, inv;  // inv 0: all codes are zero
@@ -466,7 +464,6 @@ __global__ __launch_bounds__(256) void k_i8_join(const I8MatmulArgs a, int split
 // way.  The waves' sums meet in LDS.  1 x 4096 by 11008 x 4096, 45 MB, takes 13.6 us, 3.3 TB/s: one
 // wait for all weights, which are on their way at once, after a launch.
 constexpr int kFewWaves = 8;
-constexpr int64_t kFewRows = 16;
 // LDS of M packed rows: a row is padded by a chunk, so that 16 rows lie on different banks.
 inline size_t few_lds(int64_t M, int64_t pitch) { return (size_t)M * (size_t)(pitch + 16); }
 
@@ -599,50 +596,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_i8_matmul_few(const I8Matmul
   }
 }
 
-struct Plan {
-  int bm, bn;        // tile
-  int splits, each;  // K splits and steps of each
-};
-
-// Tile and K splits of a product of more than kFewRows rows.  The tile is the one of the least expected
-// time, with n blocks on the fullest CU n (step K / 128 + rest) + wait K / 128 + once, fitted to 160 sizes
-// (M 17 to 8192, N 300 to 51200, K 128 to 11008), where the tile so chosen takes 1.03 times the best
-// one's time in the mean: 1000 x 4096 x 4096 23.0 us with 64 x 128, 27.0 with 128 x 128, 49.9 with 256 x
-// 256; 4095 x 11008 x 4096 209, 205 and 178.  Splits where tiles are few and K is long (64 x 4096 x 4096
-// 11.3 us, 13.5 without).
-Plan plan(int64_t M, int64_t N, int64_t K) {
-  struct Tile {
-    int bm, bn;
-    float step, rest, wait, once;  // us of a step, of the rest of a tile, and once a step and a call
-  };
-  constexpr Tile kTiles[3] = {{256, 256, 1.28f, 11.2f, 0.0f, 0.0f}, {128, 128, 0.46f, 3.3f, 0.11f, 4.0f}, {64, 128, 0.27f, 1.3f, 0.16f, 4.7f}};
-  Plan p = {};
-  const int64_t steps = i8_pitch(K) / 128;
-  auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  float least = INFINITY;
-  for (const Tile &t : kTiles) {
-    const float each = (float)((tiles(t.bm, t.bn) + kCus - 1) / kCus);
-    const float us = each * ((float)steps * t.step + t.rest) + (float)steps * t.wait + t.once;
-    if (us < least) {
-      least = us;
-      p.bm = t.bm;
-      p.bn = t.bn;
-    }
-  }
-  int64_t splits = 1;
-  if (steps >= 24) {
-    splits = kCus / tiles(p.bm, p.bn);
-    if (splits > steps / 8) splits = steps / 8;
-    if (splits > 16) splits = 16;
-    if (splits < 1) splits = 1;
-  }
-  p.each = (int)((steps + splits - 1) / splits);
-  p.splits = (int)((steps + p.each - 1) / p.each);
-  return p;
-}
-
 template <class S>
-void tiles_of(const I8MatmulArgs &a, const Plan &p, hipStream_t s) {
+void tiles_of(const I8MatmulArgs &a, const I8Plan &p, hipStream_t s) {
   const int tm = (int)((a.M + S::BM - 1) / S::BM), tn = (int)((a.N + S::BN - 1) / S::BN);
   k_i8_matmul<S><<<dim3((unsigned)(tm * tn), p.splits), S::T, 0, s>>>(
       a, (int)i8_pitch(a.K), tm, tn, p.each);
@@ -715,7 +670,7 @@ bool i8_matmul_packs_rows(int64_t M, int64_t K) { return M <= kFewRows && M * i8
 
 size_t i8_matmul_scratch(int64_t M, int64_t N, int64_t K) {
   if (M <= kFewRows) return 0;
-  const Plan p = plan(M, N, K);
+  const I8Plan p = i8_plan(M, N, K);
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(int32_t) : 0;
 }
 
@@ -742,7 +697,7 @@ hipError_t launch_i8_matmul(const I8MatmulArgs &a, hipStream_t s) {
       few(std::integral_constant<int, 4>{});
     return hipGetLastError();
   }
-  const Plan p = plan(a.M, a.N, a.K);
+  const I8Plan p = i8_plan(a.M, a.N, a.K);
   if (p.bm == 256)
     tiles_of<TileShape<2, 4, 8, 4, 2>>(a, p, s);
   else if (p.bm == 128)

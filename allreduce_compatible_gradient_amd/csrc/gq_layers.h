@@ -6,14 +6,13 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gq_plans.h"
+
 namespace gq {
 
 // ---------------------------------------------------------------- 8-bit matrices
 constexpr int64_t kI8MaxRows = 1 << 23;
 constexpr int64_t kI8MaxCols = 1 << 17;  // 2^17 * 127 * 127 < 2^31: a row's sum of products fits
-
-// Bytes of a packed row: whole steps of the product.
-inline int64_t i8_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
 
 struct I8QuantArgs {
   const void *x;

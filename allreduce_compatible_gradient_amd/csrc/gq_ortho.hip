@@ -598,74 +598,9 @@ __global__ __launch_bounds__(512) void k_ortho_small(const OrthoArgs a) {
 }
 
 // ---------------------------------------------------------------- host
-constexpr int kCus = 256;
 constexpr size_t kGroupBytes = (size_t)2 << 30;
 
-int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
-// Expected time of a launch in us: a block of a side takes `step` a step of 64 halves and `rest` besides,
-// as many blocks one after another as the fullest CU has; `wait` a step and `once` come on top.  The
-// symmetric products' are fitted to eleven sizes (n 256 to 6000, m 768 to 11008, batches to 48), where
-// the sides so chosen are the best ones but for four launches of 22, which lose 4 to 22 us; the update's
-// have the same loop and an epilogue of 12 bytes an element.  4096 x 4096, five Gram matrices and squares:
-// 293 us less with 192 than with 256 (253 tiles against 136 on 256 CUs), 12 x 768 x 2304, five updates:
-// 39 us less with 128 than with 256.
-struct Cost {
-  int side;
-  float step, rest, wait, once;
-};
-constexpr Cost kSymmetric[] = {{256, 0.93f, 12.8f, 0.09f, 0.8f}, {192, 0.64f, 8.3f, 0.08f, 0.3f},
-                               {128, 0.31f, 4.5f, 0.29f, 3.5f}, {64, 0.28f, 0.0f, 0.0f, 3.4f}};
-constexpr Cost kUpdate[] = {{256, 0.93f, 40.0f, 0.09f, 0.8f}, {128, 0.31f, 9.0f, 0.29f, 3.5f}, {64, 0.13f, 2.4f, 0.0f, 7.8f}};
-
-float cost_of(const Cost &c, int64_t tiles, int64_t steps) {
-  return (float)((tiles + kCus - 1) / kCus) * ((float)steps * c.step + c.rest) + (float)steps * c.wait + c.once;
-}
-
-struct Side {
-  int side, splits, each;
-  bool alone;  // a CU has one block at most
-};
-
-// Tiles of a symmetric product with sums of `steps`; the Gram matrix, whose sums may be long, in splits
-// where its tiles leave CUs idle and a launch that joins them costs less.
-Side symmetric_plan(int64_t batch, int64_t n, int64_t steps, bool may_split) {
-  Side best = {64, 1, (int)steps, false};
-  float least = INFINITY;
-  for (const Cost &c : kSymmetric) {
-    const int64_t t = (n + c.side - 1) / c.side, count = batch * t * (t + 1) / 2;
-    int64_t most = kCus / count;
-    if (most > steps / 4) most = steps / 4;
-    if (most > 16) most = 16;
-    if (most < 1 || !may_split) most = 1;
-    for (int64_t splits : {(int64_t)1, most}) {
-      const int64_t each = (steps + splits - 1) / splits;
-      // partial sums are written and read, at some 4 TB/s
-      const float join = splits > 1 ? 4.0f + (float)(count * splits) * (float)(c.side * c.side) * 2e-6f : 0.0f;
-      const float us = cost_of(c, count * splits, each) + join;
-      if (us >= least) continue;
-      least = us;
-      best = Side{c.side, (int)((steps + each - 1) / each), (int)each, count * splits <= kCus};
-    }
-  }
-  return best;
-}
-
-Side gram_plan(int64_t batch, int64_t n, int64_t m) { return symmetric_plan(batch, n, up64(m) / 64, true); }
-
-int update_side(int64_t batch, int64_t n, int64_t m) {
-  int side = 64;
-  float least = INFINITY;
-  for (const Cost &c : kUpdate) {
-    const float us = cost_of(c, batch * ((n + c.side - 1) / c.side) * ((m + c.side - 1) / c.side), up64(n) / 64);
-    if (us < least) {
-      least = us;
-      side = c.side;
-    }
-  }
-  return side;
-}
 
 struct Sizes {
   size_t x, xh, xt, f, diag, norms, partial;
@@ -712,11 +647,6 @@ template <class S>
 void update(const Work &w, const OrthoArgs &a, int64_t batch, int early, int last, hipStream_t s) {
   const int ti = (w.n + S::BM - 1) / S::BM, tj = (w.m + S::BN - 1) / S::BN;
   k_ortho_update<S><<<(unsigned)(ti * tj * batch), S::T, 0, s>>>(w, a, a.a, ti, tj, early, last);
-}
-
-// What one block holds: 64 x 512 takes 159 KB of LDS.
-bool ortho_is_small(int64_t rows, int64_t cols) {
-  return (rows < cols ? rows : cols) <= 64 && (rows < cols ? cols : rows) <= 512;
 }
 
 template <int DT>
