@@ -304,8 +304,8 @@ __device__ __forceinline__ void add_piece(const EmbedGradArgs &a, const int32_t 
 // 50257 x 768 fp32 from 8191 tokens 29 us (167 MB, 5.8 TB/s), 131071 x 4096 from 16384 395 us (2.28 GB, 5.8
 // TB/s), bound by the stores.  With every row of up to 64 tokens added here, one after another, a call at
 // the first size took 77 us, and 352 where the frequent ids are neighbours: 42 and 46 this way.
-// Non-temporal stores: 65 us a call against 95 with plain ones, 457 against 481 at the larger size (at an
-// earlier step).
+// Non-temporal stores: a call at the larger size takes 404 us against 456 with plain ones; at the first, whose
+// table the last cache holds when it is written again and again, 43 against 37.
 template <int DT, int OT>
 __global__ __launch_bounds__(256) void k_embed_rows(const EmbedGradArgs a, const int32_t *start,
                                                     const int32_t *order, const int32_t *sorted, float *sums,

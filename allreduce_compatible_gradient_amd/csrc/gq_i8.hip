@@ -459,10 +459,13 @@ __global__ __launch_bounds__(256) void k_i8_join(const I8MatmulArgs a, int split
 
 // Few rows of A (M <= 16, one decoded token to a small batch): the weights' bytes bound it, so each
 // block streams 16 rows of B straight to registers, its waves on interleaved steps of 128, AHEAD steps
-// of a wave on their way together: four, or as many as a short row has for each wave.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l mod 16 at
-// l / 16.  fp32 / bf16 rows are quantised by the block into LDS while its first weights are on their
-// way.  The waves' sums meet in LDS.  1 x 4096 by 11008 x 4096, 45 MB, takes 13.6 us, 3.3 TB/s: one
-// wait for all weights, which are on their way at once, after a launch.
+// of a wave on their way together: four, or as many as a short row has for each wave.
+// v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l mod 16 at l / 16.  fp32 / bf16 rows are
+// quantised by the block into LDS while its first weights are on their way.  Packed rows are read from
+// memory as they are multiplied, behind the weights, so that a step waits for all loads.  The waves' sums
+// meet in LDS.  1 x 4096 by 11008 x 4096, 45 MB, takes 13.5 us, 3.3 TB/s: one wait for all weights, which are
+// on their way at once, after a launch; 16 rows that a launch of their own packs 20 (15 from 9 packed
+// ones, 17 from 16); 1 x 11008 by 4096 x 11008 13.6, and 16.6 from a packed row.
 constexpr int kFewWaves = 8;
 // LDS of M packed rows: a row is padded by a chunk, so that 16 rows lie on different banks.
 inline size_t few_lds(int64_t M, int64_t pitch) { return (size_t)M * (size_t)(pitch + 16); }

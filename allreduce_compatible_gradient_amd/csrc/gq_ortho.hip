@@ -24,11 +24,13 @@
 // Work.  A and A^2 are symmetric: tiles on and above the diagonal are computed and stored both ways.
 // A step is three launches: the Gram matrix (of X's halves), its square, and the update, which
 // writes X in fp32, its halves by rows for the next Gram matrix, and by columns for the next update.
-// 4096 x 4096 takes 1.41 ms (five steps of 72, 74 and 139 us, 0.97 PFLOP/s of what the definition
-// cannot do without), 11008 x 4096 3.5 ms (197, 72 and 401; 0.89), twelve of 768 x 2304 0.65 ms.  The
+// By the card 4096 x 4096 takes 1.39 to 1.41 ms (0.98 PFLOP/s of what the definition cannot do without),
+// 11008 x 4096 3.43 to 3.51 (0.90), twelve of 768 x 2304 0.64 to 0.67.  A profiler, whose times add up to a
+// tenth more, has 155 us for a step's Gram matrix and square and 143 for its update in the first, 278 and 401
+// in the second, 50 and 78 in the third, and 53, 115 and 67 for what comes before the steps.  The
 // products reach 1.0 to 1.2 PFLOP/s (a library's product of 4096 x 4096 halves took 105 us, 1.3; a loop
 // of nothing but the instruction 1.8 on random data); an update's epilogue reads and writes 12 bytes
-// an element of X, 31 us of its 139 at 4096 x 4096 at the card's best rate, when all tiles end
+// an element of X, 31 us of its 143 at 4096 x 4096 at the card's best rate, when all tiles end
 // together, and is most of it where n is small.
 #include <math.h>
 

@@ -70,10 +70,12 @@ inline bool ortho_is_small(int64_t rows, int64_t cols) {
 // Expected time of a launch in us: a block of a side takes `step` a step of 64 halves and `rest` besides,
 // as many blocks one after another as the fullest CU has; `wait` a step and `once` come on top.  The
 // symmetric products' are fitted to eleven sizes (n 256 to 6000, m 768 to 11008, batches to 48), where
-// the sides so chosen are the best ones but for four launches of 22, which lose 4 to 22 us; the update's
-// have the same loop and an epilogue of 12 bytes an element.  4096 x 4096, five Gram matrices and squares:
-// 293 us less with 192 than with 256 (253 tiles against 136 on 256 CUs), 12 x 768 x 2304, five updates:
-// 39 us less with 128 than with 256.
+// the sides so chosen are the best ones but for four launches of 22, which lose 4 to 22 us.  4096 x 4096,
+// five Gram matrices and squares: 293 us less with 192 than with 256 (253 tiles against 136 on 256 CUs).
+// The update's have the same loop and an epilogue of 12 bytes an element; with each side at fourteen sizes
+// (n 300 to 4096, m to 11008, batches to 48) the one chosen is within 3% of the best call but twice:
+// 3000 x 3000 takes 955 us with 64 (chosen), 945 with 128 and 895 with 256; 48 of 256 x 1024 305, 318
+// (chosen) and 289; 12 of 768 x 2304 743, 677 (chosen) and 710; 4096 x 11008 5187, 3830 and 3511 (chosen).
 struct Cost {
   int side;
   float step, rest, wait, once;

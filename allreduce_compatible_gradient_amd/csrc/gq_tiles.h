@@ -89,11 +89,13 @@ __device__ __forceinline__ void arrive_but() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// Where row r's 16-byte chunks of a step are kept: chunk c at c XOR tile_key(r).
+__device__ __forceinline__ int tile_key(int r) { return (r ^ (r >> 3 & 3)) & 7; }
+
 // Steps step0 .. step0 + count - 1 (count at least 1) of the tile's sums.  Operands go from memory to
 // LDS without registers, into NB buffers in turn, each a static array of its own: LDS reads wait for
-// their own buffer's loads only.  Row r's 16-byte chunk c is kept at chunk c XOR key(r), key(r) =
-// (r XOR r / 8 mod 4) mod 8: 16 rows' reads of one chunk column fall on 16 different places of 256
-// bytes.
+// their own buffer's loads only.  With tile_key's order of chunks 16 rows' reads of one chunk column
+// fall on 16 different places of 256 bytes.
 //
 // A step is four groups of products, and a group's operands are read from LDS while the group before
 // is multiplied, across the barrier too: it stands before a step's last group, when the step's own
@@ -108,8 +110,6 @@ __device__ __forceinline__ void arrive_but() {
 // half as much again (476 against 422); operands read after the barrier instead of across it made no
 // difference (390 and 390); conflicts in LDS, see below, cost 0.11 us a step.
 // Returns with every load done and every wave past its reads: the buffers are free.
-__device__ __forceinline__ int tile_key(int r) { return (r ^ (r >> 3 & 3)) & 7; }
-
 template <class P, class S>
 __device__ __forceinline__ void tile_product(uint8_t *lds0, uint8_t *lds1, uint8_t *lds2,
                                              uint8_t *lds3, TileRows a, TileRows b, int pitch,

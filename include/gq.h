@@ -439,7 +439,8 @@ gq_status gq_int_quantize(gq_ctx *ctx, const void *x, int32_t dtype, int64_t row
 
 /* out = A B^T (+ bias) (+ out), A M x K with a scale for each row (token), B N x K with a scale for
  * each row (output channel): out_ij = (sum_k a_ik b_jk) sa_i sb_j, the sum exact in 32-bit integers
- * (K <= 2^17), the rest in fp32.
+ * (K <= 2^17), the rest in fp32 from the left (a row of A above some 1e29 may overflow in sum * sa_i
+ * where a small sb_j would bring it back).
  *   a       packed codes (a_dtype GQ_INT8, with a_scales; lda unused), or fp32 / bf16 rows of stride
  *           lda (a_scales NULL) that are quantised to nearest as gq_int_quantize would
  *   b       packed codes and scales
@@ -476,9 +477,10 @@ gq_status gq_embedding_grad(gq_ctx *ctx, const void *dout, int32_t dtype, const 
  * Operands of the products are rounded to 11 bits, their diagonals apart and X itself held in fp32,
  * and the result is rounded to bf16, the type of the output.  With the default coefficients the
  * products' roundings are some 1e-3 of the result's norm, up to 3e-3 where G has few directions, and at
- * worst 1.2e-2 where all its elements are alike; a bf16's are 1.7e-3.  A matrix of zeros gives zeros, one that holds an infinity or NaN NaN everywhere.  The coefficients have to
- * keep singular values that begin in [0, 1] below 7.5, and |b s^2 + c s^4| below 60, also where each
- * step's roundings carry a value past its bounds (GQ_EINVAL otherwise).
+ * worst 1.2e-2 where all its elements are alike; a bf16's are 1.7e-3.  A matrix of zeros gives
+ * zeros, one that holds an infinity or NaN NaN everywhere.  The coefficients have to keep singular
+ * values that begin in [0, 1] below 7.5, and |b s^2 + c s^4| below 60, also where each step's
+ * roundings carry a value past its bounds (GQ_EINVAL otherwise).
  *   g    batch matrices of rows x cols of `dtype`, row stride ldg, stride_g elements apart
  *   out  the same in bf16, row stride ldo, stride_o elements apart;  1 <= steps <= 32
  * rows and cols at most 2^16, batch at most 2^16. */
