@@ -12,7 +12,7 @@
 // steps that raise it up to a^steps-fold, is taken from the fp32 X.  Last, what X's halves h differ
 // from X by is noise in every direction, also in those that X does not have, where it grows a-fold a
 // step: (B - diag B) h + diag B X leaves -diag B (h - X) there, which for one direction in few rows came to
-// 4e-2 of the result.  Before the last two steps therefore either h carries all of X (two halves an
+// 4e-2 of the result in five steps, and to all of it in eight.  Before the last two steps therefore either h carries all of X (two halves an
 // element: small matrices), or diag B multiplies h as well, so that the noise is multiplied by the whole
 // of B and stays in X's directions; in the last two the noise of a large diag B would count for more than
 // what still grows.

@@ -21,6 +21,13 @@ def test_few_directions(rows, cols, kind):
         assert off(layers.orthogonalise_in_halves(g), layers.orthogonalise(g)) <= BOUND, seed
 
 
+@pytest.mark.parametrize("kind", layers.LOW_RANK)
+@pytest.mark.parametrize("rows,cols", [(64, 147), (257, 300)])
+def test_eight_steps(rows, cols, kind):
+    g = layers.low_rank(rows, cols, kind, 1)
+    assert off(layers.orthogonalise_in_halves(g, 8), layers.orthogonalise(g, 8)) <= BOUND
+
+
 def test_what_the_diagonal_apart_would_leave():
     """One direction in two rows of 300: with the diagonal on X itself and the rest on its halves, the
     roundings that only one of them has grow 3.4-fold a step, to more than 1%."""
