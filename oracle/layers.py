@@ -93,8 +93,9 @@ def bf16(x):
 
 
 def orthogonalise_rounded(g, steps=5, coefficients=QUINTIC):
-    """The same with the library's roundings: products of halves, diagonals apart, X in fp32, the
-    result in bf16.  How far it is from orthogonalise() is how far those roundings alone take it."""
+    """The same with products of halves, diagonals apart in every step, X in fp32, the result in bf16.  How
+    far it is from orthogonalise() is how far those roundings alone take it.  (The library's differ in
+    the steps before the last two, see orthogonalise_in_halves: on a broad spectrum by a few percent.)"""
     a, b, c = coefficients
     x = np.asarray(g, np.float64)
     flip = x.shape[0] > x.shape[1]
